@@ -20,7 +20,7 @@ SAFE_LIB_PATH = os.path.join(_HERE, "libapmoe_safe.so")
 
 OK, INVALID_ARG, UNSUPPORTED, NOT_RESIDENT, HIP_ERROR, OUT_OF_MEMORY = range(6)
 GATE_UP, DOWN = 0, 1
-F16, F32 = 0, 1
+F16, F32, BF16 = 0, 1, 2
 MIN_BITS, MAX_BITS, PLANES = 3, 8, 8
 
 EXPORTED = [
@@ -30,7 +30,8 @@ EXPORTED = [
     "apmoe_table_commit", "apmoe_lut_build", "apmoe_tiled_plane_words", "apmoe_tile_planes", "apmoe_pack_planes", "apmoe_route", "apmoe_route_workspace", "apmoe_route_stats", "apmoe_gemm",
     "apmoe_gemm_act", "apmoe_act",
     "apmoe_combine", "apmoe_moe_workspace", "apmoe_moe_forward", "apmoe_page_out", "apmoe_page_in",
-    "apmoe_moe_forward_noalloc",
+    "apmoe_moe_forward_noalloc", "apmoe_norm", "apmoe_gemm_fp8", "apmoe_gemm_act_fp8", "apmoe_moe_workspace_fp8",
+    "apmoe_moe_forward_fp8",
 ]
 
 
@@ -46,6 +47,14 @@ class BlockDesc(ctypes.Structure):
         ("resident_mask", ctypes.c_uint32),
         ("plane", ctypes.c_void_p * PLANES),
         ("lut", ctypes.c_void_p * (MAX_BITS + 1)),
+    ]
+
+
+class Fp8Desc(ctypes.Structure):
+    _fields_ = [
+        ("E", ctypes.c_int32), ("H", ctypes.c_int32), ("F", ctypes.c_int32),
+        ("gate_up", ctypes.c_void_p), ("gate_up_scale", ctypes.c_void_p),
+        ("down", ctypes.c_void_p), ("down_scale", ctypes.c_void_p),
     ]
 
 
@@ -85,6 +94,7 @@ def lib() -> ctypes.CDLL:
 
 def _declare(L):
     P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    F32_ = ctypes.c_float
     S = ctypes.c_int32
     sig = {
         "apmoe_status_string": (ctypes.c_char_p, [S]),
@@ -116,6 +126,11 @@ def _declare(L):
         "apmoe_moe_workspace": (S, [P, I32, I32, I32, I32, ctypes.POINTER(SZ)]),
         "apmoe_moe_forward": (S, [P, P, I32, P, P, P, I32, I32, I32, I32, P, SZ, P, P]),
         "apmoe_moe_forward_noalloc": (S, [P, P, I32, P, P, P, I32, I32, I32, I32, P, P]),
+        "apmoe_norm": (S, [P, P, I32, P, P, I32, P, F32_, I32, I32, P, P, P, P]),
+        "apmoe_gemm_fp8": (S, [P, P, P, P, P, I32, I32, I32, I32, P, P, I32, I32, P, I32, P]),
+        "apmoe_gemm_act_fp8": (S, [P, P, P, P, P, I32, I32, I32, I32, P, P, I32, I32, P, P, P]),
+        "apmoe_moe_workspace_fp8": (S, [P, ctypes.POINTER(Fp8Desc), I32, I32, I32, ctypes.POINTER(SZ)]),
+        "apmoe_moe_forward_fp8": (S, [P, ctypes.POINTER(Fp8Desc), P, P, P, P, P, I32, I32, I32, I32, P, SZ, P, P]),
         "apmoe_page_out": (S, [P, P, I32, I32, I32, I32, ctypes.POINTER(P), P, P, P]),
         "apmoe_page_in": (S, [P, P, I32, I32, I32, I32, ctypes.POINTER(P), ctypes.POINTER(P), P, P, P]),
     }
@@ -342,6 +357,152 @@ def moe_forward_noalloc(ctx: Context, table: Table, layer: int, x, w_router, bia
     _check(ctx.L.apmoe_moe_forward_noalloc(ctx.handle, table.handle, layer, ptr(x), ptr(w_router), ptr(bias), T,
                                            topk, n_shared, int(renormalize), ptr(out), stream_handle(stream)),
            "apmoe_moe_forward_noalloc", ctx.L)
+
+
+# --------------------------------------------------------------------------- 8-bit path
+
+_float_ids, _e4m3_types, _f32, _i32 = None, None, None, None
+
+
+def _load_types() -> None:
+    """torch is imported with the first call that takes tensors, not with the package."""
+    global _float_ids, _e4m3_types, _f32, _i32
+    if _float_ids is None:
+        import torch
+        _e4m3_types, _f32, _i32 = (torch.float8_e4m3fn, torch.uint8), (torch.float32,), (torch.int32,)
+        _float_ids = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
+
+
+def _arg(ctx: Context, t, name: str, n: int, types) -> int | None:
+    """Pointer of an argument of n elements.  A tensor must have one of the types, be
+    contiguous, lie on the context's device and hold at least n elements; None and raw
+    pointers are passed on."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype not in types or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{name}: need {n} contiguous elements of {' / '.join(map(str, types))}, got "
+                         f"{tuple(t.shape)} of {t.dtype}{'' if t.is_contiguous() else ', not contiguous'}")
+    if t.get_device() != ctx.device:
+        raise ValueError(f"{name} is on {t.device}, the context on cuda:{ctx.device}")
+    return t.data_ptr()
+
+
+def _stream_of(ctx: Context, stream) -> int | None:
+    import torch
+    s = torch.cuda.current_stream(ctx.device) if stream is None else stream
+    return s.cuda_stream or None
+
+
+def _types(t, name: str):
+    """(number of the type in the C ABI, the type as a tuple) of a floating tensor."""
+    _load_types()
+    d = _float_ids.get(t.dtype)
+    if d is None:
+        raise ValueError(f"{name}: {t.dtype} is not float16, bfloat16 or float32")
+    return d, (t.dtype,)
+
+
+def norm(ctx: Context, x, residual, residual_out, gamma, eps: float, T: int, H: int, y, y8=None, y_scale=None,
+         stream=None) -> None:
+    """Root-mean-square norm of x + residual (residual None: of x).  residual_out gets
+    the sum (it may be residual), y the norm in x's type and / or y8, y_scale the norm
+    as e4m3 with a scale for each 128 columns.  Types are the tensors' own: float16,
+    bfloat16 or float32."""
+    xt, xtypes = _types(x, "x")
+    rt, rtypes = (0, xtypes) if residual is None else _types(residual, "residual")
+    n = T * H
+    _check(ctx.L.apmoe_norm(ctx.handle, _arg(ctx, x, "x", n, xtypes), xt, _arg(ctx, residual, "residual", n, rtypes),
+                            _arg(ctx, residual_out, "residual_out", n, rtypes), rt,
+                            _arg(ctx, gamma, "gamma", H, xtypes), eps, T, H, _arg(ctx, y, "y", n, xtypes),
+                            _arg(ctx, y8, "y8", n, _e4m3_types), _arg(ctx, y_scale, "y_scale", T * -(-H // 128), _f32),
+                            _stream_of(ctx, stream)), "apmoe_norm", ctx.L)
+
+
+def _fp8_inputs(ctx, x8, x_scale, w8, w_scale, E, rows, n_scale, K, perm, offsets, T, topk, gather):
+    _load_types()
+    kb, R = -(-K // 128), T * topk
+    n = T if gather else R
+    f32, i32 = _f32, _i32
+    return (_arg(ctx, x8, "x8", n * K, _e4m3_types), _arg(ctx, x_scale, "x_scale", n * kb, f32),
+            _arg(ctx, w8, "w8", E * rows * K, _e4m3_types), _arg(ctx, w_scale, "w_scale", E * n_scale * kb, f32),
+            _arg(ctx, perm, "perm", R, i32), _arg(ctx, offsets, "offsets", E + 1, i32))
+
+
+def gemm_fp8(ctx: Context, x8, x_scale, w8, w_scale, E: int, N: int, K: int, gather: bool, perm, offsets, T: int,
+             topk: int, out, stream=None) -> None:
+    """The experts' product on e4m3 operands with fp32 scales (x_scale by 128 columns,
+    w_scale by 128 x 128 block); out's type is its tensor's.  Dense: E = topk = 1,
+    gather False, perm and offsets None."""
+    xp, xsp, wp, wsp, pp, op = _fp8_inputs(ctx, x8, x_scale, w8, w_scale, E, N, -(-N // 128), K, perm, offsets, T,
+                                           topk, gather)
+    dt, types = _types(out, "out")
+    _check(ctx.L.apmoe_gemm_fp8(ctx.handle, xp, xsp, wp, wsp, E, N, K, int(gather), pp, op, T, topk,
+                                _arg(ctx, out, "out", T * topk * N, types), dt, _stream_of(ctx, stream)),
+           "apmoe_gemm_fp8", ctx.L)
+
+
+def gemm_act_fp8(ctx: Context, x8, x_scale, w8, w_scale, E: int, F: int, K: int, gather: bool, perm, offsets, T: int,
+                 topk: int, a8, a_scale, stream=None) -> None:
+    """The gate_up product on e4m3 operands with SiLU(gate) * up and the 8-bit output in
+    its epilogue: a8 e4m3 [T*topk][F], a_scale fp32 [T*topk][ceil(F/128)]."""
+    fb = -(-F // 128)
+    xp, xsp, wp, wsp, pp, op = _fp8_inputs(ctx, x8, x_scale, w8, w_scale, E, 2 * F, 2 * fb, K, perm, offsets, T, topk,
+                                           gather)
+    _check(ctx.L.apmoe_gemm_act_fp8(ctx.handle, xp, xsp, wp, wsp, E, F, K, int(gather), pp, op, T, topk,
+                                    _arg(ctx, a8, "a8", T * topk * F, _e4m3_types),
+                                    _arg(ctx, a_scale, "a_scale", T * topk * fb, _f32),
+                                    _stream_of(ctx, stream)), "apmoe_gemm_act_fp8", ctx.L)
+
+
+class Fp8Experts:
+    """The e4m3 experts of one layer: gate_up [E][2F][H] with scales
+    [E][2][ceil(F/128)][ceil(H/128)], down [E][H][F] with scales
+    [E][ceil(H/128)][ceil(F/128)] (any shape with that many elements; E, H and F are
+    read from gate_up and down).  Holds the tensors, so they live as long as it does."""
+
+    def __init__(self, gate_up, gate_up_scale, down, down_scale):
+        _load_types()
+        E, H, F = down.shape
+        if tuple(gate_up.shape) != (E, 2 * F, H):
+            raise ValueError(f"gate_up {tuple(gate_up.shape)} and down {tuple(down.shape)} are not [E][2F][H], [E][H][F]")
+        self.E, self.H, self.F = E, H, F
+        self.device = down.get_device()
+        hb, fb = -(-H // 128), -(-F // 128)
+        self.tensors = (gate_up, gate_up_scale, down, down_scale)
+        d = Fp8Desc()
+        d.E, d.H, d.F = E, H, F
+        d.gate_up = _arg(self, gate_up, "gate_up", E * 2 * F * H, _e4m3_types)
+        d.gate_up_scale = _arg(self, gate_up_scale, "gate_up_scale", E * 2 * fb * hb, _f32)
+        d.down = _arg(self, down, "down", E * H * F, _e4m3_types)
+        d.down_scale = _arg(self, down_scale, "down_scale", E * hb * fb, _f32)
+        self.desc = d
+        self.ref = ctypes.byref(d)
+
+
+def moe_workspace_fp8(ctx: Context, experts: Fp8Experts, T: int, topk: int, n_shared: int = 0) -> int:
+    n = ctypes.c_size_t()
+    _check(ctx.L.apmoe_moe_workspace_fp8(ctx.handle, experts.ref, T, topk, n_shared, ctypes.byref(n)),
+           "apmoe_moe_workspace_fp8", ctx.L)
+    return n.value
+
+
+def moe_forward_fp8(ctx: Context, experts: Fp8Experts, x, x8, x_scale, w_router, bias, T: int, topk: int,
+                    renormalize: bool, ws, out, stream=None, n_shared: int = 0) -> None:
+    """Whole layer on e4m3 experts: x fp16 is what the router reads, x8 / x_scale the
+    same rows in 8 bits (norm gives both).  ws: a byte tensor of moe_workspace_fp8 bytes."""
+    import torch
+    if experts.device != ctx.device:
+        raise ValueError(f"the experts are on cuda:{experts.device}, the context on cuda:{ctx.device}")
+    E, H = experts.E, experts.H
+    f16, f32 = (torch.float16,), (torch.float32,)
+    _check(ctx.L.apmoe_moe_forward_fp8(ctx.handle, experts.ref, _arg(ctx, x, "x", T * H, f16),
+                                       _arg(ctx, x8, "x8", T * H, _e4m3_types),
+                                       _arg(ctx, x_scale, "x_scale", T * -(-H // 128), f32),
+                                       _arg(ctx, w_router, "w_router", (E - n_shared) * H, f16),
+                                       _arg(ctx, bias, "bias", E - n_shared, f32), T, topk, n_shared, int(renormalize),
+                                       _arg(ctx, ws, "ws", 0, (torch.uint8,)), ws.numel(),
+                                       _arg(ctx, out, "out", T * H, f16), _stream_of(ctx, stream)),
+           "apmoe_moe_forward_fp8", ctx.L)
 
 
 # --------------------------------------------------------------------------- page movement

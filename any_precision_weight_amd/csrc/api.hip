@@ -1095,4 +1095,250 @@ apmoe_status apmoe_moe_forward_noalloc(apmoe_ctx *ctx, const apmoe_table *tbl, i
                              kScratchBytes, out, stream);
 }
 
+// ----------------------------------------------------------------------------
+// the 8-bit path
+// ----------------------------------------------------------------------------
+
+namespace {
+
+// The context's device, current for the time of one call.  Made after the arguments
+// are checked: a refused call does not look into ctx or at the device.
+class OnDevice {
+  public:
+    explicit OnDevice(const apmoe_ctx *ctx)
+    {
+        hipError_t e = hipGetDevice(&before_);
+        if (e == hipSuccess && before_ != ctx->device) {
+            e = hipSetDevice(ctx->device);
+            moved_ = e == hipSuccess;
+        }
+        if (e != hipSuccess)
+            st_ = hip_fail(e, "the context's device");
+    }
+    ~OnDevice()
+    {
+        if (moved_)
+            (void)hipSetDevice(before_);
+    }
+    OnDevice(const OnDevice &) = delete;
+    OnDevice &operator=(const OnDevice &) = delete;
+    apmoe_status status() const { return st_; }
+
+  private:
+    int before_ = -1;
+    bool moved_ = false;
+    apmoe_status st_ = APMOE_OK;
+};
+
+bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
+
+bool float_type(int d) { return d == APMOE_F16 || d == APMOE_BF16 || d == APMOE_F32; }
+
+// What the two products check alike; N: rows of one expert's matrix.
+apmoe_status fp8_args(const uint8_t *x8, const float *x_scale, const uint8_t *w8, const float *w_scale, int32_t E,
+                      int32_t N, int32_t K, int32_t gather, const int32_t *perm, const int32_t *offsets, int32_t T,
+                      int32_t topk)
+{
+    if (E < 1 || E > APMOE_MAX_EXPERTS || N < 1 || K < 16 || K % 16 != 0)
+        return fail(APMOE_INVALID_ARG, "E=%d N=%d K=%d (need 1 <= E <= %d, N >= 1, K%%16==0)", E, N, K,
+                    APMOE_MAX_EXPERTS);
+    if (T < 0 || topk < 1 || topk > APMOE_MAX_ASSIGN || (int64_t)T * topk > (int64_t)1 << 30)
+        return fail(APMOE_INVALID_ARG, "T=%d topk=%d", T, topk);
+    if (!offsets && E != 1)
+        return fail(APMOE_INVALID_ARG, "offsets is NULL with %d experts", E);
+    if (T == 0)
+        return ok();
+    if (!x8 || !x_scale || !w8 || !w_scale || (gather && !perm))
+        return fail(APMOE_INVALID_ARG, "x8 / x_scale / w8 / w_scale / perm is NULL");
+    if (!aligned16(x8) || !aligned16(w8) || !aligned4(x_scale) || !aligned4(w_scale) || !aligned4(perm) ||
+        !aligned4(offsets))
+        return fail(APMOE_INVALID_ARG, "misaligned pointer (x8, w8: 16 bytes; scales, perm, offsets: 4)");
+    return ok();
+}
+
+struct WsLayout8 {
+    size_t ids, w, counts, offsets, perm, inv_perm, a8, as, y, total;
+};
+
+WsLayout8 ws_layout8(int T, int kt, int E, int H, int F)
+{
+    WsLayout8 L;
+    const size_t R = (size_t)T * kt;
+    size_t o = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = o;
+        o = up256(o + bytes);
+        return at;
+    };
+    L.ids = take(R * 4);
+    L.w = take(R * 4);
+    L.counts = take((size_t)E * 4);
+    L.offsets = take(((size_t)E + 1) * 4);
+    L.perm = take(R * 4);
+    L.inv_perm = take(R * 4);
+    L.a8 = take(R * F);
+    L.as = take(R * ((F + 127) / 128) * 4);
+    L.y = take(R * H * 4);
+    L.total = o;
+    return L;
+}
+
+// Sizes of a layer call; needs no GPU.
+apmoe_status fp8_layer_sizes(const apmoe_fp8_experts *ex, int32_t T, int32_t topk, int32_t n_shared)
+{
+    if (!ex)
+        return fail(APMOE_INVALID_ARG, "experts is NULL");
+    if (ex->E < 1 || ex->E > APMOE_MAX_EXPERTS || ex->H < 16 || ex->H % 16 != 0 || ex->F < 16 || ex->F % 16 != 0 ||
+        ex->F > (1 << 30))
+        return fail(APMOE_INVALID_ARG, "E=%d H=%d F=%d (need 1 <= E <= %d, H%%16==0, F%%16==0)", ex->E, ex->H, ex->F,
+                    APMOE_MAX_EXPERTS);
+    if (n_shared < 0 || n_shared > APMOE_MAX_SHARED || n_shared >= ex->E)
+        return fail(APMOE_INVALID_ARG, "n_shared=%d with %d experts", n_shared, ex->E);
+    if (T < 0 || topk < 1 || topk > APMOE_MAX_TOPK || topk > ex->E - n_shared ||
+        (int64_t)T * (topk + n_shared) > (int64_t)1 << 30)
+        return fail(APMOE_INVALID_ARG, "T=%d topk=%d", T, topk);
+    return ok();
+}
+
+}  // namespace
+
+apmoe_status apmoe_norm(apmoe_ctx *ctx, const void *x, int32_t x_dtype, const void *residual, void *residual_out,
+                        int32_t res_dtype, const void *gamma, float eps, int32_t T, int32_t H, void *y, uint8_t *y8,
+                        float *y_scale, void *stream)
+{
+    if (!ctx)
+        return fail(APMOE_INVALID_ARG, "ctx is NULL");
+    if (!float_type(x_dtype) || (residual && !float_type(res_dtype)))
+        return fail(APMOE_UNSUPPORTED, "x_dtype %d, res_dtype %d", x_dtype, res_dtype);
+    if (T < 0 || H < 8 || H > 65536 || H % 8 != 0)
+        return fail(APMOE_INVALID_ARG, "T=%d H=%d (need H%%8==0, 8 <= H <= 65536)", T, H);
+    if (!(eps >= 0.0f) || eps > 3.4e38f)
+        return fail(APMOE_INVALID_ARG, "eps=%g", (double)eps);
+    if (!residual != !residual_out)
+        return fail(APMOE_INVALID_ARG, "residual and residual_out: one is NULL");
+    if (!y8 != !y_scale)
+        return fail(APMOE_INVALID_ARG, "y8 and y_scale: one is NULL");
+    if (!y && !y8)
+        return fail(APMOE_INVALID_ARG, "y and y8 are NULL");
+    if (T == 0)
+        return ok();
+    if (!x || !gamma)
+        return fail(APMOE_INVALID_ARG, "x / gamma is NULL");
+    if (!aligned16(x) || !aligned16(gamma) || !aligned16(residual) || !aligned16(residual_out) || !aligned16(y) ||
+        !aligned16(y8) || !aligned4(y_scale))
+        return fail(APMOE_INVALID_ARG, "misaligned pointer (16 bytes; y_scale 4)");
+    OnDevice dev(ctx);
+    if (dev.status() != APMOE_OK)
+        return dev.status();
+    hipError_t e = apmoe::launch_norm(x, x_dtype, residual, residual_out, res_dtype, gamma, eps, T, H, y, y8, y_scale,
+                                      reinterpret_cast<hipStream_t>(stream));
+    return e == hipSuccess ? ok() : hip_fail(e, "norm launch");
+}
+
+apmoe_status apmoe_gemm_fp8(apmoe_ctx *ctx, const uint8_t *x8, const float *x_scale, const uint8_t *w8,
+                            const float *w_scale, int32_t E, int32_t N, int32_t K, int32_t gather,
+                            const int32_t *perm, const int32_t *offsets, int32_t T, int32_t topk, void *out,
+                            int32_t out_dtype, void *stream)
+{
+    if (!ctx)
+        return fail(APMOE_INVALID_ARG, "ctx is NULL");
+    if (!float_type(out_dtype))
+        return fail(APMOE_UNSUPPORTED, "out_dtype %d", out_dtype);
+    apmoe_status s = fp8_args(x8, x_scale, w8, w_scale, E, N, K, gather, perm, offsets, T, topk);
+    if (s != APMOE_OK || T == 0)
+        return s;
+    if (!out || !aligned16(out))
+        return fail(APMOE_INVALID_ARG, "out NULL or not 16-byte aligned");
+    OnDevice dev(ctx);
+    if (dev.status() != APMOE_OK)
+        return dev.status();
+    hipError_t e = apmoe::launch_gemm_fp8(x8, x_scale, w8, w_scale, E, N, K, gather, perm, offsets, topk, T * topk,
+                                          out, out_dtype, reinterpret_cast<hipStream_t>(stream));
+    return e == hipSuccess ? ok() : hip_fail(e, "gemm_fp8 launch");
+}
+
+apmoe_status apmoe_gemm_act_fp8(apmoe_ctx *ctx, const uint8_t *x8, const float *x_scale, const uint8_t *w8,
+                                const float *w_scale, int32_t E, int32_t F, int32_t K, int32_t gather,
+                                const int32_t *perm, const int32_t *offsets, int32_t T, int32_t topk, uint8_t *a8,
+                                float *a_scale, void *stream)
+{
+    if (!ctx)
+        return fail(APMOE_INVALID_ARG, "ctx is NULL");
+    if (F < 16 || F % 16 != 0 || F > (1 << 30))
+        return fail(APMOE_INVALID_ARG, "F=%d (need F%%16==0)", F);
+    apmoe_status s = fp8_args(x8, x_scale, w8, w_scale, E, 2 * F, K, gather, perm, offsets, T, topk);
+    if (s != APMOE_OK || T == 0)
+        return s;
+    if (!a8 || !a_scale || !aligned16(a8) || !aligned4(a_scale))
+        return fail(APMOE_INVALID_ARG, "a8 / a_scale NULL or misaligned");
+    OnDevice dev(ctx);
+    if (dev.status() != APMOE_OK)
+        return dev.status();
+    hipError_t e = apmoe::launch_gemm_act_fp8(x8, x_scale, w8, w_scale, E, F, K, gather, perm, offsets, topk, T * topk,
+                                              a8, a_scale, reinterpret_cast<hipStream_t>(stream));
+    return e == hipSuccess ? ok() : hip_fail(e, "gemm_act_fp8 launch");
+}
+
+apmoe_status apmoe_moe_workspace_fp8(apmoe_ctx *ctx, const apmoe_fp8_experts *ex, int32_t T, int32_t topk,
+                                     int32_t n_shared, size_t *bytes)
+{
+    if (!ctx || !bytes)
+        return fail(APMOE_INVALID_ARG, "ctx / bytes is NULL");
+    apmoe_status s = fp8_layer_sizes(ex, T, topk, n_shared);
+    if (s != APMOE_OK)
+        return s;
+    *bytes = ws_layout8(T, topk + n_shared, ex->E, ex->H, ex->F).total;
+    return ok();
+}
+
+apmoe_status apmoe_moe_forward_fp8(apmoe_ctx *ctx, const apmoe_fp8_experts *ex, const uint16_t *x, const uint8_t *x8,
+                                   const float *x_scale, const uint16_t *w_router, const float *bias, int32_t T,
+                                   int32_t topk, int32_t n_shared, int32_t renormalize, void *ws, size_t ws_bytes,
+                                   uint16_t *out, void *stream)
+{
+    if (!ctx)
+        return fail(APMOE_INVALID_ARG, "ctx is NULL");
+    apmoe_status s = fp8_layer_sizes(ex, T, topk, n_shared);
+    if (s != APMOE_OK)
+        return s;
+    if (T == 0)
+        return ok();
+    const int E = ex->E, H = ex->H, F = ex->F, kt = topk + n_shared;
+    if (!x || !x8 || !x_scale || !w_router || !ex->gate_up || !ex->gate_up_scale || !ex->down || !ex->down_scale || !out)
+        return fail(APMOE_INVALID_ARG, "x / x8 / x_scale / w_router / the experts' weights or scales / out is NULL");
+    if (!aligned16(x) || !aligned16(x8) || !aligned16(w_router) || !aligned16(ex->gate_up) || !aligned16(ex->down) ||
+        !aligned16(out) || !aligned4(x_scale) || !aligned4(bias) || !aligned4(ex->gate_up_scale) ||
+        !aligned4(ex->down_scale))
+        return fail(APMOE_INVALID_ARG, "misaligned pointer (16 bytes; scales and bias 4)");
+    const WsLayout8 L = ws_layout8(T, kt, E, H, F);
+    if (!ws || ws_bytes < L.total || ((uintptr_t)ws & 255u))
+        return fail(APMOE_INVALID_ARG, "workspace NULL, unaligned or smaller than %zu bytes", L.total);
+    char *w = reinterpret_cast<char *>(ws);
+    int32_t *ids = reinterpret_cast<int32_t *>(w + L.ids);
+    float *tw = reinterpret_cast<float *>(w + L.w);
+    int32_t *counts = reinterpret_cast<int32_t *>(w + L.counts);
+    int32_t *offsets = reinterpret_cast<int32_t *>(w + L.offsets);
+    int32_t *perm = reinterpret_cast<int32_t *>(w + L.perm);
+    int32_t *inv = reinterpret_cast<int32_t *>(w + L.inv_perm);
+    uint8_t *a8 = reinterpret_cast<uint8_t *>(w + L.a8);
+    float *as = reinterpret_cast<float *>(w + L.as);
+    float *y = reinterpret_cast<float *>(w + L.y);
+    OnDevice dev(ctx);
+    if (dev.status() != APMOE_OK)
+        return dev.status();
+    s = apmoe_route(ctx, x, w_router, bias, T, H, E - n_shared, topk, n_shared, renormalize, ids, tw, counts, offsets,
+                    perm, inv, stream);
+    if (s != APMOE_OK)
+        return s;
+    hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+    hipError_t e = apmoe::launch_gemm_act_fp8(x8, x_scale, ex->gate_up, ex->gate_up_scale, E, F, H, 1, perm, offsets,
+                                              kt, T * kt, a8, as, st);
+    if (e == hipSuccess)
+        e = apmoe::launch_gemm_fp8(a8, as, ex->down, ex->down_scale, E, H, F, 0, perm, offsets, kt, T * kt, y,
+                                   APMOE_F32, st);
+    if (e == hipSuccess)
+        e = apmoe::launch_combine(y, 1, tw, inv, T, kt, H, out, st);
+    return e == hipSuccess ? ok() : hip_fail(e, "fp8 layer launch");
+}
+
 }  // extern "C"

@@ -1,0 +1,109 @@
+// fp8.h -- device helpers of the 8-bit path (not installed): e4m3 rows with a scale for
+// each group of 128 columns, and the matrix product of two e4m3 fragments.
+//
+// A row in 8 bits: group g holds columns 128g .. 128g+127 (the last group may be
+// shorter), s[g] = max(max |v| / 448, 2^-126) in fp32 and q[c] = e4m3(v[c] / s[g]),
+// round to nearest even; it stands for q * s.  448 is e4m3's largest value, so no
+// quotient overflows; the lower bound keeps s and 1 / s normal numbers for a group of
+// zeros.  A group with an infinity or a NaN has that as its scale, so all of it stands
+// for NaN.
+#pragma once
+
+#include "device.h"
+
+namespace apmoe {
+
+constexpr int kBlk = 128;  // columns that share a scale; also the columns of one MFMA
+constexpr float kE4m3Max = 448.0f;
+constexpr float kScaleMin = 0x1p-126f;
+
+typedef int int8v __attribute__((ext_vector_type(8)));
+typedef float float4v __attribute__((ext_vector_type(4)));
+
+// 32 bytes of an e4m3 row, a lane's part of one 128-column block.
+struct Frag8 {
+    u32x4 lo, hi;
+};
+
+// The same in fp16 (e4m3's values are fp16 values: exact), as four operands of the
+// 32-column fp16 MFMA.
+struct Frag16 {
+    half8 k[4];
+};
+
+__device__ inline half8 to_half8(uint32_t w0, uint32_t w1)
+{
+    typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+    const half2v a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.0f, false);
+    const half2v b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.0f, true);
+    const half2v c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.0f, false);
+    const half2v d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.0f, true);
+    return half8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+__device__ inline Frag16 to_frag16(const Frag8 &f)
+{
+    return Frag16{{to_half8(f.lo[0], f.lo[1]), to_half8(f.lo[2], f.lo[3]), to_half8(f.hi[0], f.hi[1]),
+                   to_half8(f.hi[2], f.hi[3])}};
+}
+
+// The product of one block, C[16][16] (fp32) = A[16][128] * B[128][16].  Lane l gives 32
+// bytes of A's row l % 16 and of B's column l % 16; which of the 128 columns they are
+// follows from l / 16 in the same way for A and B, and a sum over columns does not ask
+// for their order, so any assignment that A and B share is right.  Lane l receives
+// column l % 16, rows 4 (l / 16) .. + 3.
+//
+// There are two forms.  In fp16 the products are exact and the sum is an fp32 one
+// (2^-22 of the terms' magnitudes, measured).  The e4m3 instruction takes half the
+// time (32 clocks against 4 x 16), but in each group of 8 columns it cuts the products
+// off below 2^-13 of the largest one's power of two (measured with pairs of products;
+// the same for its 32-column form): normally distributed operands give a relative error
+// of 1.5e-5 in norm.  So it serves only where the result is rounded to 16 bits at once
+// (2^-12 for fp16 on average, 16 times that); sums that are kept in fp32 or quantised
+// again take fp16.
+__device__ inline float4v block_product(const Frag16 &a, const Frag16 &b)
+{
+    float4v c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        c = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.k[i], b.k[i], c, 0, 0, 0);
+    return c;
+}
+
+__device__ inline float4v block_product(const Frag8 &a, const Frag8 &b)
+{
+    auto v = [](const Frag8 &f) {
+        return int8v{(int)f.lo[0], (int)f.lo[1], (int)f.lo[2], (int)f.lo[3],
+                     (int)f.hi[0], (int)f.hi[1], (int)f.hi[2], (int)f.hi[3]};
+    };
+    // the instruction's own power-of-two block scales are left out (operands 0)
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v(a), v(b), float4v{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+}
+
+// Magnitude as an unsigned integer: ordered as the magnitudes are, an infinity above
+// every number and a NaN above that, so an integer maximum passes both on (the float
+// maximum drops a NaN).
+__device__ inline uint32_t mag(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu; }
+
+// Scale of a group from the largest magnitude of its values.
+__device__ inline float scale_of(uint32_t amax)
+{
+    const float s = __builtin_bit_cast(float, amax) / kE4m3Max;
+    return s < kScaleMin ? kScaleMin : s;  // a NaN stays
+}
+
+// Four values -> four e4m3 bytes, v[0] lowest.
+__device__ inline uint32_t to_e4m3x4(float v0, float v1, float v2, float v3)
+{
+    int r = __builtin_amdgcn_cvt_pk_fp8_f32(v0, v1, 0, false);
+    r = __builtin_amdgcn_cvt_pk_fp8_f32(v2, v3, r, true);
+    return (uint32_t)r;
+}
+
+// fp32 -> bf16, round to nearest even; a NaN stays one.
+__device__ inline uint16_t to_bf16(float v)
+{
+    return __builtin_bit_cast(uint16_t, (__bf16)v);
+}
+
+}  // namespace apmoe

@@ -68,6 +68,7 @@ typedef int32_t apmoe_status;
 
 #define APMOE_F16 0
 #define APMOE_F32 1
+#define APMOE_BF16 2 /* the 8-bit path's calls only */
 
 #define APMOE_MIN_BITS 3
 #define APMOE_MAX_BITS 8
@@ -433,6 +434,112 @@ apmoe_status apmoe_moe_forward(apmoe_ctx *ctx, const apmoe_table *tbl, int32_t l
 apmoe_status apmoe_moe_forward_noalloc(apmoe_ctx *ctx, const apmoe_table *tbl, int32_t layer, const uint16_t *x,
                                        const uint16_t *w_router, const float *bias, int32_t T, int32_t topk,
                                        int32_t n_shared, int32_t renormalize, uint16_t *out, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * The 8-bit path: the layer on uniform e4m3 experts, and the norm in front of it
+ *
+ * An e4m3 row (OCP 8-bit floating point, 4 exponent bits, largest value 448) has an
+ * fp32 scale for each group of 128 columns (the last group may be shorter): group g
+ * of v stands for q * s with s = max(max |v| / 448, 2^-126) and q = e4m3(v / s),
+ * round to nearest even.  A group with a NaN or an infinity stands for NaN.
+ * An e4m3 weight matrix has an fp32 scale for each block of 128 rows x 128 columns
+ * (the blocks at its lower and right edge may be smaller).
+ * These calls make the context's device current for their own time only, and need
+ * no counters of the context except where said.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Root-mean-square norm with the residual's addition:
+ *   h[t] = x[t] + residual[t] (fp32 sum, rounded to the residual's type), or x[t];
+ *   y[t] = h[t] * gamma / sqrt(mean(h[t]^2) + eps).
+ *   x [T][H] of x_dtype; gamma [H] of x_dtype; residual and residual_out [T][H] of
+ *   res_dtype, both NULL or both set (the same buffer updates it in place; res_dtype
+ *   is then looked at); y [T][H] of x_dtype (may be x) or NULL; y8 e4m3 [T][H] and
+ *   y_scale fp32 [T][ceil(H/128)], both NULL or both set.  At least one of y, y8.
+ * The norm is that of the stored h.  The mean and y are computed in fp64 (squares of
+ * large values stay finite, and y8 rounds as the formula says).  A row with a NaN
+ * gives NaN.  Types: APMOE_F16, APMOE_BF16, APMOE_F32, any mixture.
+ * Limits: H % 8 == 0, 8 <= H <= 65536, T >= 0, eps >= 0 and finite.  Buffers other
+ * than the two pairs named must not overlap.  Errors (nothing enqueued): INVALID_ARG
+ * for NULL or misaligned pointers (16 bytes; y_scale 4) or bad sizes, UNSUPPORTED for
+ * another type.
+ */
+apmoe_status apmoe_norm(apmoe_ctx *ctx, const void *x, int32_t x_dtype, const void *residual, void *residual_out,
+                        int32_t res_dtype, const void *gamma, float eps, int32_t T, int32_t H, void *y, uint8_t *y8,
+                        float *y_scale, void *stream);
+
+/*
+ * Experts' product on e4m3 operands.  For expert e, rows r in [offsets[e],
+ * offsets[e+1]) of the output:
+ *   out[r][n] = sum_b x_scale[s][b] * w_scale[e][n/128][b] *
+ *               sum_{c in 128-column block b} x8[s][c] * w8[e][n][c],
+ * s = perm[r] / topk when gather != 0, else r; fp32 accumulation, each block's sum
+ * scaled in fp32.
+ *   x8 e4m3 [T][K] (gather) or [T*topk][K], x_scale fp32 [rows][ceil(K/128)];
+ *   w8 e4m3 [E][N][K], w_scale fp32 [E][ceil(N/128)][ceil(K/128)];
+ *   out [T*topk][N] of out_dtype (APMOE_F16, APMOE_BF16, APMOE_F32), RNE.
+ * perm and offsets as apmoe_route writes them; rows of the output at or past
+ * offsets[E] are not written.  A dense product is E = 1, topk = 1 with offsets NULL
+ * (every row is the one expert's) and gather = 0.
+ * Limits: 1 <= E <= 256, N >= 1, K % 16 == 0, K >= 16, 1 <= topk <= 16, T >= 0,
+ * T * topk <= 2^30.  Errors (nothing enqueued): INVALID_ARG for NULL or misaligned
+ * pointers (16 bytes; scales, perm and offsets 4), offsets NULL with E > 1, or bad
+ * sizes; UNSUPPORTED for another out_dtype.
+ */
+apmoe_status apmoe_gemm_fp8(apmoe_ctx *ctx, const uint8_t *x8, const float *x_scale, const uint8_t *w8,
+                            const float *w_scale, int32_t E, int32_t N, int32_t K, int32_t gather,
+                            const int32_t *perm, const int32_t *offsets, int32_t T, int32_t topk, void *out,
+                            int32_t out_dtype, void *stream);
+
+/*
+ * gate_up product with the expert activation and the 8-bit output in its epilogue:
+ *   g, u = rows f and F + f of the product above (fp32),  a = g / (1 + e^-g) * u,
+ *   a8, a_scale = a as e4m3 rows.
+ *   w8 e4m3 [E][2F][K]: rows [0, F) gate, [F, 2F) up; w_scale fp32
+ *   [E][2][ceil(F/128)][ceil(K/128)]: each half has blocks of its own (the layout of a
+ *   [2F][K] matrix where F % 128 == 0);
+ *   a8 e4m3 [T*topk][F], a_scale fp32 [T*topk][ceil(F/128)].
+ * F % 16 == 0, F >= 16; other arguments, limits and errors as apmoe_gemm_fp8.
+ */
+apmoe_status apmoe_gemm_act_fp8(apmoe_ctx *ctx, const uint8_t *x8, const float *x_scale, const uint8_t *w8,
+                                const float *w_scale, int32_t E, int32_t F, int32_t K, int32_t gather,
+                                const int32_t *perm, const int32_t *offsets, int32_t T, int32_t topk, uint8_t *a8,
+                                float *a_scale, void *stream);
+
+/* The experts of one layer in e4m3: E of them (the routed ones, then the shared ones),
+ * gate_up [E][2F][H] with scales [E][2][ceil(F/128)][ceil(H/128)], down [E][H][F] with
+ * scales [E][ceil(H/128)][ceil(F/128)]; device memory, caller-owned.  H and F are
+ * multiples of 16. */
+typedef struct apmoe_fp8_experts {
+    int32_t E;
+    int32_t H;
+    int32_t F;
+    const uint8_t *gate_up;
+    const float *gate_up_scale;
+    const uint8_t *down;
+    const float *down_scale;
+} apmoe_fp8_experts;
+
+/* Device workspace bytes of apmoe_moe_forward_fp8.  Host only. */
+apmoe_status apmoe_moe_workspace_fp8(apmoe_ctx *ctx, const apmoe_fp8_experts *ex, int32_t T, int32_t topk,
+                                     int32_t n_shared, size_t *bytes);
+
+/*
+ * Whole layer on e4m3 experts: apmoe_route on x, apmoe_gemm_act_fp8 on (x8, x_scale),
+ * apmoe_gemm_fp8 into fp32, apmoe_combine.  x fp16 [T][H] is what the router reads, x8
+ * and x_scale the same rows in 8 bits (apmoe_norm gives both); out fp16 [T][H].
+ * The first E - n_shared experts are the routed ones (w_router rows, bias as in
+ * apmoe_route), the last n_shared see every token with weight 1.
+ * ws is caller-owned device memory of at least apmoe_moe_workspace_fp8 bytes, 256-byte
+ * aligned.  Every limit of the steps is checked before the first launch.  The call
+ * enqueues only kernel launches on `stream`, so it can be captured in a HIP graph; two
+ * calls (or two captured graphs) that may run at the same time need a workspace each,
+ * and, as for apmoe_route, a context each.
+ */
+apmoe_status apmoe_moe_forward_fp8(apmoe_ctx *ctx, const apmoe_fp8_experts *ex, const uint16_t *x, const uint8_t *x8,
+                                   const float *x_scale, const uint16_t *w_router, const float *bias, int32_t T,
+                                   int32_t topk, int32_t n_shared, int32_t renormalize, void *ws, size_t ws_bytes,
+                                   uint16_t *out, void *stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,522 @@
+"""The 8-bit path on the GPU, through the C ABI, against plain implementations in 64
+bits (fp8_ref): the norm with the residual's addition and the 8-bit output, the e4m3
+product and the gate_up product with the activation, and the whole layer.
+
+Bounds.  The product of one block of 128 columns is an fp32 sum of 128 exact products
+(e4m3 x e4m3 has 8 significant bits), scaled with two roundings and added with one per
+block: |err| <= (128 + 2 KB + 3) 2^-23 * sum |terms| with KB blocks covers any order and
+a matrix unit that cuts off instead of rounding; the split over column parts adds at
+most 8 more terms.  16-bit outputs add half a step of their type.
+
+8-bit outputs: the scale has the relative error of the largest magnitude.  Where the
+value in 64 bits lies within its error bound of a border between two e4m3 values either
+neighbour is right, so a value may be off by half a step of e4m3 (2^-4 relative, 2^-10
+below the smallest normal number 2^-6) plus its own error."""
+import zlib
+
+import numpy as np
+import pytest
+import torch
+
+import any_precision_weight_amd as apw
+import fp8_ref as ref
+from gpu_util import ctx
+
+pytestmark = pytest.mark.gpu
+
+TORCH = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
+HALF_STEP = {"f16": 2.0 ** -11, "bf16": 2.0 ** -8, "f32": 2.0 ** -24}
+SMALLEST = {"f16": 2.0 ** -25, "bf16": 2.0 ** -134, "f32": 2.0 ** -150}  # half the spacing at zero
+
+
+def cuda(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def np64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def codes(t):
+    return t.view(torch.uint8).cpu().numpy()
+
+
+def rng_of(*key):
+    return np.random.default_rng([zlib.crc32(k.encode()) if isinstance(k, str) else int(k) for k in key])
+
+
+def cast(x, t):
+    """fp64 -> type t, as a CPU tensor."""
+    return torch.from_numpy(np.asarray(x, np.float32)).to(TORCH[t])
+
+
+# ------------------------------------------------------------------ norm
+
+def run_norm(x, res, gamma, eps, want_y=True, want_q=True, inplace=False):
+    T, H = x.shape
+    y = torch.full_like(x, 7.0) if want_y else None
+    q = torch.full((T, H), 0x55, dtype=torch.uint8, device="cuda") if want_q else None
+    s = torch.full((T, ref.groups(H)), -1.0, device="cuda") if want_q else None
+    h = None if res is None else (res if inplace else torch.full_like(res, 7.0))
+    apw.norm(ctx(), x, res, h, gamma, eps, T, H, y, q, s)
+    torch.cuda.synchronize()
+    return h, y, q, s
+
+
+def check_norm(x, res, gamma, eps, got):
+    h, y, q, s = got
+    xt = {v: k for k, v in TORCH.items()}[x.dtype]
+    store = (lambda v: v) if res is None else (lambda v: torch.from_numpy(v).to(res.dtype).float().numpy())
+    resn = None if res is None else res.float().cpu().numpy()
+    h64, y64 = ref.norm(x.float().cpu().numpy(), resn, gamma.float().cpu().numpy(), eps, store)
+    if h is not None:
+        np.testing.assert_array_equal(np64(h), h64)
+    if y is not None:
+        err = np.abs(np64(y) - y64)
+        # one rounding to fp32 and one to the type, of a value known to 2^-50
+        assert np.all(err <= np.abs(y64) * (HALF_STEP[xt] + 2.0 ** -24 + 2.0 ** -48) + SMALLEST[xt])
+    if q is not None:
+        q64, s64 = ref.quant(y64)
+        np.testing.assert_allclose(np64(s), s64, rtol=2.0 ** -23, atol=0)
+        got_q, s_ = ref.TABLE[codes(q)], ref.spread(np64(s), x.shape[1])
+        # the 64-bit quotient by the scale as written; a border between two values may fall
+        # either way only where the quotient is within 2^-23 of it (its rounding to fp32)
+        with np.errstate(invalid="ignore"):
+            v = y64 / s_
+        off = np.abs(got_q - v)
+        half = np.maximum(np.exp2(np.floor(np.log2(np.maximum(np.abs(v), 2.0 ** -6)))) * 2.0 ** -4, 2.0 ** -10)
+        assert np.all(off <= half + np.abs(v) * 2.0 ** -23)
+
+
+NORM_SHAPES = [(1, 8), (1, 128), (3, 136), (5, 504), (2, 520), (7, 704), (4, 1032), (3, 2048), (2, 2056), (3, 4096),
+               (2, 4104), (1, 8192), (2, 8200), (1, 32768), (2, 32776), (1, 65536), (333, 264), (1025, 64)]
+
+
+@pytest.mark.parametrize("T,H", NORM_SHAPES)
+def test_norm_shapes(T, H):
+    r = rng_of("norm", T, H)
+    x, res = cast(r.normal(size=(T, H)), "f16").cuda(), cast(4 * r.normal(size=(T, H)), "bf16").cuda()
+    gamma = cast(1 + 0.2 * r.normal(size=H), "f16").cuda()
+    check_norm(x, res, gamma, 1e-5, run_norm(x, res, gamma, 1e-5))
+
+
+@pytest.mark.parametrize("xt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("rt", [None, "f16", "bf16", "f32"])
+def test_norm_types_and_outputs(xt, rt):
+    r = rng_of("types", xt, str(rt))
+    T, H = 37, 712
+    x = cast(r.normal(size=(T, H)), xt).cuda()
+    gamma = cast(1 + 0.2 * r.normal(size=H), xt).cuda()
+    for want_y, want_q, inplace in ((True, True, False), (True, False, True), (False, True, False)):
+        res = None if rt is None else cast(3 * r.normal(size=(T, H)), rt).cuda()
+        before = None if res is None else res.clone()
+        got = run_norm(x, res, gamma, 1e-6, want_y, want_q, inplace)
+        check_norm(x, before, gamma, 1e-6, got)
+        if res is not None and not inplace:
+            assert torch.equal(res, before)
+
+
+def test_norm_in_place_y():
+    r = rng_of("inplace")
+    x = cast(r.normal(size=(9, 1048)), "bf16").cuda()
+    gamma = cast(1 + 0.2 * r.normal(size=1048), "bf16").cuda()
+    _, y, _, _ = run_norm(x, None, gamma, 1e-5, True, False)
+    z = x.clone()
+    apw.norm(ctx(), z, None, None, gamma, 1e-5, 9, 1048, z)
+    assert torch.equal(z.view(torch.int16), y.view(torch.int16))
+
+
+def test_norm_special_rows():
+    """Zeros, huge and tiny rows, NaN and infinities: each row by itself."""
+    H = 272
+    r = rng_of("special")
+    x = r.normal(size=(8, H))
+    x[0] = 0.0
+    x[1] *= 1e30   # squares leave fp32's range
+    x[2] *= 1e-30
+    x[3, 5] = np.nan
+    x[4, 5] = np.inf
+    x[5, :128] = 0.0  # one group of zeros
+    x[6, 140] = 3e38
+    xd = cast(x, "f32").cuda()
+    gamma = cast(np.ones(H), "f32").cuda()
+    _, y, q, s = run_norm(xd, None, gamma, 1e-5)
+    fine = [0, 1, 2, 5, 6, 7]
+    check_norm(xd[fine], None, gamma, 1e-5, (None, y[fine], q[fine], s[fine]))
+    assert torch.isnan(y[3]).all() and torch.isnan(y[4, 5])
+    values = ref.TABLE[codes(q)] * ref.spread(np64(s), H)
+    assert np.isnan(values[3]).all()
+    assert np.isnan(values[4, :128]).all() and (values[4, 128:] == 0).all()
+    assert (codes(q[0]) & 0x7F == 0).all() and (np64(s[0]) == 2.0 ** -126).all()
+    assert (codes(q[5, :128]) & 0x7F == 0).all()
+    z = torch.zeros((2, H), device="cuda")  # eps = 0 and a row of zeros: 0 / 0
+    _, yz, _, _ = run_norm(z, None, gamma, 0.0)
+    assert torch.isnan(yz).all()
+
+
+# ------------------------------------------------------------------ products
+
+def routing(r, T, topk, E, skew=0.0):
+    """Distinct experts of each token, perm and offsets."""
+    z = r.normal(size=(T, E)) - skew * np.log(np.arange(1, E + 1))
+    ids = np.argsort(-z, axis=1)[:, :topk].reshape(-1)
+    perm = np.argsort(ids, kind="stable").astype(np.int32)
+    off = np.zeros(E + 1, np.int32)
+    off[1:] = np.cumsum(np.bincount(ids, minlength=E))
+    return perm, off
+
+
+def random_weights(r, E, halves, rows, K):
+    """Random codes (no NaN code) and scales."""
+    c = r.integers(0, 256, size=(E, halves * rows, K), dtype=np.uint8)
+    c[(c & 0x7F) == 0x7F] ^= 1
+    s = np.exp2(r.uniform(-14, -8, size=(E, halves, ref.groups(rows), ref.groups(K)))).astype(np.float32)
+    return c, s
+
+
+def random_rows(r, R, K):
+    c = r.integers(0, 256, size=(R, K), dtype=np.uint8)
+    c[(c & 0x7F) == 0x7F] ^= 1
+    return c, np.exp2(r.uniform(-9, -5, size=(R, ref.groups(K)))).astype(np.float32)
+
+
+def sum_bound(K):
+    return (128 + 2 * ref.groups(K) + 3 + 8) * 2.0 ** -23
+
+
+# (T, topk, E, N, K): one row, one column block, ragged K and N, many rows, idle experts
+GEMMS = [(1, 1, 1, 1, 16), (1, 1, 1, 128, 128), (1, 1, 1, 33, 144), (3, 2, 4, 129, 240), (8, 1, 1, 256, 1024),
+         (16, 2, 8, 200, 528), (17, 1, 1, 64, 2048), (33, 1, 1, 130, 400), (40, 4, 6, 384, 1408), (64, 1, 1, 515, 656),
+         (65, 1, 2, 256, 512), (130, 2, 3, 300, 1040), (257, 1, 1, 260, 384), (300, 3, 5, 272, 272),
+         (513, 1, 1, 520, 912), (700, 2, 9, 128, 128), (1000, 1, 2, 600, 1552)]
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("T,topk,E,N,K", GEMMS)
+def test_gemm(T, topk, E, N, K, gather):
+    r = rng_of("gemm", T, topk, E, N, K, gather)
+    perm, off = routing(r, T, topk, E, 1.0 if T > 100 else 0.0)
+    R = T * topk
+    x8, xs = random_rows(r, T if gather else R, K)
+    w8, ws = random_weights(r, E, 1, N, K)
+    xv = ref.TABLE[x8] * ref.spread(xs.astype(np.float64), K)
+    wv = [ref.block_values(w8[e], ws[e, 0]) for e in range(E)]
+    want, mag = ref.product(xv, wv, perm, off, topk, gather)
+    dx, dxs, dw, dws, dp, do = (cuda(v) for v in (x8, xs, w8, ws, perm, off))
+    for t in ("f32", "f16", "bf16"):
+        out = torch.full((R + 2, N), 7.0, dtype=TORCH[t], device="cuda")
+        apw.gemm_fp8(ctx(), dx, dxs, dw, dws, E, N, K, gather, dp, do, T, topk, out)
+        torch.cuda.synchronize()
+        got = np64(out)
+        bound = mag * sum_bound(K)
+        bound = bound + (np.abs(want) + bound) * HALF_STEP[t] + SMALLEST[t]
+        err = np.abs(got[:R] - want)
+        assert np.all(err <= bound), (t, float((err - bound).max()))
+        assert (got[R:] == 7.0).all()  # rows behind the last
+
+
+def test_gemm_dense_without_offsets():
+    r = rng_of("dense")
+    T, N, K = 45, 200, 320
+    x8, xs = random_rows(r, T, K)
+    w8, ws = random_weights(r, 1, 1, N, K)
+    d = [cuda(v) for v in (x8, xs, w8, ws)]
+    a, b = (torch.empty((T, N), device="cuda") for _ in range(2))
+    apw.gemm_fp8(ctx(), *d, 1, N, K, False, None, None, T, 1, a)
+    off = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    perm = torch.arange(T, dtype=torch.int32, device="cuda")
+    apw.gemm_fp8(ctx(), *d, 1, N, K, True, perm, off, T, 1, b)
+    assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,E", [(20, 3), (200, 3)])
+def test_gemm_rows_behind_the_last_sequence(T, E):
+    """offsets that end before T * topk rows: the rows behind stay as they were."""
+    r = rng_of("behind", T)
+    N, K, used = 144, 272, T - 7
+    off = np.array([0, used // 2, used // 2, used], np.int32)
+    x8, xs = random_rows(r, T, K)
+    w8, ws = random_weights(r, E, 1, N, K)
+    perm = np.arange(T, dtype=np.int32)
+    out = torch.full((T, N), 7.0, device="cuda")
+    apw.gemm_fp8(ctx(), *(cuda(v) for v in (x8, xs, w8, ws)), E, N, K, False, cuda(perm), cuda(off), T, 1, out)
+    want, mag = ref.product(ref.TABLE[x8] * ref.spread(xs.astype(np.float64), K),
+                            [ref.block_values(w8[e], ws[e, 0]) for e in range(E)], perm, off, 1, False)
+    got = np64(out)
+    assert (got[used:] == 7.0).all()
+    assert np.all(np.abs(got[:used] - want) <= mag * sum_bound(K))
+
+
+@pytest.mark.parametrize("T", [5, 70])
+def test_gemm_nan_stays_in_its_row_and_column(T):
+    r = rng_of("nan", T)
+    N, K = 96, 400
+    x8, xs = random_rows(r, T, K)
+    w8, ws = random_weights(r, 1, 1, N, K)
+    x8[2, 390] = 0x7F
+    w8[0, 40, 3] = 0xFF
+    out = torch.empty((T, N), device="cuda")
+    apw.gemm_fp8(ctx(), *(cuda(v) for v in (x8, xs, w8, ws)), 1, N, K, False, None, None, T, 1, out)
+    nan = np.isnan(np64(out))
+    want = np.zeros((T, N), bool)
+    want[2], want[:, 40] = True, True
+    np.testing.assert_array_equal(nan, want)
+
+
+def act_bounds(gu, mag, F, K):
+    """(a in 64 bits, bound of its error): g and u known to sum_bound, SiLU(g) * u moved by
+    at most (1.1 |u| + |s|) times that (the slope of SiLU is below 1.1), and 2^-20 for the
+    exponential, the reciprocal and the products."""
+    g, u = gu[:, :F], gu[:, F:]
+    s = ref.silu(g)
+    dg, du = mag[:, :F] * sum_bound(K), mag[:, F:] * sum_bound(K)
+    err = 1.1 * dg * (np.abs(u) + du) + np.abs(s) * du + np.abs(s * u) * 2.0 ** -20
+    # e^-g overflows fp32 below about -88: SiLU is below 2^-120 there
+    return s * u, err + 2.0 ** -100 * np.abs(u)
+
+
+def check_rows8(a, err, q, s, C):
+    """8-bit rows against 64-bit values with error bounds."""
+    got_s = np64(s)
+    G = ref.groups(C)
+    for g in range(G):
+        c = slice(g * ref.BLK, min(C, (g + 1) * ref.BLK))
+        amax, e = np.abs(a[:, c]).max(axis=1), err[:, c].max(axis=1)
+        want = np.maximum(amax / 448.0, ref.TINY)
+        assert np.all(np.abs(got_s[:, g] - want) <= e / 448.0 + want * 2.0 ** -22)
+    sv = ref.spread(got_s, C)
+    v, got = a / sv, ref.TABLE[codes(q)]
+    half = np.maximum(np.exp2(np.floor(np.log2(np.maximum(np.abs(v) + err / sv, 2.0 ** -6)))) * 2.0 ** -4, 2.0 ** -10)
+    assert np.all(np.abs(got - v) <= half + err / sv + np.abs(v) * 2.0 ** -22)
+
+
+ACTS = [(1, 1, 1, 16, 16), (1, 1, 1, 128, 128), (3, 2, 4, 144, 240), (16, 2, 8, 272, 528), (33, 1, 1, 704, 256),
+        (40, 4, 6, 384, 400), (130, 2, 3, 208, 1040), (300, 1, 2, 400, 272), (600, 2, 5, 256, 512)]
+
+
+@pytest.mark.parametrize("gather", [True, False])
+@pytest.mark.parametrize("T,topk,E,F,K", ACTS)
+def test_gemm_act(T, topk, E, F, K, gather):
+    r = rng_of("act", T, topk, E, F, K, gather)
+    perm, off = routing(r, T, topk, E, 1.0 if T > 100 else 0.0)
+    R = T * topk
+    x8, xs = random_rows(r, T if gather else R, K)
+    w8, ws = random_weights(r, E, 2, F, K)
+    xs = (xs / np.sqrt(K)).astype(np.float32)
+    xv = ref.TABLE[x8] * ref.spread(xs.astype(np.float64), K)
+    wv = [np.concatenate([ref.block_values(w8[e, h * F:(h + 1) * F], ws[e, h]) for h in (0, 1)]) for e in range(E)]
+    gu, mag = ref.product(xv, wv, perm, off, topk, gather)
+    a8 = torch.full((R + 1, F), 0x55, dtype=torch.uint8, device="cuda")
+    sc = torch.full((R + 1, ref.groups(F)), -1.0, device="cuda")
+    apw.gemm_act_fp8(ctx(), *(cuda(v) for v in (x8, xs, w8, ws)), E, F, K, gather, cuda(perm), cuda(off), T, topk, a8,
+                     sc)
+    torch.cuda.synchronize()
+    a, err = act_bounds(gu, mag, F, K)
+    check_rows8(a, err, a8[:R], sc[:R], F)
+    assert (codes(a8[R:]) == 0x55).all() and (np64(sc[R:]) == -1.0).all()
+
+
+def test_gemm_act_zero_and_nan_groups():
+    """A token of zeros gives groups of zeros with the smallest scale; a NaN in a token
+    gives NaN for that token alone."""
+    r = rng_of("act-special")
+    T, F, K = 6, 144, 256
+    x8, xs = random_rows(r, T, K)
+    w8, ws = random_weights(r, 1, 2, F, K)
+    x8[1] = 0
+    x8[4, 7] = 0x7F
+    a8 = torch.empty((T, F), dtype=torch.uint8, device="cuda")
+    sc = torch.empty((T, 2), device="cuda")
+    apw.gemm_act_fp8(ctx(), *(cuda(v) for v in (x8, xs, w8, ws)), 1, F, K, False, None, None, T, 1, a8, sc)
+    v = ref.TABLE[codes(a8)] * ref.spread(np64(sc), F)
+    assert (v[1] == 0).all() and (np64(sc)[1] == 2.0 ** -126).all()
+    assert np.isnan(v[4]).all()
+    assert np.isfinite(np.delete(v, 4, axis=0)).all()
+
+
+# ------------------------------------------------------------------ layer
+
+def layer_inputs(r, E, n_shared, H, F, T):
+    Et = E + n_shared
+    w1, s1 = random_weights(r, Et, 2, F, H)
+    w2, s2 = random_weights(r, Et, 1, H, F)
+    s1 /= np.float32(np.sqrt(H))
+    s2 /= np.float32(np.sqrt(F))
+    x = (r.normal(size=(T, H))).astype(np.float16)
+    wr = (r.normal(size=(E, H)) * 0.05).astype(np.float16)
+    q, s = ref.quant(x.astype(np.float64))
+    return dict(w1=w1, s1=s1, w2=w2, s2=s2, x=x, wr=wr, x8=ref.encode(q), xs=s.astype(np.float32))
+
+
+def layer_ref(d, bias, E, n_shared, H, F, T, topk, renorm):
+    """(out, bound)."""
+    z = d["x"].astype(np.float64) @ d["wr"].astype(np.float64).T + (0 if bias is None else bias.astype(np.float64))
+    xv = ref.TABLE[d["x8"]] * ref.spread(d["xs"].astype(np.float64), H)
+    out, bound = np.zeros((T, H)), np.zeros((T, H))
+    for t in range(T):
+        ids = np.argsort(-z[t], kind="stable")[:topk]
+        p = np.exp(z[t] - z[t].max())
+        w = p[ids] / (p[ids] if renorm else p).sum()
+        for e, we in list(zip(ids, w)) + [(E + i, 1.0) for i in range(n_shared)]:
+            w1 = np.concatenate([ref.block_values(d["w1"][e, h * F:(h + 1) * F], d["s1"][e, h]) for h in (0, 1)])
+            w2 = ref.block_values(d["w2"][e], d["s2"][e, 0])
+            gu, mag = xv[t] @ w1.T, np.abs(xv[t]) @ np.abs(w1).T
+            a, err = act_bounds(gu[None], mag[None], F, H)
+            q, s = ref.quant(a)
+            sv = ref.spread(s, F)
+            v = a / sv
+            # a value near a border of e4m3 may fall either way: a whole step (twice the half) there
+            step = 2 * np.maximum(np.exp2(np.floor(np.log2(np.maximum(np.abs(v), 2.0 ** -6)))) * 2.0 ** -4, 2.0 ** -10)
+            frac = np.abs(v - q)  # distance to the chosen value; a border is half a step away
+            flips = frac >= step / 2 - err / sv - np.abs(v) * 2.0 ** -21
+            slack = np.where(flips, step, 0.0) * sv + np.abs(q * sv) * 2.0 ** -21 + np.repeat(
+                np.array([err[0, g * 128:(g + 1) * 128].max() for g in range(ref.groups(F))]), 128)[None, :F]
+            y, ymag = (q * sv) @ w2.T, np.abs(q * sv) @ np.abs(w2).T
+            out[t] += we * y[0]
+            bound[t] += we * (ymag[0] * (sum_bound(F) + 2.0 ** -22) + (slack @ np.abs(w2).T)[0])
+    return out, bound + (np.abs(out) + bound) * 2.0 ** -11 + 2.0 ** -25
+
+
+LAYERS = [  # T, E, topk, shared, H, F, renorm, bias
+    (1, 4, 2, 0, 256, 512, True, False), (1, 1, 1, 0, 16, 16, True, False), (1, 12, 4, 2, 272, 144, False, True),
+    (2, 8, 2, 1, 528, 400, True, True), (3, 60, 8, 4, 256, 208, False, False), (4, 5, 5, 0, 400, 272, True, True),
+    (7, 3, 2, 8, 144, 704, False, False), (16, 8, 2, 0, 384, 256, True, False), (17, 8, 2, 1, 384, 256, True, False),
+    (33, 6, 3, 0, 272, 272, False, True), (100, 4, 2, 1, 256, 384, True, True), (16, 200, 8, 1, 128, 64, True, False)]
+
+
+def run_layer(d, bias, E, n_shared, H, F, T, topk, renorm, stream=None):
+    ex = apw.Fp8Experts(cuda(d["w1"]), cuda(d["s1"]), cuda(d["w2"]), cuda(d["s2"]))
+    n = apw.moe_workspace_fp8(ctx(), ex, T, topk, n_shared=n_shared)
+    ws = torch.full((n,), 0xA5, dtype=torch.uint8, device="cuda")  # nothing is read before it is written
+    out = torch.full((T + 1, H), 7.0, dtype=torch.float16, device="cuda")
+    args = [cuda(d["x"]), cuda(d["x8"]), cuda(d["xs"]), cuda(d["wr"]), None if bias is None else cuda(bias)]
+    apw.moe_forward_fp8(ctx(), ex, *args, T, topk, renorm, ws, out, n_shared=n_shared)
+    torch.cuda.synchronize()
+    assert (np64(out[T:]) == 7.0).all()
+    return np64(out[:T]), (ex, args, ws, out)
+
+
+@pytest.mark.parametrize("T,E,topk,shared,H,F,renorm,has_bias", LAYERS)
+def test_layer(T, E, topk, shared, H, F, renorm, has_bias):
+    r = rng_of("layer", T, E, topk, shared, H, F)
+    d = layer_inputs(r, E, shared, H, F, T)
+    bias = (r.normal(size=E) * 0.5).astype(np.float32) if has_bias else None
+    want, bound = layer_ref(d, bias, E, shared, H, F, T, topk, renorm)
+    got, _ = run_layer(d, bias, E, shared, H, F, T, topk, renorm)
+    err = np.abs(got - want)
+    assert np.all(err <= bound), float((err / bound).max())
+
+
+@pytest.mark.parametrize("T", [1, 4, 16, 20])
+def test_layer_ties_go_to_the_lower_expert(T):
+    """Identical router rows: every token takes experts 0 .. topk-1."""
+    r = rng_of("ties", T)
+    E, topk, H, F = 6, 2, 128, 64
+    d = layer_inputs(r, E, 0, H, F, T)
+    d["wr"][:] = d["wr"][0]
+    want, bound = layer_ref(d, None, E, 0, H, F, T, topk, True)
+    got, _ = run_layer(d, None, E, 0, H, F, T, topk, True)
+    assert np.all(np.abs(got - want) <= bound)
+
+
+@pytest.mark.parametrize("T", [1, 5, 40])
+def test_layer_graph_replays(T):
+    """Captured once, replayed with new rows, with work of the program's own between."""
+    r = rng_of("graph", T)
+    E, topk, shared, H, F = 8, 2, 1, 256, 384
+    d = layer_inputs(r, E, shared, H, F, T)
+    _, (ex, args, ws, out) = run_layer(d, None, E, shared, H, F, T, topk, True)
+    other = [layer_inputs(rng_of("graph", T, i), E, shared, H, F, T) for i in range(3)]
+
+    def call(stream=None):
+        apw.moe_forward_fp8(ctx(), ex, *args, T, topk, True, ws, out, stream=stream, n_shared=shared)
+
+    def put(o):
+        for i, k in enumerate(("x", "x8", "xs")):
+            args[i].copy_(cuda(o[k]))
+
+    refs = []
+    for o in other:
+        put(o)
+        call()
+        torch.cuda.synchronize()
+        refs.append(out[:T].clone())
+    s = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        call(s)
+    noise = torch.randn(64, 64, device="cuda")
+    for rep in range(6):
+        put(other[rep % 3])
+        out.fill_(float("nan"))
+        noise = torch.tanh(noise @ noise)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[:T], refs[rep % 3]), rep
+
+
+def test_layer_on_two_streams_with_a_workspace_and_context_each():
+    r = rng_of("streams")
+    E, topk, H, F, T = 8, 2, 256, 384, 3
+    d = layer_inputs(r, E, 0, H, F, T)
+    want, (ex, args, ws, _) = run_layer(d, None, E, 0, H, F, T, topk, True)
+    ctxs = [ctx(), apw.Context(0)]
+    st = [torch.cuda.Stream() for _ in range(2)]
+    outs = [torch.empty((T, H), dtype=torch.float16, device="cuda") for _ in range(2)]
+    spaces = [torch.empty_like(ws) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i in range(2):
+            apw.moe_forward_fp8(ctxs[i], ex, *args, T, topk, True, spaces[i], outs[i], stream=st[i])
+    torch.cuda.synchronize()
+    for o in outs:
+        np.testing.assert_array_equal(np64(o), want)
+    ctxs[1].close()
+
+
+def test_norm_then_layer_then_norm():
+    """The calls as a decode step makes them: norm with the residual -> layer on its two
+    outputs -> the next norm adds the layer's output to the residual."""
+    r = rng_of("chain")
+    E, topk, H, F = 8, 2, 256, 384
+    for T in (1, 4, 24):
+        d = layer_inputs(r, E, 0, H, F, T)
+        attn = cast(r.normal(size=(T, H)), "f16").cuda()
+        res = cast(3 * r.normal(size=(T, H)), "f32").cuda()
+        res0 = res.clone()
+        gamma = cast(1 + 0.1 * r.normal(size=H), "f16").cuda()
+        x = torch.empty((T, H), dtype=torch.float16, device="cuda")
+        x8 = torch.empty((T, H), dtype=torch.float8_e4m3fn, device="cuda")
+        xs = torch.empty((T, ref.groups(H)), device="cuda")
+        apw.norm(ctx(), attn, res, res, gamma, 1e-5, T, H, x, x8, xs)
+        ex = apw.Fp8Experts(cuda(d["w1"]), cuda(d["s1"]), cuda(d["w2"]), cuda(d["s2"]))
+        ws = torch.empty(apw.moe_workspace_fp8(ctx(), ex, T, topk), dtype=torch.uint8, device="cuda")
+        out = torch.empty((T, H), dtype=torch.float16, device="cuda")
+        apw.moe_forward_fp8(ctx(), ex, x, x8, xs, cuda(d["wr"]), None, T, topk, True, ws, out)
+        x2 = torch.empty_like(x)
+        apw.norm(ctx(), out, res, res, gamma, 1e-5, T, H, x2)
+        torch.cuda.synchronize()
+        check_norm(attn, res0, gamma, 1e-5, (None, x, x8, xs))
+        d.update(x=x.cpu().numpy(), x8=codes(x8), xs=xs.cpu().numpy())
+        want, bound = layer_ref(d, None, E, 0, H, F, T, topk, True)
+        assert np.all(np.abs(np64(out) - want) <= bound)
+        mid = (attn.float() + res0)
+        assert torch.equal(res, out.float() + mid)
+        check_norm(out, mid, gamma, 1e-5, (None, x2, None, None))
+
+
+def test_same_bits_again():
+    """No atomics: the same inputs give the same bits."""
+    r = rng_of("again")
+    T, topk, E, N, K = 90, 2, 4, 256, 1408
+    perm, off = routing(r, T, topk, E)
+    x8, xs = random_rows(r, T, K)
+    w8, ws = random_weights(r, E, 1, N, K)
+    d = [cuda(v) for v in (x8, xs, w8, ws, perm, off)]
+    outs = []
+    for _ in range(3):
+        out = torch.empty((T * topk, N), device="cuda")
+        apw.gemm_fp8(ctx(), *d[:4], E, N, K, True, d[4], d[5], T, topk, out)
+        outs.append(out)
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
