@@ -1134,14 +1134,17 @@ bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
 
 bool float_type(int d) { return d == APMOE_F16 || d == APMOE_BF16 || d == APMOE_F32; }
 
+// Columns of an e4m3 matrix: 128 rows of it are addressed with a 31-bit offset.
+constexpr int kMaxCols8 = (1 << 24) - 128;
+
 // What the two products check alike; N: rows of one expert's matrix.
 apmoe_status fp8_args(const uint8_t *x8, const float *x_scale, const uint8_t *w8, const float *w_scale, int32_t E,
                       int32_t N, int32_t K, int32_t gather, const int32_t *perm, const int32_t *offsets, int32_t T,
                       int32_t topk)
 {
-    if (E < 1 || E > APMOE_MAX_EXPERTS || N < 1 || K < 16 || K % 16 != 0)
-        return fail(APMOE_INVALID_ARG, "E=%d N=%d K=%d (need 1 <= E <= %d, N >= 1, K%%16==0)", E, N, K,
-                    APMOE_MAX_EXPERTS);
+    if (E < 1 || E > APMOE_MAX_EXPERTS || N < 1 || K < 16 || K % 16 != 0 || K > kMaxCols8)
+        return fail(APMOE_INVALID_ARG, "E=%d N=%d K=%d (need 1 <= E <= %d, N >= 1, K%%16==0, 16 <= K <= %d)", E, N, K,
+                    APMOE_MAX_EXPERTS, kMaxCols8);
     if (T < 0 || topk < 1 || topk > APMOE_MAX_ASSIGN || (int64_t)T * topk > (int64_t)1 << 30)
         return fail(APMOE_INVALID_ARG, "T=%d topk=%d", T, topk);
     if (!offsets && E != 1)
@@ -1189,9 +1192,9 @@ apmoe_status fp8_layer_sizes(const apmoe_fp8_experts *ex, int32_t T, int32_t top
     if (!ex)
         return fail(APMOE_INVALID_ARG, "experts is NULL");
     if (ex->E < 1 || ex->E > APMOE_MAX_EXPERTS || ex->H < 16 || ex->H % 16 != 0 || ex->F < 16 || ex->F % 16 != 0 ||
-        ex->F > (1 << 30))
-        return fail(APMOE_INVALID_ARG, "E=%d H=%d F=%d (need 1 <= E <= %d, H%%16==0, F%%16==0)", ex->E, ex->H, ex->F,
-                    APMOE_MAX_EXPERTS);
+        ex->H > kMaxCols8 || ex->F > kMaxCols8)
+        return fail(APMOE_INVALID_ARG, "E=%d H=%d F=%d (need 1 <= E <= %d, multiples of 16 up to %d)", ex->E, ex->H,
+                    ex->F, APMOE_MAX_EXPERTS, kMaxCols8);
     if (n_shared < 0 || n_shared > APMOE_MAX_SHARED || n_shared >= ex->E)
         return fail(APMOE_INVALID_ARG, "n_shared=%d with %d experts", n_shared, ex->E);
     if (T < 0 || topk < 1 || topk > APMOE_MAX_TOPK || topk > ex->E - n_shared ||
@@ -1264,8 +1267,8 @@ apmoe_status apmoe_gemm_act_fp8(apmoe_ctx *ctx, const uint8_t *x8, const float *
 {
     if (!ctx)
         return fail(APMOE_INVALID_ARG, "ctx is NULL");
-    if (F < 16 || F % 16 != 0 || F > (1 << 30))
-        return fail(APMOE_INVALID_ARG, "F=%d (need F%%16==0)", F);
+    if (F < 16 || F % 16 != 0 || F > kMaxCols8)
+        return fail(APMOE_INVALID_ARG, "F=%d (need F%%16==0, F <= %d)", F, kMaxCols8);
     apmoe_status s = fp8_args(x8, x_scale, w8, w_scale, E, 2 * F, K, gather, perm, offsets, T, topk);
     if (s != APMOE_OK || T == 0)
         return s;

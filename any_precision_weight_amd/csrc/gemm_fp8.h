@@ -1,0 +1,76 @@
+// gemm_fp8.h -- what the e4m3 stream and tile products share (not installed).
+#pragma once
+
+#include "fp8.h"
+
+namespace apmoe {
+
+struct Fp8Params {
+    const uint8_t *x8;
+    const float *xs;
+    const uint8_t *w8;
+    const float *ws;
+    const int32_t *perm;
+    const int32_t *offsets;  // NULL: one expert with all R rows
+    void *out;               // product; a8 with the activation
+    float *os;               // scales of a8
+    int E, N, K, topk, gather, out_dtype, R;
+    int F;  // with the activation: N = 2 F
+};
+
+// Experts of at most kStreamMax rows take the stream product, the others the tile product.
+constexpr int kStreamMax = 32;
+
+__device__ inline void expert_rows(const Fp8Params &P, int e, int &r0, int &m)
+{
+    r0 = P.offsets ? P.offsets[e] : 0;
+    m = (P.offsets ? P.offsets[e + 1] : P.R) - r0;
+}
+
+__device__ inline size_t src_row(const Fp8Params &P, int r)
+{
+    return (size_t)(P.gather ? P.perm[r] / P.topk : r);
+}
+
+// SiLU(g) * u in fp32 (the hardware reciprocal, 1 ulp).
+__device__ inline float silu_mul32(float g, float u)
+{
+    return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+}
+
+// Four consecutive outputs of a row, those below N.
+__device__ inline void store4(const Fp8Params &P, size_t row, int n, const float4v &v)
+{
+    const size_t at = row * (size_t)P.N + n;
+    if (n + 4 <= P.N && P.N % 4 == 0) {
+        if (P.out_dtype == APMOE_F32) {
+            *reinterpret_cast<float4v *>(static_cast<float *>(P.out) + at) = v;
+        } else {
+            u32x2 o;
+            if (P.out_dtype == APMOE_F16) {
+                const half4 h = {(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
+                o = __builtin_bit_cast(u32x2, h);
+            } else {
+                o[0] = to_bf16(v[0]) | (uint32_t)to_bf16(v[1]) << 16;
+                o[1] = to_bf16(v[2]) | (uint32_t)to_bf16(v[3]) << 16;
+            }
+            *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(P.out) + at) = o;
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (n + i >= P.N)
+            break;
+        if (P.out_dtype == APMOE_F32)
+            static_cast<float *>(P.out)[at + i] = v[i];
+        else if (P.out_dtype == APMOE_F16)
+            static_cast<_Float16 *>(P.out)[at + i] = (_Float16)v[i];
+        else
+            static_cast<uint16_t *>(P.out)[at + i] = to_bf16(v[i]);
+    }
+}
+
+hipError_t launch_fp8_tile(const Fp8Params &P, bool act, bool exact, hipStream_t s);
+
+}  // namespace apmoe

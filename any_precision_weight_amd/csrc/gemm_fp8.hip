@@ -9,66 +9,11 @@
 // Stream product: weights go from HBM to the matrix units through registers, each
 // weight byte read once per 32 rows; a wave holds two 16-row weight tiles, kDepth
 // blocks ahead.  Bound by the weights' bytes.
+#include "gemm_fp8.h"
 #include "stream_fp8.h"
 
 namespace apmoe {
 namespace {
-
-struct Fp8Params {
-    const uint8_t *x8;
-    const float *xs;
-    const uint8_t *w8;
-    const float *ws;
-    const int32_t *perm;
-    const int32_t *offsets;  // NULL: one expert with all R rows
-    void *out;               // product; a8 with the activation
-    float *os;               // scales of a8
-    int E, N, K, topk, gather, out_dtype, R;
-    int F;  // with the activation: N = 2 F
-};
-
-__device__ inline void expert_rows(const Fp8Params &P, int e, int &r0, int &m)
-{
-    r0 = P.offsets ? P.offsets[e] : 0;
-    m = (P.offsets ? P.offsets[e + 1] : P.R) - r0;
-}
-
-__device__ inline size_t src_row(const Fp8Params &P, int r)
-{
-    return (size_t)(P.gather ? P.perm[r] / P.topk : r);
-}
-
-__device__ inline void store4(const Fp8Params &P, size_t row, int n, const float (&v)[4])
-{
-    const size_t at = row * (size_t)P.N + n;
-    if (n + 4 <= P.N && P.N % 4 == 0) {
-        if (P.out_dtype == APMOE_F32) {
-            *reinterpret_cast<float4v *>(static_cast<float *>(P.out) + at) = float4v{v[0], v[1], v[2], v[3]};
-        } else {
-            u32x2 o;
-            if (P.out_dtype == APMOE_F16) {
-                const half4 h = {(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
-                o = __builtin_bit_cast(u32x2, h);
-            } else {
-                o[0] = to_bf16(v[0]) | (uint32_t)to_bf16(v[1]) << 16;
-                o[1] = to_bf16(v[2]) | (uint32_t)to_bf16(v[3]) << 16;
-            }
-            *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(P.out) + at) = o;
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (n + i >= P.N)
-            break;
-        if (P.out_dtype == APMOE_F32)
-            static_cast<float *>(P.out)[at + i] = v[i];
-        else if (P.out_dtype == APMOE_F16)
-            static_cast<_Float16 *>(P.out)[at + i] = (_Float16)v[i];
-        else
-            static_cast<uint16_t *>(P.out)[at + i] = to_bf16(v[i]);
-    }
-}
 
 constexpr int kStreamWaves = 8;
 constexpr int kStreamRows = 32;  // weight rows of a wave
@@ -76,7 +21,7 @@ constexpr int kStreamRows = 32;  // weight rows of a wave
 // blockIdx.x: weight rows, blockIdx.y: expert.  KS waves share a wave's 32 rows, a KS-th
 // of the columns each; their sums meet in LDS in the order of the parts.
 template <int KS, int TT>
-__device__ __attribute__((always_inline)) inline void stream_tokens(const Fp8Params &P, int e, int r0, int m0, int m,
+__device__ __attribute__((always_inline)) inline void stream_tokens(const Fp8Params &P, int e, int r0, int m,
                                                                    float *red)
 {
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
@@ -97,7 +42,7 @@ __device__ __attribute__((always_inline)) inline void stream_tokens(const Fp8Par
     }
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
-        const size_t row = src_row(P, r0 + min(m0 + 16 * t + j, m - 1));
+        const size_t row = src_row(P, r0 + min(16 * t + j, m - 1));
         xr[t] = P.x8 + row * P.K + 16 * g;
         xsc[t] = P.xs + row * KB;
     }
@@ -110,7 +55,6 @@ __device__ __attribute__((always_inline)) inline void stream_tokens(const Fp8Par
     const int per = (KB + KS - 1) / KS;
     stream_product<2, TT>(wr, wsc, xr, xsc, kp * per, min(KB, (kp + 1) * per), P.K, 16 * g, acc);
     if constexpr (KS > 1) {
-        __syncthreads();  // the sums of an earlier token chunk are read
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -129,16 +73,14 @@ __device__ __attribute__((always_inline)) inline void stream_tokens(const Fp8Par
     }
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
-        const int tok = m0 + 16 * t + j;
+        const int tok = 16 * t + j;
         if (tok >= m)
             continue;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int n = n0 + 16 * r + 4 * g;
-            if (n < P.N) {
-                const float v[4] = {acc[r][t][0], acc[r][t][1], acc[r][t][2], acc[r][t][3]};
-                store4(P, (size_t)(r0 + tok), n, v);
-            }
+            if (n < P.N)
+                store4(P, (size_t)(r0 + tok), n, acc[r][t]);
         }
     }
 }
@@ -150,19 +92,19 @@ __global__ void __launch_bounds__(kStreamWaves *kWave) stream_kernel(const Fp8Pa
     const int e = blockIdx.y;
     int r0, m;
     expert_rows(P, e, r0, m);
-    for (int m0 = 0; m0 < m; m0 += 32) {
-        if (m - m0 <= 16)
-            stream_tokens<KS, 1>(P, e, r0, m0, m, red);
-        else
-            stream_tokens<KS, 2>(P, e, r0, m0, m, red);
-    }
+    if (m > kStreamMax)
+        return;  // the tile product's
+    if (m > 16)
+        stream_tokens<KS, 2>(P, e, r0, m, red);
+    else if (m > 0)
+        stream_tokens<KS, 1>(P, e, r0, m, red);
 }
 
 // gate_up: wave w holds 16 gate rows and the 16 matching up rows, the workgroup the 128
 // + 128 rows behind one group of 128 values of a8, whose scale needs all of them.
 template <int TT>
-__device__ __attribute__((always_inline)) inline void stream_act_tokens(const Fp8Params &P, int e, int r0, int m0,
-                                                                       int m, uint32_t *amax)
+__device__ __attribute__((always_inline)) inline void stream_act_tokens(const Fp8Params &P, int e, int r0, int m,
+                                                                       uint32_t *amax)
 {
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     const int j = lane & 15, g = lane >> 4;
@@ -178,7 +120,7 @@ __device__ __attribute__((always_inline)) inline void stream_act_tokens(const Fp
     }
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
-        const size_t row = src_row(P, r0 + min(m0 + 16 * t + j, m - 1));
+        const size_t row = src_row(P, r0 + min(16 * t + j, m - 1));
         xr[t] = P.x8 + row * P.K + 16 * g;
         xsc[t] = P.xs + row * KB;
     }
@@ -212,7 +154,7 @@ __device__ __attribute__((always_inline)) inline void stream_act_tokens(const Fp
         for (int v = 0; v < kStreamWaves; ++v)
             mx = max(mx, amax[(v * 2 + t) * 16 + j]);
         const float s = scale_of(mx), inv = 1.0f / s;
-        const int tok = m0 + 16 * t + j;
+        const int tok = 16 * t + j;
         if (tok < m && fw + 4 * g < P.F) {  // F is a multiple of 16
             const size_t row = (size_t)(r0 + tok);
             *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(P.out) + row * P.F + fw + 4 * g) =
@@ -221,7 +163,6 @@ __device__ __attribute__((always_inline)) inline void stream_act_tokens(const Fp
                 P.os[row * fb + blockIdx.x] = s;
         }
     }
-    __syncthreads();  // amax is read
 }
 
 __global__ void __launch_bounds__(kStreamWaves *kWave) stream_act_kernel(const Fp8Params P)
@@ -230,12 +171,12 @@ __global__ void __launch_bounds__(kStreamWaves *kWave) stream_act_kernel(const F
     const int e = blockIdx.y;
     int r0, m;
     expert_rows(P, e, r0, m);
-    for (int m0 = 0; m0 < m; m0 += 32) {
-        if (m - m0 <= 16)
-            stream_act_tokens<1>(P, e, r0, m0, m, amax);
-        else
-            stream_act_tokens<2>(P, e, r0, m0, m, amax);
-    }
+    if (m > kStreamMax)
+        return;  // the tile product's
+    if (m > 16)
+        stream_act_tokens<2>(P, e, r0, m, amax);
+    else if (m > 0)
+        stream_act_tokens<1>(P, e, r0, m, amax);
 }
 
 }  // namespace
@@ -248,7 +189,9 @@ hipError_t launch_gemm_fp8(const uint8_t *x8, const float *xs, const uint8_t *w8
     constexpr int KS = 4;
     const int rows = kStreamWaves / KS * kStreamRows;
     hipLaunchKernelGGL((stream_kernel<KS>), dim3((N + rows - 1) / rows, E), dim3(kStreamWaves * kWave), 0, s, P);
-    return hipGetLastError();
+    // fp32 results keep fp32 sums (block_product)
+    const hipError_t e = launch_fp8_tile(P, false, out_dtype == APMOE_F32, s);
+    return e == hipSuccess ? hipGetLastError() : e;
 }
 
 hipError_t launch_gemm_act_fp8(const uint8_t *x8, const float *xs, const uint8_t *w8, const float *ws, int E, int F,
@@ -257,7 +200,8 @@ hipError_t launch_gemm_act_fp8(const uint8_t *x8, const float *xs, const uint8_t
 {
     const Fp8Params P{x8, xs, w8, ws, perm, offsets, a8, as, E, 2 * F, K, topk, gather, 0, R, F};
     hipLaunchKernelGGL(stream_act_kernel, dim3((F + kBlk - 1) / kBlk, E), dim3(kStreamWaves * kWave), 0, s, P);
-    return hipGetLastError();
+    const hipError_t e = launch_fp8_tile(P, true, true, s);
+    return e == hipSuccess ? hipGetLastError() : e;
 }
 
 }  // namespace apmoe

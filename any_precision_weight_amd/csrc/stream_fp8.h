@@ -8,12 +8,6 @@ namespace apmoe {
 
 constexpr int kDepth = 4;  // column blocks requested ahead
 
-// SiLU(g) * u in fp32 (the hardware reciprocal, 1 ulp).
-__device__ inline float silu_mul32(float g, float u)
-{
-    return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
-}
-
 template <int NR, int TT>
 struct StreamStage {
     Frag8 a[NR], b[TT];

@@ -473,15 +473,18 @@ apmoe_status apmoe_norm(apmoe_ctx *ctx, const void *x, int32_t x_dtype, const vo
  * offsets[e+1]) of the output:
  *   out[r][n] = sum_b x_scale[s][b] * w_scale[e][n/128][b] *
  *               sum_{c in 128-column block b} x8[s][c] * w8[e][n][c],
- * s = perm[r] / topk when gather != 0, else r; fp32 accumulation, each block's sum
- * scaled in fp32.
+ * s = perm[r] / topk when gather != 0, else r; each block's sum is scaled and added in
+ * fp32.  The sum inside a block is an fp32 one, except for experts of more than 32 rows
+ * with a 16-bit out: there it comes from the e4m3 matrix instruction, which cuts a
+ * product off at 2^-13 of the largest one among 8 neighbours (1.5e-5 of the result in
+ * norm for normally distributed operands, at most 2^-10 of the sum of the magnitudes).
  *   x8 e4m3 [T][K] (gather) or [T*topk][K], x_scale fp32 [rows][ceil(K/128)];
  *   w8 e4m3 [E][N][K], w_scale fp32 [E][ceil(N/128)][ceil(K/128)];
  *   out [T*topk][N] of out_dtype (APMOE_F16, APMOE_BF16, APMOE_F32), RNE.
  * perm and offsets as apmoe_route writes them; rows of the output at or past
  * offsets[E] are not written.  A dense product is E = 1, topk = 1 with offsets NULL
  * (every row is the one expert's) and gather = 0.
- * Limits: 1 <= E <= 256, N >= 1, K % 16 == 0, K >= 16, 1 <= topk <= 16, T >= 0,
+ * Limits: 1 <= E <= 256, N >= 1, K % 16 == 0, 16 <= K < 2^24, 1 <= topk <= 16, T >= 0,
  * T * topk <= 2^30.  Errors (nothing enqueued): INVALID_ARG for NULL or misaligned
  * pointers (16 bytes; scales, perm and offsets 4), offsets NULL with E > 1, or bad
  * sizes; UNSUPPORTED for another out_dtype.
@@ -499,7 +502,7 @@ apmoe_status apmoe_gemm_fp8(apmoe_ctx *ctx, const uint8_t *x8, const float *x_sc
  *   [E][2][ceil(F/128)][ceil(K/128)]: each half has blocks of its own (the layout of a
  *   [2F][K] matrix where F % 128 == 0);
  *   a8 e4m3 [T*topk][F], a_scale fp32 [T*topk][ceil(F/128)].
- * F % 16 == 0, F >= 16; other arguments, limits and errors as apmoe_gemm_fp8.
+ * F % 16 == 0, 16 <= F < 2^24; other arguments, limits and errors as apmoe_gemm_fp8.
  */
 apmoe_status apmoe_gemm_act_fp8(apmoe_ctx *ctx, const uint8_t *x8, const float *x_scale, const uint8_t *w8,
                                 const float *w_scale, int32_t E, int32_t F, int32_t K, int32_t gather,
@@ -509,7 +512,7 @@ apmoe_status apmoe_gemm_act_fp8(apmoe_ctx *ctx, const uint8_t *x8, const float *
 /* The experts of one layer in e4m3: E of them (the routed ones, then the shared ones),
  * gate_up [E][2F][H] with scales [E][2][ceil(F/128)][ceil(H/128)], down [E][H][F] with
  * scales [E][ceil(H/128)][ceil(F/128)]; device memory, caller-owned.  H and F are
- * multiples of 16. */
+ * multiples of 16 below 2^24. */
 typedef struct apmoe_fp8_experts {
     int32_t E;
     int32_t H;

@@ -49,7 +49,7 @@ def gemm_args(**kw):
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(ctx=None), 1), (dict(E=0), 1), (dict(E=257), 1), (dict(N=0), 1), (dict(K=0), 1), (dict(K=24), 1),
+    (dict(ctx=None), 1), (dict(E=0), 1), (dict(E=257), 1), (dict(N=0), 1), (dict(K=0), 1), (dict(K=24), 1), (dict(K=1 << 24), 1),
     (dict(T=-1), 1), (dict(topk=0), 1), (dict(topk=17), 1), (dict(T=1 << 30, topk=2), 1), (dict(offsets=None), 1),
     (dict(perm=None), 1), (dict(x8=None), 1), (dict(xs=None), 1), (dict(w8=None), 1), (dict(ws=None), 1),
     (dict(out=None), 1), (dict(x8=A + 8), 1), (dict(w8=A + 4), 1), (dict(xs=A + 2), 1), (dict(ws=A + 1), 1),
