@@ -83,7 +83,7 @@ __device__ __attribute__((always_inline)) inline void route_token(const uint16_t
             const int e = i * kWave + lane;
             if (taken & (1u << i))
                 continue;
-            const double z = zs[e];
+            const double z = zs[e] == zs[e] ? zs[e] : -INFINITY;  // a NaN compares as the lowest
             if (be == 0x7FFFFFFF || better(z, e, bz, be)) {
                 bz = z;
                 be = e;

@@ -387,7 +387,8 @@ LAYERS = [  # T, E, topk, shared, H, F, renorm, bias
     (1, 4, 2, 0, 256, 512, True, False), (1, 1, 1, 0, 16, 16, True, False), (1, 12, 4, 2, 272, 144, False, True),
     (2, 8, 2, 1, 528, 400, True, True), (3, 60, 8, 4, 256, 208, False, False), (4, 5, 5, 0, 400, 272, True, True),
     (7, 3, 2, 8, 144, 704, False, False), (16, 8, 2, 0, 384, 256, True, False), (17, 8, 2, 1, 384, 256, True, False),
-    (33, 6, 3, 0, 272, 272, False, True), (100, 4, 2, 1, 256, 384, True, True), (16, 200, 8, 1, 128, 64, True, False)]
+    (33, 6, 3, 0, 272, 272, False, True), (100, 4, 2, 1, 256, 384, True, True), (16, 200, 8, 1, 128, 64, True, False), (1, 256, 8, 0, 64, 48, False, True), (4, 248, 8, 8, 80, 16, True, True),
+    (16, 8, 8, 8, 64, 272, True, False), (1, 8, 2, 0, 2048, 4096, True, False), (3, 6, 2, 0, 1040, 2064, False, True)]
 
 
 def run_layer(d, bias, E, n_shared, H, F, T, topk, renorm, stream=None):
@@ -411,6 +412,44 @@ def test_layer(T, E, topk, shared, H, F, renorm, has_bias):
     got, _ = run_layer(d, bias, E, shared, H, F, T, topk, renorm)
     err = np.abs(got - want)
     assert np.all(err <= bound), float((err / bound).max())
+
+
+@pytest.mark.parametrize("T", [5, 300])
+def test_route_with_a_nan_token(T):
+    """A token whose logits are all NaN still gets distinct experts (the lowest ones), so
+    that perm and inv_perm are permutations; its weights are NaN, the others' are not."""
+    r = rng_of("route-nan", T)
+    H, E, topk = 64, 6, 2
+    x = r.normal(size=(T, H)).astype(np.float16)
+    x[T // 2, 5] = np.nan
+    wr = r.normal(size=(E, H)).astype(np.float16)
+    ids, perm, inv = (torch.full((T * topk,), -1, dtype=torch.int32, device="cuda") for _ in range(3))
+    w = torch.empty((T, topk), device="cuda")
+    counts, offsets = (torch.empty(n, dtype=torch.int32, device="cuda") for n in (E, E + 1))
+    apw.route(ctx(), cuda(x), cuda(wr), None, T, H, E, topk, True, ids, w, counts, offsets, perm, inv)
+    torch.cuda.synchronize()
+    ids, w = ids.view(T, topk).cpu().numpy(), w.cpu().numpy()
+    assert ids[T // 2].tolist() == [0, 1]
+    assert np.isnan(w[T // 2]).all() and np.isfinite(np.delete(w, T // 2, axis=0)).all()
+    for p in (perm, inv):
+        assert np.array_equal(np.sort(p.cpu().numpy()), np.arange(T * topk))
+    assert int(offsets[-1]) == T * topk
+
+
+@pytest.mark.parametrize("T", [1, 3, 20])
+def test_layer_with_a_nan_token(T):
+    """A NaN in one token leaves the other tokens' outputs as they are."""
+    r = rng_of("nan-token", T)
+    E, topk, shared, H, F = 6, 2, 1, 272, 144
+    d = layer_inputs(r, E, shared, H, F, T + 1)
+    d["x"][T, 3] = np.nan
+    d["x8"][T, 3] = 0x7F
+    got, _ = run_layer(d, None, E, shared, H, F, T + 1, topk, True)
+    assert np.isnan(got[T]).all()
+    for k in ("x", "x8", "xs"):
+        d[k] = d[k][:T]
+    want, bound = layer_ref(d, None, E, shared, H, F, T, topk, True)
+    assert np.all(np.abs(got[:T] - want) <= bound)
 
 
 @pytest.mark.parametrize("T", [1, 4, 16, 20])
