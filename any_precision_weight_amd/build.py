@@ -21,7 +21,8 @@ SAFE_LIB = os.path.join(PKG, "libapmoe_safe.so")
 # a plain HBM read stream for the benchmark's ceiling (not part of the layer)
 PROBE_SRC = "hbm_probe.hip"
 PROBE_LIB = os.path.join(PKG, "libhbmprobe.so")
-SOURCES = ["api.hip", "route.hip", "gemm.hip", "gemm_tile.hip", "elementwise.hip", "norm.hip", "gemm_fp8.hip", "gemm_fp8_tile.hip"]
+SOURCES = ["api.hip", "route.hip", "gemm.hip", "gemm_tile.hip", "elementwise.hip", "norm.hip", "gemm_fp8.hip", "gemm_fp8_tile.hip",
+           "layer_fp8.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

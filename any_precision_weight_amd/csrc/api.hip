@@ -16,6 +16,7 @@
 #include <vector>
 
 #include "internal.h"
+#include "layer_fp8.h"
 
 using apmoe::DevBlock;
 
@@ -1160,7 +1161,7 @@ apmoe_status fp8_args(const uint8_t *x8, const float *x_scale, const uint8_t *w8
 }
 
 struct WsLayout8 {
-    size_t ids, w, counts, offsets, perm, inv_perm, a8, as, y, total;
+    size_t ids, w, counts, offsets, perm, inv_perm, a8, as, y, z, total;
 };
 
 WsLayout8 ws_layout8(int T, int kt, int E, int H, int F)
@@ -1181,7 +1182,10 @@ WsLayout8 ws_layout8(int T, int kt, int E, int H, int F)
     L.inv_perm = take(R * 4);
     L.a8 = take(R * F);
     L.as = take(R * ((F + 127) / 128) * 4);
-    L.y = take(R * H * 4);
+    // few tokens: the logits, and the activation in fp32 in y's place
+    const bool few = T <= apmoe::kFewTokens;
+    L.y = take(R * (few && F > H ? F : H) * 4);
+    L.z = take(few ? (size_t)T * E * 8 : 0);
     L.total = o;
     return L;
 }
@@ -1329,11 +1333,18 @@ apmoe_status apmoe_moe_forward_fp8(apmoe_ctx *ctx, const apmoe_fp8_experts *ex, 
     OnDevice dev(ctx);
     if (dev.status() != APMOE_OK)
         return dev.status();
+    hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+    if (apmoe::few_layer_fits(T, E - n_shared)) {
+        const apmoe::FewParams p{x, x8, x_scale, w_router, bias, ex->gate_up, ex->gate_up_scale, ex->down,
+                                 ex->down_scale, T, topk, kt, E - n_shared, H, F, renormalize,
+                                 reinterpret_cast<double *>(w + L.z), ids, tw, a8, as, y, out, 0};
+        const hipError_t few = apmoe::launch_few_layer(p, st);
+        return few == hipSuccess ? ok() : hip_fail(few, "few-token layer launch");
+    }
     s = apmoe_route(ctx, x, w_router, bias, T, H, E - n_shared, topk, n_shared, renormalize, ids, tw, counts, offsets,
                     perm, inv, stream);
     if (s != APMOE_OK)
         return s;
-    hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     hipError_t e = apmoe::launch_gemm_act_fp8(x8, x_scale, ex->gate_up, ex->gate_up_scale, E, F, H, 1, perm, offsets,
                                               kt, T * kt, a8, as, st);
     if (e == hipSuccess)

@@ -15,6 +15,7 @@
 namespace apmoe {
 namespace {
 
+constexpr int kDepth = 2;  // column blocks requested ahead
 constexpr int kStreamWaves = 8;
 constexpr int kStreamRows = 32;  // weight rows of a wave
 
@@ -24,21 +25,26 @@ template <int KS, int TT>
 __device__ __attribute__((always_inline)) inline void stream_tokens(const Fp8Params &P, int e, int r0, int m,
                                                                    float *red)
 {
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int j = lane & 15, g = lane >> 4;
+    const uint32_t woff = 16u * line_chunk(j, g);
     const int kp = wave % KS;
     const int n0 = ((int)blockIdx.x * (kStreamWaves / KS) + wave / KS) * kStreamRows;
     const int KB = (P.K + kBlk - 1) / kBlk;
-    const uint8_t *w = P.w8 + (size_t)e * P.N * P.K;
+    // weight rows past the last repeat it; nothing of them is stored
+    const int nl = P.N - 1;
     const int nb = (P.N + kBlk - 1) / kBlk;
     const float *sc = P.ws + (size_t)e * nb * KB;
-    const uint8_t *wr[2], *xr[TT];
+    const uint8_t *wbase[2], *xr[TT];
+    uint32_t wo[2][2];
     const float *wsc[2], *xsc[TT];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-        const int n = min(n0 + 16 * r + j, P.N - 1);
-        wr[r] = w + (size_t)n * P.K + 16 * g;
-        wsc[r] = sc + (size_t)(min(n0 + 16 * r, P.N - 1) / kBlk) * KB;
+        const int nr = min(n0 + 16 * r, nl);
+        wbase[r] = P.w8 + ((size_t)e * P.N + nr) * P.K;
+        wo[r][0] = (uint32_t)min(j % 8, nl - nr) * (uint32_t)P.K + woff;
+        wo[r][1] = (uint32_t)min(8 + j % 8, nl - nr) * (uint32_t)P.K + woff;
+        wsc[r] = sc + (size_t)(nr / kBlk) * KB;
     }
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
@@ -53,7 +59,7 @@ __device__ __attribute__((always_inline)) inline void stream_tokens(const Fp8Par
         for (int t = 0; t < TT; ++t)
             acc[r][t] = float4v{0.f, 0.f, 0.f, 0.f};
     const int per = (KB + KS - 1) / KS;
-    stream_product<2, TT>(wr, wsc, xr, xsc, kp * per, min(KB, (kp + 1) * per), P.K, 16 * g, acc);
+    stream_product<2, TT, kDepth>(wbase, wo, wsc, xr, xsc, kp * per, min(KB, (kp + 1) * per), P.K, 16 * g, (int)woff, 4 * wave + (int)blockIdx.x, acc);
     if constexpr (KS > 1) {
 #pragma unroll
         for (int r = 0; r < 2; ++r)
@@ -85,16 +91,16 @@ __device__ __attribute__((always_inline)) inline void stream_tokens(const Fp8Par
     }
 }
 
-template <int KS>
-__global__ void __launch_bounds__(kStreamWaves *kWave) stream_kernel(const Fp8Params P)
+template <int KS, int TT>
+__global__ void __launch_bounds__(kStreamWaves *kWave, TT == 1 ? 4 : 2) stream_kernel(const Fp8Params P)
 {
-    __shared__ __attribute__((aligned(16))) float red[KS > 1 ? kStreamWaves * 2 * 2 * 256 : 4];
+    __shared__ __attribute__((aligned(16))) float red[KS > 1 ? kStreamWaves * 2 * TT * 256 : 4];
     const int e = blockIdx.y;
     int r0, m;
     expert_rows(P, e, r0, m);
     if (m > kStreamMax)
         return;  // the tile product's
-    if (m > 16)
+    if (TT == 2 && m > 16)
         stream_tokens<KS, 2>(P, e, r0, m, red);
     else if (m > 0)
         stream_tokens<KS, 1>(P, e, r0, m, red);
@@ -106,16 +112,20 @@ template <int TT>
 __device__ __attribute__((always_inline)) inline void stream_act_tokens(const Fp8Params &P, int e, int r0, int m,
                                                                        uint32_t *amax)
 {
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int j = lane & 15, g = lane >> 4;
+    const uint32_t woff = 16u * line_chunk(j, g);
     const int f0 = (int)blockIdx.x * kBlk, fw = f0 + 16 * wave;
     const int KB = (P.K + kBlk - 1) / kBlk, fb = (P.F + kBlk - 1) / kBlk;
-    const uint8_t *w = P.w8 + (size_t)e * P.N * P.K;
-    const uint8_t *wr[2], *xr[TT];
+    const int fc = min(fw, P.F - 16);  // F is a multiple of 16
+    const uint8_t *wbase[2], *xr[TT];
+    uint32_t wo[2][2];
     const float *wsc[2], *xsc[TT];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        wr[h] = w + (size_t)(h * P.F + min(fw + j, P.F - 1)) * P.K + 16 * g;
+        wbase[h] = P.w8 + ((size_t)e * P.N + (size_t)h * P.F + fc) * P.K;
+        wo[h][0] = (uint32_t)(j % 8) * (uint32_t)P.K + woff;
+        wo[h][1] = (uint32_t)(8 + j % 8) * (uint32_t)P.K + woff;
         wsc[h] = P.ws + ((size_t)(2 * e + h) * fb + blockIdx.x) * KB;
     }
 #pragma unroll
@@ -130,7 +140,7 @@ __device__ __attribute__((always_inline)) inline void stream_act_tokens(const Fp
 #pragma unroll
         for (int t = 0; t < TT; ++t)
             acc[h][t] = float4v{0.f, 0.f, 0.f, 0.f};
-    stream_product<2, TT>(wr, wsc, xr, xsc, 0, KB, P.K, 16 * g, acc);
+    stream_product<2, TT, kDepth>(wbase, wo, wsc, xr, xsc, 0, KB, P.K, 16 * g, (int)woff, 4 * wave + (int)blockIdx.x, acc);
     float a[TT][4];
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
@@ -165,7 +175,8 @@ __device__ __attribute__((always_inline)) inline void stream_act_tokens(const Fp
     }
 }
 
-__global__ void __launch_bounds__(kStreamWaves *kWave) stream_act_kernel(const Fp8Params P)
+template <int TT>
+__global__ void __launch_bounds__(kStreamWaves *kWave, TT == 1 ? 4 : 2) stream_act_kernel(const Fp8Params P)
 {
     __shared__ uint32_t amax[kStreamWaves * 2 * 16];
     const int e = blockIdx.y;
@@ -173,7 +184,7 @@ __global__ void __launch_bounds__(kStreamWaves *kWave) stream_act_kernel(const F
     expert_rows(P, e, r0, m);
     if (m > kStreamMax)
         return;  // the tile product's
-    if (m > 16)
+    if (TT == 2 && m > 16)
         stream_act_tokens<2>(P, e, r0, m, amax);
     else if (m > 0)
         stream_act_tokens<1>(P, e, r0, m, amax);
@@ -186,9 +197,27 @@ hipError_t launch_gemm_fp8(const uint8_t *x8, const float *xs, const uint8_t *w8
                            int out_dtype, hipStream_t s)
 {
     const Fp8Params P{x8, xs, w8, ws, perm, offsets, out, nullptr, E, N, K, topk, gather, out_dtype, R, 0};
-    constexpr int KS = 4;
-    const int rows = kStreamWaves / KS * kStreamRows;
-    hipLaunchKernelGGL((stream_kernel<KS>), dim3((N + rows - 1) / rows, E), dim3(kStreamWaves * kWave), 0, s, P);
+    // No expert has more than R / topk rows.  KS: enough waves to fill the device, 8 on a CU.
+    const int active = E < R ? E : R;
+    const long waves = (long)active * ((N + kStreamRows - 1) / kStreamRows);
+    const int KB = (K + kBlk - 1) / kBlk;
+    auto go = [&](auto ks) {
+        constexpr int KS = decltype(ks)::value;
+        const int rows = kStreamWaves / KS * kStreamRows;
+        const dim3 grid((N + rows - 1) / rows, E), block(kStreamWaves * kWave);
+        if (R / topk > 16)
+            hipLaunchKernelGGL((stream_kernel<KS, 2>), grid, block, 0, s, P);
+        else
+            hipLaunchKernelGGL((stream_kernel<KS, 1>), grid, block, 0, s, P);
+    };
+    if (waves >= 2048 || KB < 4)
+        go(std::integral_constant<int, 1>{});
+    else if (waves >= 1024 || KB < 8)
+        go(std::integral_constant<int, 2>{});
+    else if (waves >= 512 || KB < 16)
+        go(std::integral_constant<int, 4>{});
+    else
+        go(std::integral_constant<int, 8>{});
     // fp32 results keep fp32 sums (block_product)
     const hipError_t e = launch_fp8_tile(P, false, out_dtype == APMOE_F32, s);
     return e == hipSuccess ? hipGetLastError() : e;
@@ -199,7 +228,11 @@ hipError_t launch_gemm_act_fp8(const uint8_t *x8, const float *xs, const uint8_t
                                uint8_t *a8, float *as, hipStream_t s)
 {
     const Fp8Params P{x8, xs, w8, ws, perm, offsets, a8, as, E, 2 * F, K, topk, gather, 0, R, F};
-    hipLaunchKernelGGL(stream_act_kernel, dim3((F + kBlk - 1) / kBlk, E), dim3(kStreamWaves * kWave), 0, s, P);
+    const dim3 grid((F + kBlk - 1) / kBlk, E), block(kStreamWaves * kWave);
+    if (R / topk > 16)
+        hipLaunchKernelGGL((stream_act_kernel<2>), grid, block, 0, s, P);
+    else
+        hipLaunchKernelGGL((stream_act_kernel<1>), grid, block, 0, s, P);
     const hipError_t e = launch_fp8_tile(P, true, true, s);
     return e == hipSuccess ? hipGetLastError() : e;
 }
