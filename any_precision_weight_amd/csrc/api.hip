@@ -1260,7 +1260,8 @@ apmoe_status apmoe_gemm_fp8(apmoe_ctx *ctx, const uint8_t *x8, const float *x_sc
     if (dev.status() != APMOE_OK)
         return dev.status();
     hipError_t e = apmoe::launch_gemm_fp8(x8, x_scale, w8, w_scale, E, N, K, gather, perm, offsets, topk, T * topk,
-                                          out, out_dtype, reinterpret_cast<hipStream_t>(stream));
+                                          out, out_dtype, out_dtype == APMOE_F32,
+                                          reinterpret_cast<hipStream_t>(stream));
     return e == hipSuccess ? ok() : hip_fail(e, "gemm_fp8 launch");
 }
 
@@ -1334,7 +1335,7 @@ apmoe_status apmoe_moe_forward_fp8(apmoe_ctx *ctx, const apmoe_fp8_experts *ex, 
     if (dev.status() != APMOE_OK)
         return dev.status();
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-    if (apmoe::few_layer_fits(T, E - n_shared)) {
+    if (apmoe::few_layer_fits(T, kt, E - n_shared, F)) {
         const apmoe::FewParams p{x, x8, x_scale, w_router, bias, ex->gate_up, ex->gate_up_scale, ex->down,
                                  ex->down_scale, T, topk, kt, E - n_shared, H, F, renormalize,
                                  reinterpret_cast<double *>(w + L.z), ids, tw, a8, as, y, out, 0};
@@ -1349,7 +1350,7 @@ apmoe_status apmoe_moe_forward_fp8(apmoe_ctx *ctx, const apmoe_fp8_experts *ex, 
                                               kt, T * kt, a8, as, st);
     if (e == hipSuccess)
         e = apmoe::launch_gemm_fp8(a8, as, ex->down, ex->down_scale, E, H, F, 0, perm, offsets, kt, T * kt, y,
-                                   APMOE_F32, st);
+                                   APMOE_F32, false, st);  // out is rounded to fp16 at once
     if (e == hipSuccess)
         e = apmoe::launch_combine(y, 1, tw, inv, T, kt, H, out, st);
     return e == hipSuccess ? ok() : hip_fail(e, "fp8 layer launch");

@@ -71,6 +71,11 @@ __device__ inline void store4(const Fp8Params &P, size_t row, int n, const float
     }
 }
 
-hipError_t launch_fp8_tile(const Fp8Params &P, bool act, bool exact, hipStream_t s);
+// Rows that an expert can have: a token's experts are distinct, so one for each token;
+// a single expert has every row.
+inline int most_rows(const Fp8Params &P) { return P.E == 1 ? P.R : P.R / P.topk; }
+
+// exact: fp32 sums inside a block (block_product), which fp32 results keep.
+hipError_t launch_fp8_tile(const Fp8Params &P, int most, bool act, bool exact, hipStream_t s);
 
 }  // namespace apmoe

@@ -194,10 +194,11 @@ __global__ void __launch_bounds__(kStreamWaves *kWave, TT == 1 ? 4 : 2) stream_a
 
 hipError_t launch_gemm_fp8(const uint8_t *x8, const float *xs, const uint8_t *w8, const float *ws, int E, int N, int K,
                            int gather, const int32_t *perm, const int32_t *offsets, int topk, int R, void *out,
-                           int out_dtype, hipStream_t s)
+                           int out_dtype, bool exact, hipStream_t s)
 {
     const Fp8Params P{x8, xs, w8, ws, perm, offsets, out, nullptr, E, N, K, topk, gather, out_dtype, R, 0};
-    // No expert has more than R / topk rows.  KS: enough waves to fill the device, 8 on a CU.
+    const int most = most_rows(P);
+    // KS: enough waves to fill the device, 8 on a CU.
     const int active = E < R ? E : R;
     const long waves = (long)active * ((N + kStreamRows - 1) / kStreamRows);
     const int KB = (K + kBlk - 1) / kBlk;
@@ -205,7 +206,7 @@ hipError_t launch_gemm_fp8(const uint8_t *x8, const float *xs, const uint8_t *w8
         constexpr int KS = decltype(ks)::value;
         const int rows = kStreamWaves / KS * kStreamRows;
         const dim3 grid((N + rows - 1) / rows, E), block(kStreamWaves * kWave);
-        if (R / topk > 16)
+        if (most > 16)
             hipLaunchKernelGGL((stream_kernel<KS, 2>), grid, block, 0, s, P);
         else
             hipLaunchKernelGGL((stream_kernel<KS, 1>), grid, block, 0, s, P);
@@ -218,8 +219,7 @@ hipError_t launch_gemm_fp8(const uint8_t *x8, const float *xs, const uint8_t *w8
         go(std::integral_constant<int, 4>{});
     else
         go(std::integral_constant<int, 8>{});
-    // fp32 results keep fp32 sums (block_product)
-    const hipError_t e = launch_fp8_tile(P, false, out_dtype == APMOE_F32, s);
+    const hipError_t e = launch_fp8_tile(P, most, false, exact, s);
     return e == hipSuccess ? hipGetLastError() : e;
 }
 
@@ -229,11 +229,12 @@ hipError_t launch_gemm_act_fp8(const uint8_t *x8, const float *xs, const uint8_t
 {
     const Fp8Params P{x8, xs, w8, ws, perm, offsets, a8, as, E, 2 * F, K, topk, gather, 0, R, F};
     const dim3 grid((F + kBlk - 1) / kBlk, E), block(kStreamWaves * kWave);
-    if (R / topk > 16)
+    const int most = most_rows(P);
+    if (most > 16)
         hipLaunchKernelGGL((stream_act_kernel<2>), grid, block, 0, s, P);
     else
         hipLaunchKernelGGL((stream_act_kernel<1>), grid, block, 0, s, P);
-    const hipError_t e = launch_fp8_tile(P, true, true, s);
+    const hipError_t e = launch_fp8_tile(P, most, true, true, s);
     return e == hipSuccess ? hipGetLastError() : e;
 }
 

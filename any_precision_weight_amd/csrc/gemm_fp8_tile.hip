@@ -298,8 +298,10 @@ __global__ void __launch_bounds__(kThreads) fp8_tile_kernel(const TileParams T)
 
 }  // namespace
 
-hipError_t launch_fp8_tile(const Fp8Params &P, bool act, bool exact, hipStream_t s)
+hipError_t launch_fp8_tile(const Fp8Params &P, int most, bool act, bool exact, hipStream_t s)
 {
+    if (most <= kStreamMax)
+        return hipSuccess;
     // token tiles: at most one per started kMaxTok rows of an expert with more than kStreamMax
     const int served = P.E < P.R / (kStreamMax + 1) ? P.E : P.R / (kStreamMax + 1);
     if (served == 0)

@@ -49,8 +49,11 @@ inline bool few_quantises_late(int T, int topk, int kt, int Er, int F)
 }
 
 // The selection compares every expert of a token with every other: at most this many
-// comparisons (512 threads share them).
-inline bool few_layer_fits(int T, int Er) { return T <= kFewTokens && (long)T * Er * Er <= 256 * 1024; }
+// comparisons (512 threads share them).  few_down holds the activation's scales in LDS.
+inline bool few_layer_fits(int T, int kt, int Er, int F)
+{
+    return T <= kFewTokens && (long)T * Er * Er <= 256 * 1024 && (long)T * kt * 4 * ((F + 127) / 128) <= kFewRows8;
+}
 
 hipError_t launch_few_layer(FewParams P, hipStream_t s);
 

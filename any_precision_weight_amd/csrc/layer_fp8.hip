@@ -241,6 +241,7 @@ __global__ void __launch_bounds__(NW *kWave) few_gate_up(const FewParams P)
 struct DownStage {
     Frag8 a, b;
     float sw, f;
+    bool chosen, lo, hi;  // whether the token chose the expert; whether b.lo / b.hi are its columns
 };
 
 // blockIdx.x: 16 columns of the output.  QUANT: a32 is quantised into LDS first.
@@ -283,10 +284,14 @@ __global__ void __launch_bounds__(kThreads) few_down(const FewParams P)
         list[place(tid)] = tid;
     for (int i = tid; i < R; i += kThreads)
         rows[place(P.ids[i])][i / P.kt] = (int16_t)i;
-    if constexpr (QUANT) {
+    // the activation's scales [R][FB]; with QUANT after the rows themselves
+    float *qs = reinterpret_cast<float *>(smem + (QUANT ? R * F : 0));
+    if constexpr (!QUANT) {
+        for (int i = tid; i < R * FB; i += kThreads)
+            qs[i] = P.as[i];
+    } else {
         // 16 lanes take a group of 128 values, 8 each
         char *q8 = smem;
-        float *qs = reinterpret_cast<float *>(smem + (size_t)R * F);
         for (int i = tid; i < R * FB * 16; i += kThreads) {
             const int grp = i / 16, r = grp / FB, kb = grp % FB, c = kb * kBlk + 8 * (i % 16);
             float v[8];
@@ -339,24 +344,26 @@ __global__ void __launch_bounds__(kThreads) few_down(const FewParams P)
         s.a.lo = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(wb + (uint32_t)(j % 8) * (uint32_t)F + col));
         s.a.hi = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(wb + (uint32_t)(8 + j % 8) * (uint32_t)F + col));
         s.sw = P.down_s[((size_t)e * nbk + n0 / kBlk) * FB + kb];
-        // a token that did not choose the expert: zeros
-        const int r = rows[ai][j], c = kb * kBlk + 16 * g;
-        const u32x4 z = {0, 0, 0, 0};
-        if constexpr (QUANT) {
-            const char *q8 = smem + (size_t)max(r, 0) * F;
-            s.b.lo = r >= 0 && c < F ? *reinterpret_cast<const u32x4 *>(q8 + c) : z;
-            s.b.hi = r >= 0 && c + 64 < F ? *reinterpret_cast<const u32x4 *>(q8 + c + 64) : z;
-            s.f = r >= 0 ? reinterpret_cast<const float *>(smem + (size_t)R * F)[r * FB + kb] * wt[r] : 0.f;
-        } else {
-            const uint8_t *q8 = P.a8 + (size_t)max(r, 0) * F;
-            s.b.lo = r >= 0 && c < F ? *reinterpret_cast<const u32x4 *>(q8 + c) : z;
-            s.b.hi = r >= 0 && c + 64 < F ? *reinterpret_cast<const u32x4 *>(q8 + c + 64) : z;
-            s.f = r >= 0 ? P.as[(size_t)r * FB + kb] * wt[r] : 0.f;
-        }
+        // a token that did not choose the expert has zeros there; what is loaded for it is
+        // another row's (no request is skipped: stream_product)
+        const int r = rows[ai][j], rc = max(r, 0), c = kb * kBlk + 16 * g;
+        s.chosen = r >= 0;
+        s.lo = r >= 0 && c < F;
+        s.hi = r >= 0 && c + 64 < F;
+        const char *q8 = QUANT ? smem + rc * F : reinterpret_cast<const char *>(P.a8) + (size_t)rc * F;
+        s.b.lo = *reinterpret_cast<const u32x4 *>(q8 + (c < F ? c : 0));
+        s.b.hi = *reinterpret_cast<const u32x4 *>(q8 + (c + 64 < F ? c + 64 : 0));
+        s.f = qs[rc * FB + kb] * wt[rc];
     };
     auto mul = [&](const DownStage &s) {
-        const float4v p = block_product(to_frag16(whole_rows(s.a)), to_frag16(s.b));
-        const float f = s.f * s.sw;
+        Frag8 b;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            b.lo[i] = s.lo ? s.b.lo[i] : 0u;
+            b.hi[i] = s.hi ? s.b.hi[i] : 0u;
+        }
+        const float4v p = block_product(to_frag16(whole_rows(s.a)), to_frag16(b));
+        const float f = s.chosen ? s.f * s.sw : 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             acc[i] = __builtin_fmaf(p[i], f, acc[i]);
@@ -416,12 +423,12 @@ hipError_t launch_few_layer(FewParams P, hipStream_t s)
     else
         hipLaunchKernelGGL((few_gate_up<kWaves, false>), grid, block, zbytes, s, P);
     const size_t red = kWaves * 256 * sizeof(float);
-    if (quant) {
-        const size_t q = (size_t)P.T * P.kt * (P.F + 4 * ((P.F + kBlk - 1) / kBlk));
-        hipLaunchKernelGGL((few_down<true>), dim3(P.H / 16), dim3(kThreads), q > red ? q : red, s, P);
-    } else {
-        hipLaunchKernelGGL((few_down<false>), dim3(P.H / 16), dim3(kThreads), red, s, P);
-    }
+    const size_t q = (size_t)P.T * P.kt * ((quant ? P.F : 0) + 4 * ((P.F + kBlk - 1) / kBlk));
+    const size_t lds = q > red ? q : red;
+    if (quant)
+        hipLaunchKernelGGL((few_down<true>), dim3(P.H / 16), dim3(kThreads), lds, s, P);
+    else
+        hipLaunchKernelGGL((few_down<false>), dim3(P.H / 16), dim3(kThreads), lds, s, P);
     return hipGetLastError();
 }
 

@@ -481,7 +481,8 @@ apmoe_status apmoe_norm(apmoe_ctx *ctx, const void *x, int32_t x_dtype, const vo
  *   x8 e4m3 [T][K] (gather) or [T*topk][K], x_scale fp32 [rows][ceil(K/128)];
  *   w8 e4m3 [E][N][K], w_scale fp32 [E][ceil(N/128)][ceil(K/128)];
  *   out [T*topk][N] of out_dtype (APMOE_F16, APMOE_BF16, APMOE_F32), RNE.
- * perm and offsets as apmoe_route writes them; rows of the output at or past
+ * perm and offsets as apmoe_route writes them (with E > 1 an expert has at most T rows:
+ * a token's experts are distinct); rows of the output at or past
  * offsets[E] are not written.  A dense product is E = 1, topk = 1 with offsets NULL
  * (every row is the one expert's) and gather = 0.
  * Limits: 1 <= E <= 256, N >= 1, K % 16 == 0, 16 <= K < 2^24, 1 <= topk <= 16, T >= 0,
@@ -529,7 +530,11 @@ apmoe_status apmoe_moe_workspace_fp8(apmoe_ctx *ctx, const apmoe_fp8_experts *ex
 
 /*
  * Whole layer on e4m3 experts: apmoe_route on x, apmoe_gemm_act_fp8 on (x8, x_scale),
- * apmoe_gemm_fp8 into fp32, apmoe_combine.  x fp16 [T][H] is what the router reads, x8
+ * apmoe_gemm_fp8 into fp32 (for experts of more than 32 rows with the sums of a 16-bit
+ * out), apmoe_combine.  Up to 16 tokens (T * E^2 up to 2^18) take two launches, or three
+ * where T * E * H is above 65536: the selection inside the gate_up launch (logits summed
+ * in another order than apmoe_route's), then down with the sum over the experts, in the
+ * order of the experts, in its accumulators.  x fp16 [T][H] is what the router reads, x8
  * and x_scale the same rows in 8 bits (apmoe_norm gives both); out fp16 [T][H].
  * The first E - n_shared experts are the routed ones (w_router rows, bias as in
  * apmoe_route), the last n_shared see every token with weight 1.
@@ -537,7 +542,7 @@ apmoe_status apmoe_moe_workspace_fp8(apmoe_ctx *ctx, const apmoe_fp8_experts *ex
  * aligned.  Every limit of the steps is checked before the first launch.  The call
  * enqueues only kernel launches on `stream`, so it can be captured in a HIP graph; two
  * calls (or two captured graphs) that may run at the same time need a workspace each,
- * and, as for apmoe_route, a context each.
+ * and, as for apmoe_route, a context each (above 16 tokens).
  */
 apmoe_status apmoe_moe_forward_fp8(apmoe_ctx *ctx, const apmoe_fp8_experts *ex, const uint16_t *x, const uint8_t *x8,
                                    const float *x_scale, const uint16_t *w_router, const float *bias, int32_t T,
