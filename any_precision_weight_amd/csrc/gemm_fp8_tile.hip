@@ -23,7 +23,8 @@ constexpr int kGroup = 8;              // weight tiles that share their token ti
 constexpr uint32_t kStageW = 2 * kHalf * kBlk;
 constexpr uint32_t kStage = kStageW + kMaxTok * kBlk;
 constexpr uint32_t kScales = kMaxTok * 4;
-constexpr uint32_t kLds = 2 * (kStage + kScales);
+constexpr uint32_t kBuffer = kStage + kScales;  // a stage and its tokens' scales
+constexpr uint32_t kLds = 2 * kBuffer;
 
 __device__ const u32x4 kZeros = {0, 0, 0, 0};
 
@@ -77,33 +78,23 @@ __device__ inline bool resolve(const TileParams &T, int *scan, Tile &t)
     int r0, m;
     expert_rows(P, lo, r0, m);
     const int m0 = (u - (lo > 0 ? scan[lo - 1] : 0)) * kMaxTok;
-    t.e = __builtin_amdgcn_readfirstlane(lo);
-    t.r0 = __builtin_amdgcn_readfirstlane(r0);
-    t.m0 = __builtin_amdgcn_readfirstlane(m0);
-    t.M = __builtin_amdgcn_readfirstlane(min(kMaxTok, m - m0));
-    t.nt = __builtin_amdgcn_readfirstlane(k * kGroup + rem % gs);
+    t = Tile{lo, r0, m0, min(kMaxTok, m - m0), k * kGroup + rem % gs};
     return true;
 }
 
-template <bool EXACT>
-struct Operand;
-template <>
-struct Operand<true> {
-    typedef Frag16 type;
-    static __device__ inline Frag16 of(const Frag8 &f) { return to_frag16(f); }
-};
-template <>
-struct Operand<false> {
-    typedef Frag8 type;
-    static __device__ inline Frag8 of(const Frag8 &f) { return f; }
-};
+// A pointer that is the same in every lane, in scalar registers.
+__device__ inline const uint8_t *scalar_ptr(const uint8_t *p)
+{
+    const uint64_t v = (uint64_t)(uintptr_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    return reinterpret_cast<const uint8_t *>((uintptr_t)((uint64_t)hi << 32 | lo));
+}
 
 // TTN: 16-token tiles of a wave.  EXACT: fp16 products (block_product).
 template <bool EXACT, bool ACT, int TTN>
 __device__ __attribute__((always_inline)) inline void tile(const TileParams &T, const Tile &t, char *smem)
 {
     const Fp8Params &P = T.p;
-    typedef Operand<EXACT> Op;
     constexpr int kTok = 32 * TTN;  // tokens of the tile
     constexpr int kXi = kTok > 64 ? kTok / 64 : 1;
     const int tid = threadIdx.x, lane = tid % kWave;
@@ -129,25 +120,30 @@ __device__ __attribute__((always_inline)) inline void tile(const TileParams &T, 
     __amdgpu_buffer_rsrc_t rw[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h)  // rows past the matrix read as zeros
-        rw[h] = make_rsrc(wbase + (size_t)row[h] * K, (uint32_t)rows[h] * (uint32_t)K);
+        rw[h] = make_rsrc(scalar_ptr(wbase + (size_t)row[h] * K),
+                          __builtin_amdgcn_readfirstlane((uint32_t)rows[h] * (uint32_t)K));
     const int crow = 8 * wave + lane / 8;
     const int chunk = (lane % 8) ^ ((crow / 2) % 8);
     uint32_t woff[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
         woff[i] = (uint32_t)(64 * i + crow) * (uint32_t)K + 16u * chunk;
-    const uint8_t *xp[kXi];
+    uint32_t xrow[kXi];  // token rows
 #pragma unroll
     for (int i = 0; i < kXi; ++i)
-        xp[i] = P.x8 + src_row(P, t.r0 + t.m0 + min(64 * i + crow, t.M - 1)) * K + 16 * chunk;
-    const bool scaler = wave * 64 < kTok;  // waves that copy the tokens' scales
-    const float *xsp = P.xs;
-    if (scaler)
-        xsp += src_row(P, t.r0 + t.m0 + min(wave * 64 + lane, t.M - 1)) * KB;
+        xrow[i] = (uint32_t)src_row(P, t.r0 + t.m0 + min(64 * i + crow, t.M - 1));
+    const uint8_t *x8 = scalar_ptr(P.x8);
+    // every 64 tokens' scales are copied by one wave of kXi (and again by the others: no
+    // branch in the pipeline)
+    const int srow = kTok > 64 ? wave % kXi : 0;
+    const float *xsp = P.xs + src_row(P, t.r0 + t.m0 + min(srow * 64 + lane, t.M - 1)) * KB;
+    const uint64_t zeros = (uint64_t)(uintptr_t)&kZeros;
     auto copy = [&](int kb, uint32_t buf) {
         char *dst = smem + buf;
-        // K's last block may be shorter: zeros there, for the weights by an offset out of range
+        // K's last block may be shorter: zeros there, for the weights by an offset out of
+        // range, for the tokens from kZeros
         const bool in = kb * kBlk + 16 * chunk < K;
+        const uint64_t pick = in ? ~0ull : 0ull;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -157,14 +153,13 @@ __device__ __attribute__((always_inline)) inline void tile(const TileParams &T, 
                     in ? woff[i] : 0x80000000u, (uint32_t)kb * kBlk, 0, 0);
 #pragma unroll
         for (int i = 0; i < kXi; ++i) {
-            const void *src = in ? (const void *)(xp[i] + (size_t)kb * kBlk) : (const void *)&kZeros;
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
-                                             (__attribute__((address_space(3))) void *)(dst + kStageW + (64 * i + 8 * wave) * kBlk),
-                                             16, 0, 0);
+            const uint64_t src = (uint64_t)(uintptr_t)(x8 + (uint32_t)kb * kBlk + 16 * chunk) + (uint64_t)xrow[i] * (uint32_t)K;
+            __builtin_amdgcn_global_load_lds(
+                (const __attribute__((address_space(1))) void *)(uintptr_t)((src & pick) | (zeros & ~pick)),
+                (__attribute__((address_space(3))) void *)(dst + kStageW + (64 * i + 8 * wave) * kBlk), 16, 0, 0);
         }
-        if (scaler)
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(xsp + kb),
-                                             (__attribute__((address_space(3))) void *)(dst + kStage + wave * 256), 4, 0, 0);
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(xsp + kb),
+                                         (__attribute__((address_space(3))) void *)(dst + kStage + srow * 256), 4, 0, 0);
     };
 
     const uint32_t swz = 16u * (uint32_t)(g ^ ((j / 2) % 8));  // chunk g of rows j, j + 16, ...; chunk g + 4 is at swz ^ 64
@@ -177,43 +172,144 @@ __device__ __attribute__((always_inline)) inline void tile(const TileParams &T, 
             acc[r][c] = float4v{0.f, 0.f, 0.f, 0.f};
     const bool active = wt * 16 * TTN < t.M;
 
-    copy(0, 0);
-    uint32_t buf = 0;
-    for (int kb = 0; kb < KB; ++kb) {
-        // this stage has landed for every wave, and every wave is done with the other buffer
+    // LDS addresses of a buffer: chunks g and g + 4 of the wave's first weight and token
+    // row, and the scale of its first token.  Everything else is a constant further; the
+    // empty asm keeps the compiler from holding each sum in a register of its own.
+    struct At {
+        uint32_t a[2], b[2], s;
+    };
+    auto at = [&](uint32_t buf) {
+        const uint32_t sb = base + buf;
+        At v = {{sb + arow + swz, sb + arow + (swz ^ 64u)},
+                {sb + brow + swz, sb + brow + (swz ^ 64u)},
+                sb + kStage + 4u * (uint32_t)(wt * 16 * TTN + j)};
+        asm volatile("" : "+v"(v.a[0]), "+v"(v.a[1]), "+v"(v.b[0]), "+v"(v.b[1]), "+v"(v.s));
+        return v;
+    };
+    auto read_a = [&](const At &v, int r) {
+        const uint32_t o = (r >> 1) * kHalf * kBlk + (r & 1) * 16 * kBlk;
+        return Frag8{lds_b128(v.a[0] + o), lds_b128(v.a[1] + o)};
+    };
+    auto read_b = [&](const At &v, int c) {
+        return Frag8{lds_b128(v.b[0] + c * 16 * kBlk), lds_b128(v.b[1] + c * 16 * kBlk)};
+    };
+    auto read_sx = [&](const At &v, int c) {
+        return *reinterpret_cast<const __attribute__((address_space(3))) float *>((uintptr_t)(v.s + 64u * c));
+    };
+
+    if constexpr (EXACT) {
+        copy(0, 0);
+        uint32_t buf = 0;
+        for (int kb = 0; kb < KB; ++kb) {
+            // this stage has landed for every wave, and every wave is done with the other buffer
+            __builtin_amdgcn_s_waitcnt(wait_vm<0>());
+            asm volatile("s_barrier" ::: "memory");
+            const uint32_t next = buf ^ kBuffer;
+            if (kb + 1 < KB)
+                copy(kb + 1, next);
+            if (active) {
+                const At sb = at(buf);
+                const float sw0 = ws[0][kb], sw1 = ws[1][kb];
+                Frag16 a[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    a[r] = to_frag16(read_a(sb, r));
+#pragma unroll
+                for (int c = 0; c < TTN; ++c) {
+                    const Frag16 b = to_frag16(read_b(sb, c));
+                    const float sx = read_sx(sb, c);
+                    const float f0 = sx * sw0, f1 = sx * sw1;
+                    float4v p[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        p[r] = block_product(a[r], b);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            acc[r][c][i] = __builtin_fmaf(p[r][i], r < 2 ? f0 : f1, acc[r][c][i]);
+                }
+            }
+            buf = next;
+        }
+    } else {
+        // Step c of a stage multiplies token tile c by the four weight tiles; each MFMA is
+        // preceded by the four scaled additions of the product that its registers held
+        // before.  b is read a step ahead.  In step TTN - 2, with the stage's last b on its
+        // way, one barrier says that the stage's buffer is free and that the next stage has
+        // landed; the next stage's first fragments are read while the last two steps
+        // multiply.
+        static_assert(TTN % 2 == 0, "b's two register sets alternate across stages");
+        copy(0, 0);
+        copy(min(1, KB - 1), kBuffer);
         __builtin_amdgcn_s_waitcnt(wait_vm<0>());
         asm volatile("s_barrier" ::: "memory");
-        const uint32_t next = buf ^ (kStage + kScales);
-        if (kb + 1 < KB)
-            copy(kb + 1, next);
-        if (active) {
-            const uint32_t sb = base + buf;
-            const float sw0 = ws[0][kb], sw1 = ws[1][kb];
-            typename Op::type a[4];
+        const At buf0 = at(0), buf1 = at(kBuffer);
+        Frag8 a[2][2], a2[2], b[2];  // weight tiles 0, 1 in two sets; 2, 3 in one
+        float sx[2], f[2] = {0.f, 0.f};
+        float sw[2] = {ws[0][0], ws[1][0]}, swn[2] = {0.f, 0.f};
+        float4v p[4];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const uint32_t ad = sb + (r >> 1) * kHalf * kBlk + arow + (r & 1) * 16 * kBlk;
-                a[r] = Op::of(Frag8{lds_b128(ad + swz), lds_b128(ad + (swz ^ 64u))});
-            }
+        for (int r = 0; r < 4; ++r) {
+            (r < 2 ? a[0][r] : a2[r - 2]) = read_a(buf0, r);
+            p[r] = float4v{0.f, 0.f, 0.f, 0.f};
+        }
+        b[0] = read_b(buf0, 0);
+        sx[0] = read_sx(buf0, 0);
+        auto stage = [&](auto par, int kb) {
+            constexpr int Q = decltype(par)::value;  // buffer and register set of this stage
+            const At &sb = Q ? buf1 : buf0, &sn = Q ? buf0 : buf1;
 #pragma unroll
             for (int c = 0; c < TTN; ++c) {
-                const uint32_t bd = sb + brow + c * 16 * kBlk;
-                const typename Op::type b = Op::of(Frag8{lds_b128(bd + swz), lds_b128(bd + (swz ^ 64u))});
-                const float sx = *reinterpret_cast<const __attribute__((address_space(3))) float *>(
-                    (uintptr_t)(sb + kStage + 4u * (wt * 16 * TTN + 16 * c + j)));
-                const float f0 = sx * sw0, f1 = sx * sw1;
-                float4v p[4];
+                if (c + 1 < TTN) {
+                    b[(c + 1) % 2] = read_b(sb, c + 1);
+                    sx[(c + 1) % 2] = read_sx(sb, c + 1);
+                } else {
+                    b[0] = read_b(sn, 0);
+                    sx[0] = read_sx(sn, 0);
+                }
+                if (c == TTN - 2) {
+                    const int k1 = min(kb + 1, KB - 1);
+                    swn[0] = ws[0][k1];
+                    swn[1] = ws[1][k1];
+                    __builtin_amdgcn_sched_barrier(0);
+                    __builtin_amdgcn_s_waitcnt(wait_vm<0>());
+                    asm volatile("s_barrier" ::: "memory");
+                    copy(min(kb + 2, KB - 1), Q * kBuffer);
+                }
+                if (c >= TTN - 2)
+                    a[1 - Q][c + 2 - TTN] = read_a(sn, c + 2 - TTN);
+                __builtin_amdgcn_sched_barrier(0);
+                const int pc = c == 0 ? TTN - 1 : c - 1;  // the product in p: the step before
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    p[r] = block_product(a[r], b);
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
+                for (int r = 0; r < 4; ++r) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        acc[r][c][i] = __builtin_fmaf(p[r][i], r < 2 ? f0 : f1, acc[r][c][i]);
+                        acc[r][pc][i] = __builtin_fmaf(p[r][i], f[r >> 1], acc[r][pc][i]);
+                    p[r] = block_product(r < 2 ? a[Q][r] : a2[r - 2], b[c % 2]);
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (r >= 2 && c == TTN - 1)
+                        a2[r - 2] = read_a(sn, r);
+                }
+                f[0] = sx[c % 2] * sw[0];
+                f[1] = sx[c % 2] * sw[1];
             }
+            sw[0] = swn[0];
+            sw[1] = swn[1];
+        };
+        int kb = 0;
+        for (; kb + 2 <= KB; kb += 2) {
+            stage(std::integral_constant<int, 0>{}, kb);
+            stage(std::integral_constant<int, 1>{}, kb + 1);
         }
-        buf = next;
+        if (kb < KB)
+            stage(std::integral_constant<int, 0>{}, kb);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                acc[r][TTN - 1][i] = __builtin_fmaf(p[r][i], f[r >> 1], acc[r][TTN - 1][i]);
+        __builtin_amdgcn_s_waitcnt(wait_vm<0>());  // no copy into LDS is left when it is used again
     }
 
     // ---- epilogue
@@ -283,11 +379,17 @@ template <bool EXACT, bool ACT>
 __global__ void __launch_bounds__(kThreads) fp8_tile_kernel(const TileParams T)
 {
     __shared__ __attribute__((aligned(1024))) char smem[kLds];
-    Tile t;
-    const bool mine = resolve(T, reinterpret_cast<int *>(smem), t);
-    __syncthreads();  // the scan is read
-    if (!mine)
+    Tile t = {0, 0, 0, 0, 0};
+    if (!resolve(T, reinterpret_cast<int *>(smem), t))
         return;
+    __syncthreads();  // the scan is read
+    // the same in every lane: into scalar registers (here, behind the branch that the
+    // compiler takes to depend on the lane)
+    t.e = __builtin_amdgcn_readfirstlane(t.e);
+    t.r0 = __builtin_amdgcn_readfirstlane(t.r0);
+    t.m0 = __builtin_amdgcn_readfirstlane(t.m0);
+    t.M = __builtin_amdgcn_readfirstlane(t.M);
+    t.nt = __builtin_amdgcn_readfirstlane(t.nt);
     if (t.M > 128)
         tile<EXACT, ACT, 8>(T, t, smem);
     else if (t.M > 64)
