@@ -60,10 +60,16 @@ __device__ inline half8 to_half8(uint32_t w0, uint32_t w1)
     return half8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
+// Operand i of Frag16.
+__device__ inline half8 quarter(const Frag8 &f, int i)
+{
+    const u32x4 &v = i < 2 ? f.lo : f.hi;
+    return to_half8(v[2 * (i & 1)], v[2 * (i & 1) + 1]);
+}
+
 __device__ inline Frag16 to_frag16(const Frag8 &f)
 {
-    return Frag16{{to_half8(f.lo[0], f.lo[1]), to_half8(f.lo[2], f.lo[3]), to_half8(f.hi[0], f.hi[1]),
-                   to_half8(f.hi[2], f.hi[3])}};
+    return Frag16{{quarter(f, 0), quarter(f, 1), quarter(f, 2), quarter(f, 3)}};
 }
 
 // The product of one block, C[16][16] (fp32) = A[16][128] * B[128][16].  Lane l gives 32

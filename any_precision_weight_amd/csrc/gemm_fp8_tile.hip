@@ -18,7 +18,7 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kHalf = 128;             // weight rows of a half
-constexpr int kMaxTok = 256;           // tokens of a tile
+constexpr int kMaxTok = 256;           // tokens of a stage
 constexpr int kGroup = 8;              // weight tiles that share their token tiles through an XCD's L2
 constexpr uint32_t kStageW = 2 * kHalf * kBlk;
 constexpr uint32_t kStage = kStageW + kMaxTok * kBlk;
@@ -40,7 +40,7 @@ struct Tile {
 // Workgroup -> tile; every thread computes the same answer.  Tiles in order: groups of
 // kGroup weight tiles, in a group the token tiles of every served expert, then the
 // group's weight tiles.  XCD x (workgroups b with b % 8 = x) takes the x-th eighth.
-__device__ inline bool resolve(const TileParams &T, int *scan, Tile &t)
+__device__ inline bool resolve(const TileParams &T, int tok, int *scan, Tile &t)
 {
     const Fp8Params &P = T.p;
     const int tid = threadIdx.x;
@@ -48,7 +48,7 @@ __device__ inline bool resolve(const TileParams &T, int *scan, Tile &t)
     if (tid < P.E) {
         int r0, m;
         expert_rows(P, tid, r0, m);
-        n = m > kStreamMax ? (m + kMaxTok - 1) / kMaxTok : 0;
+        n = m > kStreamMax ? (m + tok - 1) / tok : 0;
     }
     scan[tid] = n;
     __syncthreads();
@@ -77,8 +77,8 @@ __device__ inline bool resolve(const TileParams &T, int *scan, Tile &t)
     }
     int r0, m;
     expert_rows(P, lo, r0, m);
-    const int m0 = (u - (lo > 0 ? scan[lo - 1] : 0)) * kMaxTok;
-    t = Tile{lo, r0, m0, min(kMaxTok, m - m0), k * kGroup + rem % gs};
+    const int m0 = (u - (lo > 0 ? scan[lo - 1] : 0)) * tok;
+    t = Tile{lo, r0, m0, min(tok, m - m0), k * kGroup + rem % gs};
     return true;
 }
 
@@ -170,8 +170,6 @@ __device__ __attribute__((always_inline)) inline void tile(const TileParams &T, 
 #pragma unroll
         for (int c = 0; c < TTN; ++c)
             acc[r][c] = float4v{0.f, 0.f, 0.f, 0.f};
-    const bool active = wt * 16 * TTN < t.M;
-
     // LDS addresses of a buffer: chunks g and g + 4 of the wave's first weight and token
     // row, and the scale of its first token.  Everything else is a constant further; the
     // empty asm keeps the compiler from holding each sum in a register of its own.
@@ -197,63 +195,121 @@ __device__ __attribute__((always_inline)) inline void tile(const TileParams &T, 
         return *reinterpret_cast<const __attribute__((address_space(3))) float *>((uintptr_t)(v.s + 64u * c));
     };
 
-    if constexpr (EXACT) {
-        copy(0, 0);
-        uint32_t buf = 0;
-        for (int kb = 0; kb < KB; ++kb) {
-            // this stage has landed for every wave, and every wave is done with the other buffer
-            __builtin_amdgcn_s_waitcnt(wait_vm<0>());
-            asm volatile("s_barrier" ::: "memory");
-            const uint32_t next = buf ^ kBuffer;
-            if (kb + 1 < KB)
-                copy(kb + 1, next);
-            if (active) {
-                const At sb = at(buf);
-                const float sw0 = ws[0][kb], sw1 = ws[1][kb];
-                Frag16 a[4];
+    // Both pipelines: step c of a stage multiplies token tile c by the four weight tiles,
+    // and the products of the step before are scaled and added before their registers are
+    // written again.  Fragments are read ahead.  At the start of step TTN - 2, when every
+    // read of the stage has been sent, one barrier says that the stage's buffer is free
+    // and that the next stage has landed; the next stage's first fragments are read while
+    // the last two steps multiply.
+    static_assert(TTN % 2 == 0, "b's two register sets alternate across stages");
+    copy(0, 0);
+    copy(min(1, KB - 1), kBuffer);
+    __builtin_amdgcn_s_waitcnt(wait_vm<0>());
+    asm volatile("s_barrier" ::: "memory");
+    const At buf0 = at(0), buf1 = at(kBuffer);
+    float sx[2], f[2] = {0.f, 0.f};
+    float sw[2] = {ws[0][0], ws[1][0]}, swn[2] = {0.f, 0.f};
+    float4v p[4];
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    a[r] = to_frag16(read_a(sb, r));
+    for (int r = 0; r < 4; ++r)
+        p[r] = float4v{0.f, 0.f, 0.f, 0.f};
+    auto add = [&](int r, int c) {  // the product in p[r] is tile c's
 #pragma unroll
-                for (int c = 0; c < TTN; ++c) {
-                    const Frag16 b = to_frag16(read_b(sb, c));
-                    const float sx = read_sx(sb, c);
-                    const float f0 = sx * sw0, f1 = sx * sw1;
-                    float4v p[4];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        p[r] = block_product(a[r], b);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            acc[r][c][i] = __builtin_fmaf(p[r][i], r < 2 ? f0 : f1, acc[r][c][i]);
-                }
-            }
-            buf = next;
-        }
-    } else {
-        // Step c of a stage multiplies token tile c by the four weight tiles; each MFMA is
-        // preceded by the four scaled additions of the product that its registers held
-        // before.  b is read a step ahead.  In step TTN - 2, with the stage's last b on its
-        // way, one barrier says that the stage's buffer is free and that the next stage has
-        // landed; the next stage's first fragments are read while the last two steps
-        // multiply.
-        static_assert(TTN % 2 == 0, "b's two register sets alternate across stages");
-        copy(0, 0);
-        copy(min(1, KB - 1), kBuffer);
+        for (int i = 0; i < 4; ++i)
+            acc[r][c][i] = __builtin_fmaf(p[r][i], f[r >> 1], acc[r][c][i]);
+    };
+    auto turn = [&](int kb, uint32_t buf) {  // the barrier of stage kb, whose buffer is buf
+        const int k1 = min(kb + 1, KB - 1);
+        swn[0] = ws[0][k1];
+        swn[1] = ws[1][k1];
+        __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_waitcnt(wait_vm<0>());
         asm volatile("s_barrier" ::: "memory");
-        const At buf0 = at(0), buf1 = at(kBuffer);
-        Frag8 a[2][2], a2[2], b[2];  // weight tiles 0, 1 in two sets; 2, 3 in one
-        float sx[2], f[2] = {0.f, 0.f};
-        float sw[2] = {ws[0][0], ws[1][0]}, swn[2] = {0.f, 0.f};
-        float4v p[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            (r < 2 ? a[0][r] : a2[r - 2]) = read_a(buf0, r);
-            p[r] = float4v{0.f, 0.f, 0.f, 0.f};
+        copy(min(kb + 2, KB - 1), buf);
+    };
+    auto run = [&](auto &&stage) {
+        int kb = 0;
+        for (; kb + 2 <= KB; kb += 2) {
+            stage(std::integral_constant<int, 0>{}, kb);
+            stage(std::integral_constant<int, 1>{}, kb + 1);
         }
+        if (kb < KB)
+            stage(std::integral_constant<int, 0>{}, kb);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            add(r, TTN - 1);
+        __builtin_amdgcn_s_waitcnt(wait_vm<0>());  // no copy into LDS is left when it is used again
+    };
+
+    if constexpr (EXACT) {
+        // 16 fp16 MFMAs a step, column quarter by quarter; the next token tile is
+        // converted between them, and in the stage's last step the next stage's weights,
+        // each quarter once its last MFMA has been sent.
+        Frag16 a[4], b[2];
+        Frag8 ra[4], rb;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            a[r] = to_frag16(read_a(buf0, r));
+        b[0] = to_frag16(read_b(buf0, 0));
+        rb = read_b(buf0, 1);
+        sx[0] = read_sx(buf0, 0);
+        sx[1] = read_sx(buf0, 1);
+        auto stage = [&](auto par, int kb) {
+            constexpr int Q = decltype(par)::value;
+            const At &sb = Q ? buf1 : buf0, &sn = Q ? buf0 : buf1;
+#pragma unroll
+            for (int c = 0; c < TTN; ++c) {
+                if (c == TTN - 2) {
+                    turn(kb, Q * kBuffer);
+                    ra[0] = read_a(sn, 0);
+                    ra[1] = read_a(sn, 1);
+                }
+                if (c == TTN - 1) {
+                    ra[2] = read_a(sn, 2);
+                    ra[3] = read_a(sn, 3);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (k > 0)
+                        b[(c + 1) % 2].k[k - 1] = quarter(rb, k - 1);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        if (k == 0) {
+                            add(r, c == 0 ? TTN - 1 : c - 1);
+                            p[r] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[r].k[0], b[c % 2].k[0],
+                                                                          float4v{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+                        } else {
+                            p[r] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[r].k[k], b[c % 2].k[k], p[r], 0, 0, 0);
+                            if (c == TTN - 1)
+                                a[r].k[k - 1] = quarter(ra[r], k - 1);
+                        }
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                b[(c + 1) % 2].k[3] = quarter(rb, 3);
+                if (c == TTN - 1) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        a[r].k[3] = quarter(ra[r], 3);
+                }
+                f[0] = sx[c % 2] * sw[0];
+                f[1] = sx[c % 2] * sw[1];
+                const At &from = c + 2 < TTN ? sb : sn;
+                rb = read_b(from, (c + 2) % TTN);
+                sx[c % 2] = read_sx(from, (c + 2) % TTN);
+            }
+            sw[0] = swn[0];
+            sw[1] = swn[1];
+        };
+        run(stage);
+    } else {
+        // Each MFMA is preceded by the four additions of the product that its registers
+        // held; b is read a step ahead.
+        Frag8 a[2][2], a2[2], b[2];  // weight tiles 0, 1 in two sets; 2, 3 in one
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            (r < 2 ? a[0][r] : a2[r - 2]) = read_a(buf0, r);
         b[0] = read_b(buf0, 0);
         sx[0] = read_sx(buf0, 0);
         auto stage = [&](auto par, int kb) {
@@ -261,31 +317,23 @@ __device__ __attribute__((always_inline)) inline void tile(const TileParams &T, 
             const At &sb = Q ? buf1 : buf0, &sn = Q ? buf0 : buf1;
 #pragma unroll
             for (int c = 0; c < TTN; ++c) {
-                if (c + 1 < TTN) {
+                const At &from = c + 1 < TTN ? sb : sn;
+                if (c + 1 < TTN) {  // (before the barrier in step TTN - 2)
                     b[(c + 1) % 2] = read_b(sb, c + 1);
                     sx[(c + 1) % 2] = read_sx(sb, c + 1);
-                } else {
-                    b[0] = read_b(sn, 0);
-                    sx[0] = read_sx(sn, 0);
                 }
-                if (c == TTN - 2) {
-                    const int k1 = min(kb + 1, KB - 1);
-                    swn[0] = ws[0][k1];
-                    swn[1] = ws[1][k1];
-                    __builtin_amdgcn_sched_barrier(0);
-                    __builtin_amdgcn_s_waitcnt(wait_vm<0>());
-                    asm volatile("s_barrier" ::: "memory");
-                    copy(min(kb + 2, KB - 1), Q * kBuffer);
+                if (c == TTN - 2)
+                    turn(kb, Q * kBuffer);
+                if (c + 1 == TTN) {
+                    b[0] = read_b(from, 0);
+                    sx[0] = read_sx(from, 0);
                 }
                 if (c >= TTN - 2)
                     a[1 - Q][c + 2 - TTN] = read_a(sn, c + 2 - TTN);
                 __builtin_amdgcn_sched_barrier(0);
-                const int pc = c == 0 ? TTN - 1 : c - 1;  // the product in p: the step before
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        acc[r][pc][i] = __builtin_fmaf(p[r][i], f[r >> 1], acc[r][pc][i]);
+                    add(r, c == 0 ? TTN - 1 : c - 1);
                     p[r] = block_product(r < 2 ? a[Q][r] : a2[r - 2], b[c % 2]);
                     __builtin_amdgcn_sched_barrier(0);
                     if (r >= 2 && c == TTN - 1)
@@ -297,22 +345,11 @@ __device__ __attribute__((always_inline)) inline void tile(const TileParams &T, 
             sw[0] = swn[0];
             sw[1] = swn[1];
         };
-        int kb = 0;
-        for (; kb + 2 <= KB; kb += 2) {
-            stage(std::integral_constant<int, 0>{}, kb);
-            stage(std::integral_constant<int, 1>{}, kb + 1);
-        }
-        if (kb < KB)
-            stage(std::integral_constant<int, 0>{}, kb);
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                acc[r][TTN - 1][i] = __builtin_fmaf(p[r][i], f[r >> 1], acc[r][TTN - 1][i]);
-        __builtin_amdgcn_s_waitcnt(wait_vm<0>());  // no copy into LDS is left when it is used again
+        run(stage);
     }
 
     // ---- epilogue
+    const bool active = wt * 16 * TTN < t.M;  // this half of the tile has tokens
     if constexpr (ACT) {
         uint32_t *amax = reinterpret_cast<uint32_t *>(smem);  // [4 row groups][kTok]
         __syncthreads();                                      // the last stage is read
@@ -375,12 +412,19 @@ __device__ __attribute__((always_inline)) inline void tile(const TileParams &T, 
     }
 }
 
+#ifndef EXTOK
+#define EXTOK 128
+#endif
+// Tokens of a tile.  fp16 fragments take twice the registers: 128 tokens (EXTOK).
+template <bool EXACT>
+constexpr int kTileTok = EXACT ? EXTOK : 256;
+
 template <bool EXACT, bool ACT>
 __global__ void __launch_bounds__(kThreads) fp8_tile_kernel(const TileParams T)
 {
     __shared__ __attribute__((aligned(1024))) char smem[kLds];
     Tile t = {0, 0, 0, 0, 0};
-    if (!resolve(T, reinterpret_cast<int *>(smem), t))
+    if (!resolve(T, kTileTok<EXACT>, reinterpret_cast<int *>(smem), t))
         return;
     __syncthreads();  // the scan is read
     // the same in every lane: into scalar registers (here, behind the branch that the
@@ -390,8 +434,8 @@ __global__ void __launch_bounds__(kThreads) fp8_tile_kernel(const TileParams T)
     t.m0 = __builtin_amdgcn_readfirstlane(t.m0);
     t.M = __builtin_amdgcn_readfirstlane(t.M);
     t.nt = __builtin_amdgcn_readfirstlane(t.nt);
-    if (t.M > 128)
-        tile<EXACT, ACT, 8>(T, t, smem);
+    if (kTileTok<EXACT> > 128 && t.M > 128)
+        tile<EXACT, ACT, (kTileTok<EXACT> > 128 ? kTileTok<EXACT> / 32 : 2)>(T, t, smem);
     else if (t.M > 64)
         tile<EXACT, ACT, 4>(T, t, smem);
     else
@@ -404,11 +448,12 @@ hipError_t launch_fp8_tile(const Fp8Params &P, int most, bool act, bool exact, h
 {
     if (most <= kStreamMax)
         return hipSuccess;
-    // token tiles: at most one per started kMaxTok rows of an expert with more than kStreamMax
+    // token tiles: at most one for each `tok` rows, and one more for each served expert
+    const int tok = exact ? kTileTok<true> : kTileTok<false>;
     const int served = P.E < P.R / (kStreamMax + 1) ? P.E : P.R / (kStreamMax + 1);
     if (served == 0)
         return hipSuccess;
-    const long MT = (long)(P.R / kMaxTok) + served;
+    const long MT = (long)(P.R / tok) + served;
     const TileParams T{P, act ? (P.F + kHalf - 1) / kHalf : (P.N + 2 * kHalf - 1) / (2 * kHalf)};
     const long grid = (MT * T.NT + kXcds - 1) / kXcds * kXcds;
     if (grid > 0x7FFFFFFFl)
