@@ -18,13 +18,19 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kHalf = 128;             // weight rows of a half
-constexpr int kMaxTok = 256;           // tokens of a stage
 constexpr int kGroup = 8;              // weight tiles that share their token tiles through an XCD's L2
 constexpr uint32_t kStageW = 2 * kHalf * kBlk;
-constexpr uint32_t kStage = kStageW + kMaxTok * kBlk;
-constexpr uint32_t kScales = kMaxTok * 4;
-constexpr uint32_t kBuffer = kStage + kScales;  // a stage and its tokens' scales
-constexpr uint32_t kLds = 2 * kBuffer;
+// LDS of tiles of 32 TTN tokens: NB buffers, each a stage and its tokens' scales.  A
+// stage is multiplied in about 1 us, less than a copy may take: three buffers where they
+// fit.
+template <int TTN>
+struct Lds {
+    static constexpr uint32_t kStage = kStageW + 32 * TTN * kBlk;
+    static constexpr uint32_t kBuffer = kStage + 32 * TTN * 4;
+    static constexpr int NB = TTN <= 4 ? 3 : 2;
+};
+constexpr uint32_t kLds = 3 * Lds<4>::kBuffer;
+static_assert(kLds >= 2 * Lds<8>::kBuffer && kLds <= 160 * 1024, "LDS of a workgroup");
 
 __device__ const u32x4 kZeros = {0, 0, 0, 0};
 
@@ -97,6 +103,9 @@ __device__ __attribute__((always_inline)) inline void tile(const TileParams &T, 
     const Fp8Params &P = T.p;
     constexpr int kTok = 32 * TTN;  // tokens of the tile
     constexpr int kXi = kTok > 64 ? kTok / 64 : 1;
+    constexpr int kCopies = 4 + kXi + 1;  // requests of a wave for a stage
+    constexpr uint32_t kStage = Lds<TTN>::kStage, kBuffer = Lds<TTN>::kBuffer;
+    constexpr int NB = Lds<TTN>::NB;
     const int tid = threadIdx.x, lane = tid % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int wr = wave & 3, wt = wave >> 2;
@@ -202,13 +211,18 @@ __device__ __attribute__((always_inline)) inline void tile(const TileParams &T, 
     // and that the next stage has landed; the next stage's first fragments are read while
     // the last two steps multiply.
     static_assert(TTN % 2 == 0, "b's two register sets alternate across stages");
-    copy(0, 0);
-    copy(min(1, KB - 1), kBuffer);
-    __builtin_amdgcn_s_waitcnt(wait_vm<0>());
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+        copy(min(i, KB - 1), i * kBuffer);
+    __builtin_amdgcn_s_waitcnt(wait_vm<(NB - 1) * kCopies>());
     asm volatile("s_barrier" ::: "memory");
-    const At buf0 = at(0), buf1 = at(kBuffer);
+    const At bufs[3] = {at(0), at(kBuffer), at(NB > 2 ? 2 * kBuffer : 0)};
+    // the weights' scales: scalar loads, complete with the LDS reads at a turn
+    auto scale = [&](int h, int kb) {
+        return *reinterpret_cast<const __attribute__((address_space(4))) float *>((uintptr_t)(ws[h] + kb));
+    };
     float sx[2], f[2] = {0.f, 0.f};
-    float sw[2] = {ws[0][0], ws[1][0]}, swn[2] = {0.f, 0.f};
+    float sw[2] = {scale(0, 0), scale(1, 0)}, swn[2] = {0.f, 0.f};
     float4v p[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r)
@@ -220,21 +234,25 @@ __device__ __attribute__((always_inline)) inline void tile(const TileParams &T, 
     };
     auto turn = [&](int kb, uint32_t buf) {  // the barrier of stage kb, whose buffer is buf
         const int k1 = min(kb + 1, KB - 1);
-        swn[0] = ws[0][k1];
-        swn[1] = ws[1][k1];
+        swn[0] = scale(0, k1);
+        swn[1] = scale(1, k1);
         __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_waitcnt(wait_vm<0>());
+        __builtin_amdgcn_s_waitcnt(wait_vm<(NB - 2) * kCopies>());  // stage kb + 1 has landed
         asm volatile("s_barrier" ::: "memory");
-        copy(min(kb + 2, KB - 1), buf);
+        copy(min(kb + NB, KB - 1), buf);
     };
     auto run = [&](auto &&stage) {
         int kb = 0;
-        for (; kb + 2 <= KB; kb += 2) {
+        for (; kb + NB <= KB; kb += NB) {
             stage(std::integral_constant<int, 0>{}, kb);
             stage(std::integral_constant<int, 1>{}, kb + 1);
+            if constexpr (NB > 2)
+                stage(std::integral_constant<int, 2>{}, kb + 2);
         }
         if (kb < KB)
             stage(std::integral_constant<int, 0>{}, kb);
+        if (NB > 2 && kb + 1 < KB)
+            stage(std::integral_constant<int, 1>{}, kb + 1);
 #pragma unroll
         for (int r = 0; r < 4; ++r)
             add(r, TTN - 1);
@@ -249,14 +267,14 @@ __device__ __attribute__((always_inline)) inline void tile(const TileParams &T, 
         Frag8 ra[4], rb;
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-            a[r] = to_frag16(read_a(buf0, r));
-        b[0] = to_frag16(read_b(buf0, 0));
-        rb = read_b(buf0, 1);
-        sx[0] = read_sx(buf0, 0);
-        sx[1] = read_sx(buf0, 1);
+            a[r] = to_frag16(read_a(bufs[0], r));
+        b[0] = to_frag16(read_b(bufs[0], 0));
+        rb = read_b(bufs[0], 1);
+        sx[0] = read_sx(bufs[0], 0);
+        sx[1] = read_sx(bufs[0], 1);
         auto stage = [&](auto par, int kb) {
-            constexpr int Q = decltype(par)::value;
-            const At &sb = Q ? buf1 : buf0, &sn = Q ? buf0 : buf1;
+            constexpr int Q = decltype(par)::value;  // buffer of this stage
+            const At &sb = bufs[Q], &sn = bufs[(Q + 1) % NB];
 #pragma unroll
             for (int c = 0; c < TTN; ++c) {
                 if (c == TTN - 2) {
@@ -306,15 +324,15 @@ __device__ __attribute__((always_inline)) inline void tile(const TileParams &T, 
     } else {
         // Each MFMA is preceded by the four additions of the product that its registers
         // held; b is read a step ahead.
-        Frag8 a[2][2], a2[2], b[2];  // weight tiles 0, 1 in two sets; 2, 3 in one
+        Frag8 a[NB][2], a2[2], b[2];  // weight tiles 0, 1 in a set for each buffer; 2, 3 in one
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-            (r < 2 ? a[0][r] : a2[r - 2]) = read_a(buf0, r);
-        b[0] = read_b(buf0, 0);
-        sx[0] = read_sx(buf0, 0);
+            (r < 2 ? a[0][r] : a2[r - 2]) = read_a(bufs[0], r);
+        b[0] = read_b(bufs[0], 0);
+        sx[0] = read_sx(bufs[0], 0);
         auto stage = [&](auto par, int kb) {
-            constexpr int Q = decltype(par)::value;  // buffer and register set of this stage
-            const At &sb = Q ? buf1 : buf0, &sn = Q ? buf0 : buf1;
+            constexpr int Q = decltype(par)::value;  // buffer of this stage
+            const At &sb = bufs[Q], &sn = bufs[(Q + 1) % NB];
 #pragma unroll
             for (int c = 0; c < TTN; ++c) {
                 const At &from = c + 1 < TTN ? sb : sn;
@@ -329,7 +347,7 @@ __device__ __attribute__((always_inline)) inline void tile(const TileParams &T, 
                     sx[0] = read_sx(from, 0);
                 }
                 if (c >= TTN - 2)
-                    a[1 - Q][c + 2 - TTN] = read_a(sn, c + 2 - TTN);
+                    a[(Q + 1) % NB][c + 2 - TTN] = read_a(sn, c + 2 - TTN);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
