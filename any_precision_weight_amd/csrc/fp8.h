@@ -50,21 +50,20 @@ struct Frag16 {
     half8 k[4];
 };
 
-__device__ inline half8 to_half8(uint32_t w0, uint32_t w1)
+// Word i (two values) of the fp16 operand made of half h of 16 bytes.
+__device__ inline uint32_t half2_of(const u32x4 &v, int h, int i)
 {
-    typedef _Float16 half2v __attribute__((ext_vector_type(2)));
-    const half2v a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.0f, false);
-    const half2v b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.0f, true);
-    const half2v c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.0f, false);
-    const half2v d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.0f, true);
-    return half8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+    const uint32_t w = v[2 * h + (i >> 1)];
+    return __builtin_bit_cast(uint32_t, (i & 1) ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true)
+                                                : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false));
 }
 
 // Operand i of Frag16.
 __device__ inline half8 quarter(const Frag8 &f, int i)
 {
     const u32x4 &v = i < 2 ? f.lo : f.hi;
-    return to_half8(v[2 * (i & 1)], v[2 * (i & 1) + 1]);
+    const u32x4 q = {half2_of(v, i & 1, 0), half2_of(v, i & 1, 1), half2_of(v, i & 1, 2), half2_of(v, i & 1, 3)};
+    return __builtin_bit_cast(half8, q);
 }
 
 __device__ inline Frag16 to_frag16(const Frag8 &f)

@@ -193,23 +193,20 @@ __device__ __attribute__((always_inline)) inline void tile(const TileParams &T, 
         asm volatile("" : "+v"(v.a[0]), "+v"(v.a[1]), "+v"(v.b[0]), "+v"(v.b[1]), "+v"(v.s));
         return v;
     };
-    auto read_a = [&](const At &v, int r) {
-        const uint32_t o = (r >> 1) * kHalf * kBlk + (r & 1) * 16 * kBlk;
-        return Frag8{lds_b128(v.a[0] + o), lds_b128(v.a[1] + o)};
+    // half 0: chunk g, half 1: chunk g + 4
+    auto read_a = [&](const At &v, int r, int half) {
+        return lds_b128(v.a[half] + (r >> 1) * kHalf * kBlk + (r & 1) * 16 * kBlk);
     };
-    auto read_b = [&](const At &v, int c) {
-        return Frag8{lds_b128(v.b[0] + c * 16 * kBlk), lds_b128(v.b[1] + c * 16 * kBlk)};
-    };
+    auto read_b = [&](const At &v, int c, int half) { return lds_b128(v.b[half] + c * 16 * kBlk); };
     auto read_sx = [&](const At &v, int c) {
         return *reinterpret_cast<const __attribute__((address_space(3))) float *>((uintptr_t)(v.s + 64u * c));
     };
 
-    // Both pipelines: step c of a stage multiplies token tile c by the four weight tiles,
-    // and the products of the step before are scaled and added before their registers are
-    // written again.  Fragments are read ahead.  At the start of step TTN - 2, when every
-    // read of the stage has been sent, one barrier says that the stage's buffer is free
-    // and that the next stage has landed; the next stage's first fragments are read while
-    // the last two steps multiply.
+    // Both pipelines read their fragments ahead.  When every read of a stage has been
+    // sent, one barrier (turn) says that the stage's buffer is free and that the next
+    // stage has landed; the next stage's first fragments are read while the rest of this
+    // one multiplies.  The products of a step are scaled and added before the MFMA that
+    // writes their registers again.
     static_assert(TTN % 2 == 0, "b's two register sets alternate across stages");
 #pragma unroll
     for (int i = 0; i < NB; ++i)
@@ -221,17 +218,7 @@ __device__ __attribute__((always_inline)) inline void tile(const TileParams &T, 
     auto scale = [&](int h, int kb) {
         return *reinterpret_cast<const __attribute__((address_space(4))) float *>((uintptr_t)(ws[h] + kb));
     };
-    float sx[2], f[2] = {0.f, 0.f};
     float sw[2] = {scale(0, 0), scale(1, 0)}, swn[2] = {0.f, 0.f};
-    float4v p[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-        p[r] = float4v{0.f, 0.f, 0.f, 0.f};
-    auto add = [&](int r, int c) {  // the product in p[r] is tile c's
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            acc[r][c][i] = __builtin_fmaf(p[r][i], f[r >> 1], acc[r][c][i]);
-    };
     auto turn = [&](int kb, uint32_t buf) {  // the barrier of stage kb, whose buffer is buf
         const int k1 = min(kb + 1, KB - 1);
         swn[0] = scale(0, k1);
@@ -253,101 +240,135 @@ __device__ __attribute__((always_inline)) inline void tile(const TileParams &T, 
             stage(std::integral_constant<int, 0>{}, kb);
         if (NB > 2 && kb + 1 < KB)
             stage(std::integral_constant<int, 1>{}, kb + 1);
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            add(r, TTN - 1);
         __builtin_amdgcn_s_waitcnt(wait_vm<0>());  // no copy into LDS is left when it is used again
     };
 
     if constexpr (EXACT) {
-        // 16 fp16 MFMAs a step, column quarter by quarter; the next token tile is
-        // converted between them, and in the stage's last step the next stage's weights,
-        // each quarter once its last MFMA has been sent.
-        Frag16 a[4], b[2];
-        Frag8 ra[4], rb;
+        // Quarter q of a stage: the 32 columns of one fp16 MFMA for all 4 x TTN products,
+        // whose sums over the four quarters stay in p.  Between the MFMAs, one conversion
+        // for each: the next token tile's quarter, and the next quarter of the weights
+        // (the vector unit would otherwise be idle in the 16 clocks of an MFMA, and a run
+        // of conversions would leave the matrix unit idle).  A fragment's register is read
+        // again right after its last conversion, 4 TTN MFMAs before it is needed.
+        u32x4 a[2][4], b[2], ra[4], rb[TTN];
+        float4v p[4][TTN];
+        float sx[TTN], swp[2] = {0.f, 0.f};  // of the products in p
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-            a[r] = to_frag16(read_a(bufs[0], r));
-        b[0] = to_frag16(read_b(bufs[0], 0));
-        rb = read_b(bufs[0], 1);
-        sx[0] = read_sx(bufs[0], 0);
-        sx[1] = read_sx(bufs[0], 1);
+        for (int r = 0; r < 4; ++r) {
+            ra[r] = read_a(bufs[0], r, 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                a[0][r][i] = half2_of(ra[r], 0, i);
+        }
+#pragma unroll
+        for (int c = 0; c < TTN; ++c) {
+            rb[c] = read_b(bufs[0], c, 0);
+            sx[c] = 0.f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                p[r][c] = float4v{0.f, 0.f, 0.f, 0.f};
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            b[0][i] = half2_of(rb[0], 0, i);
+        auto add = [&](int r, int c) {
+            const float f = sx[c] * swp[r >> 1];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                acc[r][c][i] = __builtin_fmaf(p[r][c][i], f, acc[r][c][i]);
+        };
         auto stage = [&](auto par, int kb) {
             constexpr int Q = decltype(par)::value;  // buffer of this stage
             const At &sb = bufs[Q], &sn = bufs[(Q + 1) % NB];
 #pragma unroll
-            for (int c = 0; c < TTN; ++c) {
-                if (c == TTN - 2) {
+            for (int q = 0; q < 4; ++q) {
+                if (q == 2)
                     turn(kb, Q * kBuffer);
-                    ra[0] = read_a(sn, 0);
-                    ra[1] = read_a(sn, 1);
-                }
-                if (c == TTN - 1) {
-                    ra[2] = read_a(sn, 2);
-                    ra[3] = read_a(sn, 3);
-                }
-                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (k > 0)
-                        b[(c + 1) % 2].k[k - 1] = quarter(rb, k - 1);
+                for (int c = 0; c < TTN; ++c) {
+                    const int cur = (q * TTN + c) % 2;
+                    const int nc = (c + 1) % TTN, nq = c + 1 < TTN ? q : q + 1;  // the next token fragment
+                    constexpr int kA = 4 / TTN > 1 ? 4 / TTN : 1;                 // weight tiles converted beside c
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        if (k == 0) {
-                            add(r, c == 0 ? TTN - 1 : c - 1);
-                            p[r] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[r].k[0], b[c % 2].k[0],
-                                                                          float4v{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+                        const half8 av = __builtin_bit_cast(half8, a[q % 2][r]), bv = __builtin_bit_cast(half8, b[cur]);
+                        if (q == 0) {
+                            add(r, c);
+                            p[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(av, bv, float4v{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
                         } else {
-                            p[r] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[r].k[k], b[c % 2].k[k], p[r], 0, 0, 0);
-                            if (c == TTN - 1)
-                                a[r].k[k - 1] = quarter(ra[r], k - 1);
+                            p[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(av, bv, p[r][c], 0, 0, 0);
                         }
+                        b[1 - cur][r] = half2_of(rb[nc], nq % 2, r);
+#pragma unroll
+                        for (int w = 0; w < kA; ++w)
+                            if (kA * c + w < 4)
+                                a[(q + 1) % 2][kA * c + w][r] = half2_of(ra[kA * c + w], (q + 1) % 2, r);
+                        __builtin_amdgcn_sched_barrier(0);
                     }
+                    // fragments whose two quarters are converted: the next half, of this
+                    // stage or the next
+                    if (nq % 2 == 1)
+                        rb[nc] = nq == 1 ? read_b(sb, nc, 1) : read_b(sn, nc, 0);
+                    if (q % 2 == 0) {
+#pragma unroll
+                        for (int w = 0; w < kA; ++w)
+                            if (kA * c + w < 4)
+                                ra[kA * c + w] = q == 0 ? read_a(sb, kA * c + w, 1) : read_a(sn, kA * c + w, 0);
+                    }
+                    if (q == 1)
+                        sx[c] = read_sx(sb, c);
                     __builtin_amdgcn_sched_barrier(0);
                 }
-                b[(c + 1) % 2].k[3] = quarter(rb, 3);
-                if (c == TTN - 1) {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        a[r].k[3] = quarter(ra[r], 3);
-                }
-                f[0] = sx[c % 2] * sw[0];
-                f[1] = sx[c % 2] * sw[1];
-                const At &from = c + 2 < TTN ? sb : sn;
-                rb = read_b(from, (c + 2) % TTN);
-                sx[c % 2] = read_sx(from, (c + 2) % TTN);
             }
+            swp[0] = sw[0];
+            swp[1] = sw[1];
             sw[0] = swn[0];
             sw[1] = swn[1];
         };
         run(stage);
-    } else {
-        // Each MFMA is preceded by the four additions of the product that its registers
-        // held; b is read a step ahead.
-        Frag8 a[NB][2], a2[2], b[2];  // weight tiles 0, 1 in a set for each buffer; 2, 3 in one
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-            (r < 2 ? a[0][r] : a2[r - 2]) = read_a(bufs[0], r);
-        b[0] = read_b(bufs[0], 0);
+#pragma unroll
+            for (int c = 0; c < TTN; ++c)
+                add(r, c);
+    } else {
+        // Step c multiplies token tile c by the four weight tiles.  Each MFMA is preceded
+        // by the four additions of the product that its registers held; b is read a step
+        // ahead.
+        Frag8 a[NB][2], a2[2], b[2];  // weight tiles 0, 1 in a set for each buffer; 2, 3 in one
+        float4v p[4];
+        float sx[2], f[2] = {0.f, 0.f};
+        auto frag_a = [&](const At &v, int r) { return Frag8{read_a(v, r, 0), read_a(v, r, 1)}; };
+        auto frag_b = [&](const At &v, int c) { return Frag8{read_b(v, c, 0), read_b(v, c, 1)}; };
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            (r < 2 ? a[0][r] : a2[r - 2]) = frag_a(bufs[0], r);
+            p[r] = float4v{0.f, 0.f, 0.f, 0.f};
+        }
+        b[0] = frag_b(bufs[0], 0);
         sx[0] = read_sx(bufs[0], 0);
+        auto add = [&](int r, int c) {  // the product in p[r] is tile c's
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                acc[r][c][i] = __builtin_fmaf(p[r][i], f[r >> 1], acc[r][c][i]);
+        };
         auto stage = [&](auto par, int kb) {
             constexpr int Q = decltype(par)::value;  // buffer of this stage
             const At &sb = bufs[Q], &sn = bufs[(Q + 1) % NB];
 #pragma unroll
             for (int c = 0; c < TTN; ++c) {
-                const At &from = c + 1 < TTN ? sb : sn;
-                if (c + 1 < TTN) {  // (before the barrier in step TTN - 2)
-                    b[(c + 1) % 2] = read_b(sb, c + 1);
+                if (c + 1 < TTN) {  // (in step TTN - 2: before the turn)
+                    b[(c + 1) % 2] = frag_b(sb, c + 1);
                     sx[(c + 1) % 2] = read_sx(sb, c + 1);
                 }
                 if (c == TTN - 2)
                     turn(kb, Q * kBuffer);
                 if (c + 1 == TTN) {
-                    b[0] = read_b(from, 0);
-                    sx[0] = read_sx(from, 0);
+                    b[0] = frag_b(sn, 0);
+                    sx[0] = read_sx(sn, 0);
                 }
                 if (c >= TTN - 2)
-                    a[(Q + 1) % NB][c + 2 - TTN] = read_a(sn, c + 2 - TTN);
+                    a[(Q + 1) % NB][c + 2 - TTN] = frag_a(sn, c + 2 - TTN);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
@@ -355,7 +376,7 @@ __device__ __attribute__((always_inline)) inline void tile(const TileParams &T, 
                     p[r] = block_product(r < 2 ? a[Q][r] : a2[r - 2], b[c % 2]);
                     __builtin_amdgcn_sched_barrier(0);
                     if (r >= 2 && c == TTN - 1)
-                        a2[r - 2] = read_a(sn, r);
+                        a2[r - 2] = frag_a(sn, r);
                 }
                 f[0] = sx[c % 2] * sw[0];
                 f[1] = sx[c % 2] * sw[1];
@@ -364,6 +385,9 @@ __device__ __attribute__((always_inline)) inline void tile(const TileParams &T, 
             sw[1] = swn[1];
         };
         run(stage);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            add(r, TTN - 1);
     }
 
     // ---- epilogue
@@ -430,12 +454,9 @@ __device__ __attribute__((always_inline)) inline void tile(const TileParams &T, 
     }
 }
 
-#ifndef EXTOK
-#define EXTOK 128
-#endif
 // Tokens of a tile.  fp16 fragments take twice the registers: 128 tokens (EXTOK).
 template <bool EXACT>
-constexpr int kTileTok = EXACT ? EXTOK : 256;
+constexpr int kTileTok = EXACT ? 128 : 256;
 
 template <bool EXACT, bool ACT>
 __global__ void __launch_bounds__(kThreads) fp8_tile_kernel(const TileParams T)
@@ -452,8 +473,8 @@ __global__ void __launch_bounds__(kThreads) fp8_tile_kernel(const TileParams T)
     t.m0 = __builtin_amdgcn_readfirstlane(t.m0);
     t.M = __builtin_amdgcn_readfirstlane(t.M);
     t.nt = __builtin_amdgcn_readfirstlane(t.nt);
-    if (kTileTok<EXACT> > 128 && t.M > 128)
-        tile<EXACT, ACT, (kTileTok<EXACT> > 128 ? kTileTok<EXACT> / 32 : 2)>(T, t, smem);
+    if (!EXACT && t.M > 128)
+        tile<EXACT, ACT, EXACT ? 2 : 8>(T, t, smem);
     else if (t.M > 64)
         tile<EXACT, ACT, 4>(T, t, smem);
     else
