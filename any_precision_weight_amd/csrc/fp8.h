@@ -104,6 +104,11 @@ __device__ inline float4v block_product(const Frag8 &a, const Frag8 &b)
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v(a), v(b), float4v{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
 }
 
+__device__ inline float lds_f32(uint32_t addr)
+{
+    return *reinterpret_cast<const __attribute__((address_space(3))) float *>((uintptr_t)addr);
+}
+
 // Magnitude as an unsigned integer: ordered as the magnitudes are, an infinity above
 // every number and a NaN above that, so an integer maximum passes both on (the float
 // maximum drops a NaN).
