@@ -110,7 +110,11 @@ __device__ inline const uint8_t *scalar_ptr(const uint8_t *p)
 }
 
 // The stages of one tile: their copies into LDS, the weights' scales, the turns.
-template <bool ACT, int TOK>
+// The copies of a stage are sent one by one between the products: a CU takes about 50
+// clocks for each, and a wave whose request finds no room waits with everything behind it.
+// Steps are counted from a turn to the next; a step sends EACH requests, every EVERY-th
+// step, until all are sent.  POST: steps between a turn and the stage's end.
+template <bool ACT, int TOK, int EACH, int EVERY, int POST>
 struct Stages {
     static constexpr uint32_t kStage = Lds<TOK>::kStage, kBuffer = Lds<TOK>::kBuffer;
     static constexpr int NB = Lds<TOK>::NB;
@@ -164,30 +168,42 @@ struct Stages {
         sw[1] = scale(1, 0);
     }
 
-    __device__ inline void copy(int kb, uint32_t buf) const
+    // Request i of stage kb into buffer number q.
+    __device__ __attribute__((always_inline)) inline void copy(int i, int kb, int q) const
     {
-        char *dst = smem + buf;
+        char *dst = smem + q * kBuffer;
         // K's last block may be shorter: zeros there, for the weights by an offset out of
         // range, for the tokens from kZeros
         const bool in = kb * kBlk + 16 * chunk < K;
-        const uint64_t pick = in ? ~0ull : 0ull, zeros = (uint64_t)(uintptr_t)&kZeros;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                    rw[h], (__attribute__((address_space(3))) void *)(dst + h * kHalf * kBlk + (64 * i + 8 * wave) * kBlk), 16,
-                    in ? woff[i] : 0x80000000u, (uint32_t)kb * kBlk, 0, 0);
-#pragma unroll
-        for (int i = 0; i < kXi; ++i) {
-            const uint64_t src = (uint64_t)(uintptr_t)(x8 + (uint32_t)kb * kBlk + 16 * chunk) + (uint64_t)xrow[i] * (uint32_t)K;
+        if (i < 4) {
+            const int h = i / 2, u = i % 2;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rw[h], (__attribute__((address_space(3))) void *)(dst + h * kHalf * kBlk + (64 * u + 8 * wave) * kBlk), 16,
+                in ? woff[u] : 0x80000000u, (uint32_t)kb * kBlk, 0, 0);
+        } else if (i < 4 + kXi) {
+            const int u = i - 4;
+            const uint64_t pick = in ? ~0ull : 0ull, zeros = (uint64_t)(uintptr_t)&kZeros;
+            const uint64_t src = (uint64_t)(uintptr_t)(x8 + (uint32_t)kb * kBlk + 16 * chunk) + (uint64_t)xrow[u] * (uint32_t)K;
             __builtin_amdgcn_global_load_lds(
                 (const __attribute__((address_space(1))) void *)(uintptr_t)((src & pick) | (zeros & ~pick)),
-                (__attribute__((address_space(3))) void *)(dst + kStageW + (64 * i + 8 * wave) * kBlk), 16, 0, 0);
+                (__attribute__((address_space(3))) void *)(dst + kStageW + (64 * u + 8 * wave) * kBlk), 16, 0, 0);
+        } else {
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(xsp + kb),
+                                             (__attribute__((address_space(3))) void *)(dst + kStage + srow * 256), 4, 0, 0);
         }
-        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(xsp + kb),
-                                         (__attribute__((address_space(3))) void *)(dst + kStage + srow * 256), 4, 0, 0);
     }
+
+    // Step `st` after the turn of stage kb in buffer q: its share of the copies of stage
+    // kb + NB into that buffer.  Before a stage's own turn, the steps are those after the
+    // turn of the stage before it.
+    __device__ __attribute__((always_inline)) inline void step(int st, int kb, int q) const
+    {
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i)
+            if (st % EVERY == 0 && i / EACH == st / EVERY)
+                copy(i, min(kb + NB, KB - 1), q);
+    }
+    static constexpr int kPost = (POST + EVERY - 1) / EVERY * EACH < kCopies ? (POST + EVERY - 1) / EVERY * EACH : kCopies;
 
     // A scalar load: complete, with the LDS reads, at the next turn.
     __device__ inline float scale(int h, int kb) const
@@ -195,18 +211,21 @@ struct Stages {
         return *reinterpret_cast<const __attribute__((address_space(4))) float *>((uintptr_t)(ws[h] + kb));
     }
 
+    // The first stages; of the last buffer's, what a turn would have sent.
     __device__ __attribute__((always_inline)) inline void begin() const
     {
 #pragma unroll
-        for (int i = 0; i < NB; ++i)
-            copy(min(i, KB - 1), i * kBuffer);
-        __builtin_amdgcn_s_waitcnt(wait_vm<(NB - 1) * kCopies>());
+        for (int q = 0; q < NB; ++q)
+#pragma unroll
+            for (int i = 0; i < (q + 1 < NB ? kCopies : kPost); ++i)
+                copy(i, min(q, KB - 1), q);
+        __builtin_amdgcn_s_waitcnt(wait_vm<(NB - 2) * kCopies + kPost>());
         asm volatile("s_barrier" ::: "memory");
     }
 
-    // Every read of stage kb, in buffer buf, has been sent: waits for them and for the next
-    // stage, and starts the copies of the stage that takes the buffer.
-    __device__ __attribute__((always_inline)) inline void turn(int kb, uint32_t buf)
+    // Every read of stage kb has been sent: waits for them and for the next stage (all but
+    // the last NB - 2 stages' copies have landed).
+    __device__ __attribute__((always_inline)) inline void turn(int kb)
     {
         const int k1 = min(kb + 1, KB - 1);
         swn[0] = scale(0, k1);
@@ -214,7 +233,6 @@ struct Stages {
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_waitcnt(wait_vm<(NB - 2) * kCopies>());
         asm volatile("s_barrier" ::: "memory");
-        copy(min(kb + NB, KB - 1), buf);
     }
 
     // stage(buffer number as a constant, kb) for every block.
@@ -243,7 +261,7 @@ __device__ __attribute__((always_inline)) inline void tile_fast(const TileParams
 {
     static_assert(TTN % 2 == 0, "b's two register sets alternate across stages");
     const Fp8Params &P = T.p;
-    typedef Stages<false, 32 * TTN> S;
+    typedef Stages<false, 32 * TTN, TTN == 2 ? 3 : 2, 1, 2> S;
     constexpr int NB = S::NB;
     S s(T, t, smem);
     const int lane = threadIdx.x % kWave, wr = s.wave & 3, wt = s.wave >> 2;
@@ -307,13 +325,17 @@ __device__ __attribute__((always_inline)) inline void tile_fast(const TileParams
                 sx[(c + 1) % 2] = read_sx(sb, c + 1);
             }
             if (c == TTN - 2)
-                s.turn(kb, Q * S::kBuffer);
+                s.turn(kb);
             if (c + 1 == TTN) {
                 b[0] = read_b(sn, 0);
                 sx[0] = read_sx(sn, 0);
             }
             if (c >= TTN - 2)
                 a[(Q + 1) % NB][c + 2 - TTN] = read_a(sn, c + 2 - TTN);
+            if (c >= TTN - 2)
+                s.step(c + 2 - TTN, kb, Q);
+            else
+                s.step(c + 2, kb - 1, (Q + NB - 1) % NB);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
@@ -359,7 +381,7 @@ __device__ __attribute__((always_inline)) inline void tile_exact(const TileParam
 {
     const Fp8Params &P = T.p;
     constexpr int TOK = 64 * TB;
-    typedef Stages<ACT, TOK> S;
+    typedef Stages<ACT, TOK, 1, TB, 2 * TB> S;
     constexpr int NB = S::NB;
     S s(T, t, smem);
     const int lane = threadIdx.x % kWave, wr = s.wave & 3, wt = s.wave >> 2;
@@ -430,7 +452,7 @@ __device__ __attribute__((always_inline)) inline void tile_exact(const TileParam
             // chunk h is read when chunk h - 1 has been converted: the stage's last reads are
             // sent in eighth 5 (b: 2h + 1 = 5 reads chunk 3)
             if (q == 6)
-                s.turn(kb, Q * S::kBuffer);
+                s.turn(kb);
 #pragma unroll
             for (int c = 0; c < TB; ++c) {
                 const int cur = (q * TB + c) % 2;
@@ -466,6 +488,10 @@ __device__ __attribute__((always_inline)) inline void tile_exact(const TileParam
                 }
                 if (q == 1)
                     sx[c] = lds_f32(sb.s + 128u * c);
+                if (q >= 6)
+                    s.step((q - 6) * TB + c, kb, Q);
+                else
+                    s.step((q + 2) * TB + c, kb - 1, (Q + NB - 1) % NB);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
