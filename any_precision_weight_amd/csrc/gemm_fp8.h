@@ -38,24 +38,34 @@ __device__ inline float silu_mul32(float g, float u)
     return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
 }
 
+// Four outputs in the product's type: 16 bytes, or the lower 8 of them.
+__device__ inline u32x4 pack4(int dtype, const float4v &v)
+{
+    if (dtype == APMOE_F32)
+        return __builtin_bit_cast(u32x4, v);
+    u32x4 o = {0, 0, 0, 0};
+    if (dtype == APMOE_F16) {
+        const half4 h = {(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
+        const u32x2 b = __builtin_bit_cast(u32x2, h);
+        o[0] = b[0];
+        o[1] = b[1];
+    } else {
+        o[0] = to_bf16(v[0]) | (uint32_t)to_bf16(v[1]) << 16;
+        o[1] = to_bf16(v[2]) | (uint32_t)to_bf16(v[3]) << 16;
+    }
+    return o;
+}
+
 // Four consecutive outputs of a row, those below N.
 __device__ inline void store4(const Fp8Params &P, size_t row, int n, const float4v &v)
 {
     const size_t at = row * (size_t)P.N + n;
+    const u32x4 o = pack4(P.out_dtype, v);
     if (n + 4 <= P.N && P.N % 4 == 0) {
-        if (P.out_dtype == APMOE_F32) {
-            *reinterpret_cast<float4v *>(static_cast<float *>(P.out) + at) = v;
-        } else {
-            u32x2 o;
-            if (P.out_dtype == APMOE_F16) {
-                const half4 h = {(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
-                o = __builtin_bit_cast(u32x2, h);
-            } else {
-                o[0] = to_bf16(v[0]) | (uint32_t)to_bf16(v[1]) << 16;
-                o[1] = to_bf16(v[2]) | (uint32_t)to_bf16(v[3]) << 16;
-            }
-            *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(P.out) + at) = o;
-        }
+        if (P.out_dtype == APMOE_F32)
+            *reinterpret_cast<u32x4 *>(static_cast<float *>(P.out) + at) = o;
+        else
+            *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(P.out) + at) = u32x2{o[0], o[1]};
         return;
     }
 #pragma unroll
@@ -63,11 +73,9 @@ __device__ inline void store4(const Fp8Params &P, size_t row, int n, const float
         if (n + i >= P.N)
             break;
         if (P.out_dtype == APMOE_F32)
-            static_cast<float *>(P.out)[at + i] = v[i];
-        else if (P.out_dtype == APMOE_F16)
-            static_cast<_Float16 *>(P.out)[at + i] = (_Float16)v[i];
+            static_cast<uint32_t *>(P.out)[at + i] = o[i];
         else
-            static_cast<uint16_t *>(P.out)[at + i] = to_bf16(v[i]);
+            static_cast<uint16_t *>(P.out)[at + i] = (uint16_t)(o[i / 2] >> (16 * (i % 2)));
     }
 }
 

@@ -39,6 +39,7 @@ struct Lds {
 };
 constexpr uint32_t kLds = 3 * Lds<128>::kBuffer;
 static_assert(kLds >= 2 * Lds<256>::kBuffer && kLds <= 160 * 1024, "LDS of a workgroup");
+static_assert(kLds >= 256 * (512 + 16) && kLds >= 128 * (1024 + 16), "the output rows fit");
 
 __device__ const u32x4 kZeros = {0, 0, 0, 0};
 
@@ -254,6 +255,52 @@ struct Stages {
     }
 };
 
+// Rows of `bytes` bytes on their way out through LDS: a product's lane has 4 values of 16
+// or 32 tokens, and stored from there a request would touch 16 or more lines (12 us a
+// tile); from LDS it covers whole ones.
+constexpr uint32_t kRowPad = 16;
+
+__device__ __attribute__((always_inline)) inline void store_rows(const char *smem, uint32_t bytes, int rows, char *out,
+                                                                size_t stride, int valid)
+{
+    const int per = (int)bytes / 16;
+    for (int c = threadIdx.x; c < rows * per; c += kThreads) {
+        const int r = c / per, b = c % per * 16;
+        if (b < valid)
+            *reinterpret_cast<u32x4 *>(out + (size_t)r * stride + b) =
+                *reinterpret_cast<const u32x4 *>(smem + (uint32_t)r * (bytes + kRowPad) + b);
+    }
+}
+
+// The product's tile: put(f) calls f(token, row of the tile, four values) for what the
+// lane holds.
+template <typename F>
+__device__ __attribute__((always_inline)) inline void store_product(const Fp8Params &P, const Tile &t, char *smem, F &&put)
+{
+    const int size = P.out_dtype == APMOE_F32 ? 4 : 2;
+    const int n0 = t.nt * 2 * kHalf;
+    if (P.N * size % 16 != 0) {  // rows that do not start on 16 bytes
+        put([&](int tok, int n, const float4v &v) {
+            if (tok < t.M && n0 + n < P.N)
+                store4(P, (size_t)(t.r0 + t.m0 + tok), n0 + n, v);
+        });
+        return;
+    }
+    const uint32_t bytes = 2u * kHalf * (uint32_t)size;
+    __syncthreads();  // the last stage is read
+    put([&](int tok, int n, const float4v &v) {
+        char *at = smem + (uint32_t)tok * (bytes + kRowPad) + (uint32_t)(n * size);
+        const u32x4 o = pack4(P.out_dtype, v);
+        if (size == 4)
+            *reinterpret_cast<u32x4 *>(at) = o;
+        else
+            *reinterpret_cast<u32x2 *>(at) = u32x2{o[0], o[1]};
+    });
+    __syncthreads();
+    store_rows(smem, bytes, t.M, static_cast<char *>(P.out) + ((size_t)(t.r0 + t.m0) * P.N + n0) * size,
+               (size_t)P.N * size, (P.N - n0) * size);
+}
+
 // 4 weight tiles x TTN token tiles of 16 a wave, one e4m3 MFMA and four additions each
 // for a block.  Lane l has token l % 16 and weight rows 4 (l / 16) .. + 3 of a product.
 template <int TTN>
@@ -355,18 +402,13 @@ __device__ __attribute__((always_inline)) inline void tile_fast(const TileParams
     for (int r = 0; r < 4; ++r)
         add(r, TTN - 1);
 
+    store_product(P, t, smem, [&](auto &&put) {
 #pragma unroll
-    for (int c = 0; c < TTN; ++c) {
-        const int tok = wt * 16 * TTN + 16 * c + j;
-        if (tok < t.M) {
+        for (int c = 0; c < TTN; ++c)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int n = s.row[r >> 1] + 32 * wr + 16 * (r & 1) + 4 * g;
-                if (n < P.N)
-                    store4(P, (size_t)(t.r0 + t.m0 + tok), n, acc[r][c]);
-            }
-        }
-    }
+            for (int r = 0; r < 4; ++r)
+                put(wt * 16 * TTN + 16 * c + j, (r >> 1) * kHalf + 32 * wr + 16 * (r & 1) + 4 * g, acc[r][c]);
+    });
 }
 
 // 2 weight tiles (one of each half) x TB token tiles of 32 a wave.  Lane l has token
@@ -508,7 +550,8 @@ __device__ __attribute__((always_inline)) inline void tile_exact(const TileParam
 
     if constexpr (ACT) {
         const int fb = (P.F + kBlk - 1) / kBlk, f0 = t.nt * kHalf + 32 * wr + 4 * g;
-        uint32_t *amax = reinterpret_cast<uint32_t *>(smem);  // [4 row groups][TOK]
+        uint32_t *amax = reinterpret_cast<uint32_t *>(smem);  // [4 row groups][TOK], then the 8-bit rows
+        char *out8 = smem + 4 * TOK * sizeof(uint32_t);
         __syncthreads();                                      // the last stage is read
 #pragma unroll
         for (int c = 0; c < TB; ++c) {
@@ -532,34 +575,27 @@ __device__ __attribute__((always_inline)) inline void tile_exact(const TileParam
             for (int w = 0; w < 4; ++w)
                 mx = max(mx, amax[w * TOK + tok]);
             const float sc = scale_of(mx), inv = 1.0f / sc;
-            if (tok < t.M) {
-                const size_t orow = (size_t)(t.r0 + t.m0 + tok);
 #pragma unroll
-                for (int v = 0; v < 16; v += 4)
-                    if (f0 + 2 * v < P.F)
-                        *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(P.out) + orow * P.F + f0 + 2 * v) =
-                            to_e4m3x4(acc[0][c][v] * inv, acc[0][c][v + 1] * inv, acc[0][c][v + 2] * inv,
-                                      acc[0][c][v + 3] * inv);
-                if (wr == 0 && g == 0)
-                    P.os[orow * fb + t.nt] = sc;
-            }
+            for (int v = 0; v < 16; v += 4)
+                *reinterpret_cast<uint32_t *>(out8 + (uint32_t)tok * (kHalf + kRowPad) + 32 * wr + 4 * g + 2 * v) =
+                    to_e4m3x4(acc[0][c][v] * inv, acc[0][c][v + 1] * inv, acc[0][c][v + 2] * inv, acc[0][c][v + 3] * inv);
+            if (tok < t.M && wr == 0 && g == 0)
+                P.os[(size_t)(t.r0 + t.m0 + tok) * fb + t.nt] = sc;
         }
+        __syncthreads();
+        store_rows(out8, kHalf, t.M, static_cast<char *>(P.out) + (size_t)(t.r0 + t.m0) * P.F + t.nt * kHalf, P.F,
+                   P.F - t.nt * kHalf);
     } else {
+        store_product(P, t, smem, [&](auto &&put) {
 #pragma unroll
-        for (int c = 0; c < TB; ++c) {
-            const int tok = wt * 32 * TB + 32 * c + i;
-            if (tok < t.M) {
+            for (int c = 0; c < TB; ++c)
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
 #pragma unroll
-                    for (int v = 0; v < 16; v += 4) {
-                        const int n = s.row[r] + 32 * wr + 2 * v + 4 * g;
-                        if (n < P.N)
-                            store4(P, (size_t)(t.r0 + t.m0 + tok), n,
-                                   float4v{acc[r][c][v], acc[r][c][v + 1], acc[r][c][v + 2], acc[r][c][v + 3]});
-                    }
-            }
-        }
+                    for (int v = 0; v < 16; v += 4)
+                        put(wt * 32 * TB + 32 * c + i, r * kHalf + 32 * wr + 4 * g + 2 * v,
+                            float4v{acc[r][c][v], acc[r][c][v + 1], acc[r][c][v + 2], acc[r][c][v + 3]});
+        });
     }
 }
 
