@@ -137,17 +137,23 @@ __device__ inline void write_choices(const FewParams &P, const double *zs, const
 }
 
 // blockIdx.x: part of F, blockIdx.y: slot of the active experts; one more y for the
-// choices.  NW = 8 waves hold a group of 128 values and quantise it (a8, as); with
-// NW = 2 the workgroups are four times as many, each with 32 values, stored in fp32
-// (a32) and quantised by few_down.
-template <int NW, bool FUSED>
-__global__ void __launch_bounds__(NW *kWave) few_gate_up(const FewParams P)
+// choices.  A wave holds NP pairs of a gate and an up tile of 16 rows.  NW = 4 waves with
+// two pairs hold a group of 128 values and quantise it (a8, as): three such workgroups
+// fit a CU, so 4 tokens' 5 or 6 active experts of the Mixtral shape (560 to 672
+// workgroups) run at once, where 8 waves with one pair took another round for a part of
+// them (190 -> 184 us a layer).  With NW = 2 and one pair the workgroups are four times
+// as many, each with 32 values, stored in fp32 (a32) and quantised by few_down.  (Also
+// measured: four waves sharing a pair's columns, quantised by the last workgroup of a
+// group: slower, each workgroup pays for its selection, 133 -> 147 us.)
+template <int NW, int NP, bool FUSED>
+__global__ void __launch_bounds__(NW *kWave, NP == 2 ? 3 : 4) few_gate_up(const FewParams P)
 {
     extern __shared__ __attribute__((aligned(16))) char smem[];
     double *zs = reinterpret_cast<double *>(smem);
     __shared__ int ids[kFewTokens * APMOE_MAX_ASSIGN];
     __shared__ int flags[APMOE_MAX_EXPERTS];
     __shared__ uint32_t amax[NW * 16];
+    constexpr int kFw = 16 * NP;  // values of F of a wave
     constexpr int NT = NW * kWave;
     const int tid = threadIdx.x, lane = tid % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -185,55 +191,67 @@ __global__ void __launch_bounds__(NW *kWave) few_gate_up(const FewParams P)
     const int j = lane & 15, g = lane >> 4;
     const uint32_t woff = 16u * line_chunk(j, g);
     const int F = P.F, K = P.H, KB = (K + kBlk - 1) / kBlk, fb = (F + kBlk - 1) / kBlk;
-    const int fw = ((int)blockIdx.x * NW + wave) * 16;
-    const int fc = min(fw, F - 16);  // F is a multiple of 16
-    const uint8_t *wbase[2], *xr[1];
-    uint32_t wo[2][2];
-    const float *wsc[2], *xsc[1];
+    const int fw = ((int)blockIdx.x * NW + wave) * kFw;
+    const uint8_t *wbase[2 * NP], *xr[1];
+    uint32_t wo[2 * NP][2];
+    const float *wsc[2 * NP], *xsc[1];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        wbase[h] = P.gate_up + ((size_t)e * 2 * F + (size_t)h * F + fc) * K;
-        wo[h][0] = (uint32_t)(j % 8) * (uint32_t)K + woff;
-        wo[h][1] = (uint32_t)(8 + j % 8) * (uint32_t)K + woff;
-        wsc[h] = P.gate_up_s + ((size_t)(2 * e + h) * fb + fc / kBlk) * KB;
+    for (int r = 0; r < 2 * NP; ++r) {  // gate and up tile of each 16 values
+        const int h = r % 2, fc = min(fw + 16 * (r / 2), F - 16);  // F is a multiple of 16
+        wbase[r] = P.gate_up + ((size_t)e * 2 * F + (size_t)h * F + fc) * K;
+        wo[r][0] = (uint32_t)(j % 8) * (uint32_t)K + woff;
+        wo[r][1] = (uint32_t)(8 + j % 8) * (uint32_t)K + woff;
+        wsc[r] = P.gate_up_s + ((size_t)(2 * e + h) * fb + fc / kBlk) * KB;
     }
     const int t = min(j, P.T - 1);
     xr[0] = P.x8 + (size_t)t * K + 16 * g;
     xsc[0] = P.xs + (size_t)t * KB;
-    float4v acc[2][1] = {{float4v{0.f, 0.f, 0.f, 0.f}}, {float4v{0.f, 0.f, 0.f, 0.f}}};
-    stream_product<2, 1, kFewDepth>(wbase, wo, wsc, xr, xsc, 0, KB, K, 16 * g, (int)woff, 4 * wave + (int)blockIdx.x, acc);
+    float4v acc[2 * NP][1];
+#pragma unroll
+    for (int r = 0; r < 2 * NP; ++r)
+        acc[r][0] = float4v{0.f, 0.f, 0.f, 0.f};
+    stream_product<2 * NP, 1, kFewDepth>(wbase, wo, wsc, xr, xsc, 0, KB, K, 16 * g, (int)woff,
+                                         4 * wave + (int)blockIdx.x, acc);
 
     int row = -1;  // this lane's token's assignment to e
     if (j < P.T)
         for (int s = 0; s < P.kt; ++s)
             if (ids[j * P.kt + s] == e)
                 row = j * P.kt + s;
-    float a[4];
+    float4v a[NP];
     uint32_t mx = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        a[i] = silu_mul32(acc[0][0][i], acc[1][0][i]);
-        mx = max(mx, fw < F ? mag(a[i]) : 0u);
-    }
-    if constexpr (NW == kWaves) {
+    for (int p = 0; p < NP; ++p)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[p][i] = silu_mul32(acc[2 * p][0][i], acc[2 * p + 1][0][i]);
+            mx = max(mx, fw + 16 * p < F ? mag(a[p][i]) : 0u);
+        }
+    if constexpr (NW * kFw == kBlk) {
         mx = max(mx, (uint32_t)__shfl_xor((int)mx, 16, kWave));
         mx = max(mx, (uint32_t)__shfl_xor((int)mx, 32, kWave));
         if (g == 0)
             amax[wave * 16 + j] = mx;
         __syncthreads();
-        if (row < 0 || fw >= F)
+        if (row < 0)
             return;
         mx = 0;
 #pragma unroll
         for (int v = 0; v < NW; ++v)
             mx = max(mx, amax[v * 16 + j]);
         const float s = scale_of(mx), inv = 1.0f / s;
-        *reinterpret_cast<uint32_t *>(P.a8 + (size_t)row * F + fw + 4 * g) =
-            to_e4m3x4(a[0] * inv, a[1] * inv, a[2] * inv, a[3] * inv);
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+            if (fw + 16 * p < F)
+                *reinterpret_cast<uint32_t *>(P.a8 + (size_t)row * F + fw + 16 * p + 4 * g) =
+                    to_e4m3x4(a[p][0] * inv, a[p][1] * inv, a[p][2] * inv, a[p][3] * inv);
         if (wave == 0 && g == 0)
             P.as[(size_t)row * fb + blockIdx.x] = s;
-    } else if (row >= 0 && fw < F) {
-        *reinterpret_cast<float4v *>(P.a32 + (size_t)row * F + fw + 4 * g) = float4v{a[0], a[1], a[2], a[3]};
+    } else if (row >= 0) {
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+            if (fw + 16 * p < F)
+                *reinterpret_cast<float4v *>(P.a32 + (size_t)row * F + fw + 16 * p + 4 * g) = a[p];
     }
 }
 
@@ -412,16 +430,16 @@ hipError_t launch_few_layer(FewParams P, hipStream_t s)
     P.slots = few_slots(P.T, P.topk, P.kt, P.Er);
     if (!fused)
         hipLaunchKernelGGL(few_logits, dim3((P.T * P.Er + 3) / 4), dim3(256), 0, s, P);
-    const int nw = quant ? 2 : kWaves;
-    const dim3 grid((P.F + 16 * nw - 1) / (16 * nw), P.slots + 1), block(nw * kWave);
+    const int per = quant ? 32 : kBlk;
+    const dim3 grid((P.F + per - 1) / per, P.slots + 1), block((quant ? 2 : 4) * kWave);
     if (quant && fused)
-        hipLaunchKernelGGL((few_gate_up<2, true>), grid, block, zbytes, s, P);
+        hipLaunchKernelGGL((few_gate_up<2, 1, true>), grid, block, zbytes, s, P);
     else if (quant)
-        hipLaunchKernelGGL((few_gate_up<2, false>), grid, block, zbytes, s, P);
+        hipLaunchKernelGGL((few_gate_up<2, 1, false>), grid, block, zbytes, s, P);
     else if (fused)
-        hipLaunchKernelGGL((few_gate_up<kWaves, true>), grid, block, zbytes, s, P);
+        hipLaunchKernelGGL((few_gate_up<4, 2, true>), grid, block, zbytes, s, P);
     else
-        hipLaunchKernelGGL((few_gate_up<kWaves, false>), grid, block, zbytes, s, P);
+        hipLaunchKernelGGL((few_gate_up<4, 2, false>), grid, block, zbytes, s, P);
     const size_t red = kWaves * 256 * sizeof(float);
     const size_t q = (size_t)P.T * P.kt * ((quant ? P.F : 0) + 4 * ((P.F + kBlk - 1) / kBlk));
     const size_t lds = q > red ? q : red;
