@@ -16,9 +16,10 @@ struct Fp8Params {
     float *os;               // scales of a8
     int E, N, K, topk, gather, out_dtype, R;
     int F;  // with the activation: N = 2 F
+    int stream_max;  // experts of at most so many rows take the stream product, the others the tile product
 };
 
-// Experts of at most kStreamMax rows take the stream product, the others the tile product.
+// Rows of an expert up to which the stream product reads its weights once.
 constexpr int kStreamMax = 32;
 
 __device__ inline void expert_rows(const Fp8Params &P, int e, int &r0, int &m)
@@ -82,6 +83,10 @@ __device__ inline void store4(const Fp8Params &P, size_t row, int n, const float
 // Rows that an expert can have: a token's experts are distinct, so one for each token;
 // a single expert has every row.
 inline int most_rows(const Fp8Params &P) { return P.E == 1 ? P.R : P.R / P.topk; }
+
+// Upper bound of the tile product's workgroups where it takes experts of more than
+// kStreamMax rows: for each of them its tiles of rows, the last one started.
+long fp8_tiles(const Fp8Params &P, bool act, bool exact);
 
 // exact: fp32 sums inside a block (block_product), which fp32 results keep.
 hipError_t launch_fp8_tile(const Fp8Params &P, int most, bool act, bool exact, hipStream_t s);

@@ -10,6 +10,7 @@
 // weight byte read once per 32 rows; a wave holds two 16-row weight tiles, kDepth
 // blocks ahead.  Bound by the weights' bytes.
 #include "gemm_fp8.h"
+#include "launch_fp8.h"
 #include "stream_fp8.h"
 
 namespace apmoe {
@@ -19,8 +20,9 @@ constexpr int kDepth = 2;  // column blocks requested ahead
 constexpr int kStreamWaves = 8;
 constexpr int kStreamRows = 32;  // weight rows of a wave
 
-// blockIdx.x: weight rows, blockIdx.y: expert.  KS waves share a wave's 32 rows, a KS-th
-// of the columns each; their sums meet in LDS in the order of the parts.
+// blockIdx.x: weight rows, blockIdx.y: expert, blockIdx.z: kStreamMax of its rows.  KS waves
+// share a wave's 32 weight rows, a KS-th of the columns each; their sums meet in LDS in the
+// order of the parts.
 template <int KS, int TT>
 __device__ __attribute__((always_inline)) inline void stream_tokens(const Fp8Params &P, int e, int r0, int m,
                                                                    float *red)
@@ -98,35 +100,39 @@ __global__ void __launch_bounds__(kStreamWaves *kWave, TT == 1 ? 4 : 2) stream_k
     const int e = blockIdx.y;
     int r0, m;
     expert_rows(P, e, r0, m);
-    if (m > kStreamMax)
+    if (m > P.stream_max)
         return;  // the tile product's
+    r0 += kStreamMax * (int)blockIdx.z;
+    m = min(m - kStreamMax * (int)blockIdx.z, kStreamMax);
     if (TT == 2 && m > 16)
         stream_tokens<KS, 2>(P, e, r0, m, red);
     else if (m > 0)
         stream_tokens<KS, 1>(P, e, r0, m, red);
 }
 
-// gate_up: wave w holds 16 gate rows and the 16 matching up rows, the workgroup the 128
-// + 128 rows behind one group of 128 values of a8, whose scale needs all of them.
-template <int TT>
+// gate_up: a wave holds NP pairs of a tile of 16 gate rows and the tile of the matching up
+// rows, the workgroup the 128 + 128 rows behind one group of 128 values of a8, whose scale
+// needs all of them.
+template <int TT, int NP>
 __device__ __attribute__((always_inline)) inline void stream_act_tokens(const Fp8Params &P, int e, int r0, int m,
                                                                        uint32_t *amax)
 {
+    constexpr int kWaves = kStreamWaves / NP;
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int j = lane & 15, g = lane >> 4;
     const uint32_t woff = 16u * line_chunk(j, g);
-    const int f0 = (int)blockIdx.x * kBlk, fw = f0 + 16 * wave;
+    const int fw = (int)blockIdx.x * kBlk + 16 * NP * wave;
     const int KB = (P.K + kBlk - 1) / kBlk, fb = (P.F + kBlk - 1) / kBlk;
-    const int fc = min(fw, P.F - 16);  // F is a multiple of 16
-    const uint8_t *wbase[2], *xr[TT];
-    uint32_t wo[2][2];
-    const float *wsc[2], *xsc[TT];
+    const uint8_t *wbase[2 * NP], *xr[TT];
+    uint32_t wo[2 * NP][2];
+    const float *wsc[2 * NP], *xsc[TT];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        wbase[h] = P.w8 + ((size_t)e * P.N + (size_t)h * P.F + fc) * P.K;
-        wo[h][0] = (uint32_t)(j % 8) * (uint32_t)P.K + woff;
-        wo[h][1] = (uint32_t)(8 + j % 8) * (uint32_t)P.K + woff;
-        wsc[h] = P.ws + ((size_t)(2 * e + h) * fb + blockIdx.x) * KB;
+    for (int r = 0; r < 2 * NP; ++r) {
+        const int h = r % 2, fc = min(fw + 16 * (r / 2), P.F - 16);  // F is a multiple of 16
+        wbase[r] = P.w8 + ((size_t)e * P.N + (size_t)h * P.F + fc) * P.K;
+        wo[r][0] = (uint32_t)(j % 8) * (uint32_t)P.K + woff;
+        wo[r][1] = (uint32_t)(8 + j % 8) * (uint32_t)P.K + woff;
+        wsc[r] = P.ws + ((size_t)(2 * e + h) * fb + blockIdx.x) * KB;
     }
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
@@ -134,60 +140,66 @@ __device__ __attribute__((always_inline)) inline void stream_act_tokens(const Fp
         xr[t] = P.x8 + row * P.K + 16 * g;
         xsc[t] = P.xs + row * KB;
     }
-    float4v acc[2][TT];
+    float4v acc[2 * NP][TT];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int r = 0; r < 2 * NP; ++r)
 #pragma unroll
         for (int t = 0; t < TT; ++t)
-            acc[h][t] = float4v{0.f, 0.f, 0.f, 0.f};
-    stream_product<2, TT, kDepth>(wbase, wo, wsc, xr, xsc, 0, KB, P.K, 16 * g, (int)woff, 4 * wave + (int)blockIdx.x, acc);
-    float a[TT][4];
+            acc[r][t] = float4v{0.f, 0.f, 0.f, 0.f};
+    stream_product<2 * NP, TT, kDepth>(wbase, wo, wsc, xr, xsc, 0, KB, P.K, 16 * g, (int)woff, 4 * wave + (int)blockIdx.x,
+                                       acc);
+    float4v a[NP][TT];
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
         uint32_t mx = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            a[t][i] = silu_mul32(acc[0][t][i], acc[1][t][i]);
-            if (fw + 4 * g + i < P.F)
-                mx = max(mx, mag(a[t][i]));
-        }
+        for (int p = 0; p < NP; ++p)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                a[p][t][i] = silu_mul32(acc[2 * p][t][i], acc[2 * p + 1][t][i]);
+                mx = max(mx, fw + 16 * p < P.F ? mag(a[p][t][i]) : 0u);
+            }
         mx = max(mx, (uint32_t)__shfl_xor((int)mx, 16, kWave));
         mx = max(mx, (uint32_t)__shfl_xor((int)mx, 32, kWave));
         if (g == 0)
-            amax[(wave * 2 + t) * 16 + j] = mx;
+            amax[(wave * TT + t) * 16 + j] = mx;
     }
     __syncthreads();
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
         uint32_t mx = 0;
 #pragma unroll
-        for (int v = 0; v < kStreamWaves; ++v)
-            mx = max(mx, amax[(v * 2 + t) * 16 + j]);
+        for (int v = 0; v < kWaves; ++v)
+            mx = max(mx, amax[(v * TT + t) * 16 + j]);
         const float s = scale_of(mx), inv = 1.0f / s;
         const int tok = 16 * t + j;
-        if (tok < m && fw + 4 * g < P.F) {  // F is a multiple of 16
+        if (tok < m) {
             const size_t row = (size_t)(r0 + tok);
-            *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(P.out) + row * P.F + fw + 4 * g) =
-                to_e4m3x4(a[t][0] * inv, a[t][1] * inv, a[t][2] * inv, a[t][3] * inv);
+#pragma unroll
+            for (int p = 0; p < NP; ++p)
+                if (fw + 16 * p < P.F)
+                    *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(P.out) + row * P.F + fw + 16 * p + 4 * g) =
+                        to_e4m3x4(a[p][t][0] * inv, a[p][t][1] * inv, a[p][t][2] * inv, a[p][t][3] * inv);
             if (wave == 0 && g == 0)
                 P.os[row * fb + blockIdx.x] = s;
         }
     }
 }
 
-template <int TT>
-__global__ void __launch_bounds__(kStreamWaves *kWave, TT == 1 ? 4 : 2) stream_act_kernel(const Fp8Params P)
+template <int TT, int NP>
+__global__ void __launch_bounds__(kStreamWaves / NP *kWave, NP == 2 ? 3 : TT == 1 ? 4 : 2)
+    stream_act_kernel(const Fp8Params P)
 {
-    __shared__ uint32_t amax[kStreamWaves * 2 * 16];
+    __shared__ uint32_t amax[kStreamWaves / NP * TT * 16];
     const int e = blockIdx.y;
     int r0, m;
     expert_rows(P, e, r0, m);
-    if (m > kStreamMax)
+    if (m > P.stream_max)
         return;  // the tile product's
     if (TT == 2 && m > 16)
-        stream_act_tokens<2>(P, e, r0, m, amax);
+        stream_act_tokens<2, NP>(P, e, r0, m, amax);
     else if (m > 0)
-        stream_act_tokens<1>(P, e, r0, m, amax);
+        stream_act_tokens<1, NP>(P, e, r0, m, amax);
 }
 
 }  // namespace
@@ -196,22 +208,31 @@ hipError_t launch_gemm_fp8(const uint8_t *x8, const float *xs, const uint8_t *w8
                            int gather, const int32_t *perm, const int32_t *offsets, int topk, int R, void *out,
                            int out_dtype, bool exact, hipStream_t s)
 {
-    const Fp8Params P{x8, xs, w8, ws, perm, offsets, out, nullptr, E, N, K, topk, gather, out_dtype, R, 0};
+    Fp8Params P{x8, xs, w8, ws, perm, offsets, out, nullptr, E, N, K, topk, gather, out_dtype, R, 0, kStreamMax};
     const int most = most_rows(P);
+    // So few tiles leave most of the device idle, and the stream product, split over K
+    // and over chunks of the rows, fills it although each chunk reads the weights again:
+    // 512 rows of fp32, 2048 x 2048 (32 tiles), 30 us as tiles and 26 as chunks, 1024 rows
+    // (64 tiles) 32 and 44; 512 rows of fp16 (16 tiles) 31 and 26, 1024 rows (32 tiles) 31 and 43.
+    if (most > kStreamMax && fp8_tiles(P, false, exact) <= (exact ? 32 : 16))
+        P.stream_max = most;
+    const unsigned chunks = (unsigned)((most < P.stream_max ? most : P.stream_max) + kStreamMax - 1) / kStreamMax;
     // KS: enough waves to fill the device, 8 on a CU.
     const int active = E < R ? E : R;
-    const long waves = (long)active * ((N + kStreamRows - 1) / kStreamRows);
+    const long waves = (long)active * ((N + kStreamRows - 1) / kStreamRows) * chunks;
     const int KB = (K + kBlk - 1) / kBlk;
     auto go = [&](auto ks) {
         constexpr int KS = decltype(ks)::value;
         const int rows = kStreamWaves / KS * kStreamRows;
-        const dim3 grid((N + rows - 1) / rows, E), block(kStreamWaves * kWave);
+        const dim3 grid((N + rows - 1) / rows, E, chunks), block(kStreamWaves * kWave);
         if (most > 16)
             hipLaunchKernelGGL((stream_kernel<KS, 2>), grid, block, 0, s, P);
         else
             hipLaunchKernelGGL((stream_kernel<KS, 1>), grid, block, 0, s, P);
     };
-    if (waves >= 2048 || KB < 4)
+    if (!offsets && R > P.stream_max)
+        ;  // the one expert is the tile product's
+    else if (waves >= 2048 || KB < 4)
         go(std::integral_constant<int, 1>{});
     else if (waves >= 1024 || KB < 8)
         go(std::integral_constant<int, 2>{});
@@ -227,13 +248,18 @@ hipError_t launch_gemm_act_fp8(const uint8_t *x8, const float *xs, const uint8_t
                                int K, int gather, const int32_t *perm, const int32_t *offsets, int topk, int R,
                                uint8_t *a8, float *as, hipStream_t s)
 {
-    const Fp8Params P{x8, xs, w8, ws, perm, offsets, a8, as, E, 2 * F, K, topk, gather, 0, R, F};
-    const dim3 grid((F + kBlk - 1) / kBlk, E), block(kStreamWaves * kWave);
+    const Fp8Params P{x8, xs, w8, ws, perm, offsets, a8, as, E, 2 * F, K, topk, gather, 0, R, F, kStreamMax};
+    const dim3 grid((F + kBlk - 1) / kBlk, E);
     const int most = most_rows(P);
-    if (most > 16)
-        hipLaunchKernelGGL((stream_act_kernel<2>), grid, block, 0, s, P);
+    // Up to 16 rows four waves with two pairs of tiles each, three workgroups on a CU (16 tokens,
+    // 8 experts of 2 x 14336 x 4096: 172 us, eight waves with one pair 176); more rows have no
+    // registers for that.
+    if (!offsets && R > P.stream_max)
+        ;  // the one expert is the tile product's
+    else if (most > 16)
+        hipLaunchKernelGGL((stream_act_kernel<2, 1>), grid, dim3(kStreamWaves * kWave), 0, s, P);
     else
-        hipLaunchKernelGGL((stream_act_kernel<1>), grid, block, 0, s, P);
+        hipLaunchKernelGGL((stream_act_kernel<1, 2>), grid, dim3(kStreamWaves / 2 * kWave), 0, s, P);
     const hipError_t e = launch_fp8_tile(P, most, true, true, s);
     return e == hipSuccess ? hipGetLastError() : e;
 }

@@ -67,7 +67,7 @@ __device__ inline bool resolve(const TileParams &T, int tok, Tile &t)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int m = o[i + 1] - o[i];
-        n[i] = m > kStreamMax ? (m + tok - 1) / tok : 0;
+        n[i] = m > P.stream_max ? (m + tok - 1) / tok : 0;
         sum += n[i];
     }
     int incl = sum;
@@ -627,18 +627,24 @@ __global__ void __launch_bounds__(kThreads) fp8_tile_kernel(const TileParams T)
 
 }  // namespace
 
-hipError_t launch_fp8_tile(const Fp8Params &P, int most, bool act, bool exact, hipStream_t s)
+static int weight_tiles(const Fp8Params &P, bool act)
 {
-    if (most <= kStreamMax)
-        return hipSuccess;
-    // token tiles: at most one for each `tok` rows, and one more for each served expert
+    return act ? (P.F + kHalf - 1) / kHalf : (P.N + 2 * kHalf - 1) / (2 * kHalf);
+}
+
+long fp8_tiles(const Fp8Params &P, bool act, bool exact)
+{
     const int tok = exact ? kTileTok<true> : kTileTok<false>;
     const int served = P.E < P.R / (kStreamMax + 1) ? P.E : P.R / (kStreamMax + 1);
-    if (served == 0)
+    return ((long)(P.R - served) / tok + served) * weight_tiles(P, act);  // ceil(m / tok) = (m - 1) / tok + 1
+}
+
+hipError_t launch_fp8_tile(const Fp8Params &P, int most, bool act, bool exact, hipStream_t s)
+{
+    if (most <= P.stream_max)
         return hipSuccess;
-    const long MT = (long)(P.R / tok) + served;
-    const TileParams T{P, act ? (P.F + kHalf - 1) / kHalf : (P.N + 2 * kHalf - 1) / (2 * kHalf)};
-    const long grid = (MT * T.NT + kXcds - 1) / kXcds * kXcds;
+    const TileParams T{P, weight_tiles(P, act)};
+    const long grid = (fp8_tiles(P, act, exact) + kXcds - 1) / kXcds * kXcds;
     if (grid > 0x7FFFFFFFl)
         return hipErrorInvalidValue;
     if (act)

@@ -104,16 +104,6 @@ hipError_t launch_gemm_tile(const DevBlock *table, int kind, int E, int N, int K
                             int gather, const int32_t *perm, const int32_t *offsets, int topk, void *out, int out_f32,
                             int act, int R, hipStream_t s);
 
-// The 8-bit path (norm.hip, gemm_fp8.hip): definitions in apmoe.h.
-hipError_t launch_norm(const void *x, int x_dtype, const void *residual, void *h, int res_dtype, const void *gamma,
-                       float eps, int T, int H, void *y, uint8_t *y8, float *ys, hipStream_t s);
-hipError_t launch_gemm_fp8(const uint8_t *x8, const float *xs, const uint8_t *w8, const float *ws, int E, int N, int K,
-                           int gather, const int32_t *perm, const int32_t *offsets, int topk, int R, void *out,
-                           int out_dtype, bool exact, hipStream_t s);
-hipError_t launch_gemm_act_fp8(const uint8_t *x8, const float *xs, const uint8_t *w8, const float *ws, int E, int F,
-                               int K, int gather, const int32_t *perm, const int32_t *offsets, int topk, int R,
-                               uint8_t *a8, float *as, hipStream_t s);
-
 hipError_t launch_act(const uint16_t *h, int R, int F, uint16_t *a, hipStream_t s);
 hipError_t launch_combine(const void *y, int y_f32, const float *w, const int32_t *inv_perm, int T, int topk, int H,
                           uint16_t *out, hipStream_t s);

@@ -2,7 +2,7 @@
 // installed).
 #pragma once
 
-#include "internal.h"
+#include "launch_fp8.h"
 
 namespace apmoe {
 

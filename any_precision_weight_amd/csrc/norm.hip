@@ -4,6 +4,7 @@
 //   h = x + residual (fp32, stored in the residual's type), or x without one;
 //   y = h * gamma / sqrt(mean(h^2) + eps);  y8, s = y in e4m3 with a scale per 128 columns.
 #include "fp8.h"
+#include "launch_fp8.h"
 
 namespace apmoe {
 namespace {

@@ -191,7 +191,10 @@ def sum_bound(K):
 GEMMS = [(1, 1, 1, 1, 16), (1, 1, 1, 128, 128), (1, 1, 1, 33, 144), (3, 2, 4, 129, 240), (8, 1, 1, 256, 1024),
          (16, 2, 8, 200, 528), (17, 1, 1, 64, 2048), (33, 1, 1, 130, 400), (40, 4, 6, 384, 1408), (64, 1, 1, 515, 656),
          (65, 1, 2, 256, 512), (130, 2, 3, 300, 1040), (257, 1, 1, 260, 384), (300, 3, 5, 272, 272),
-         (513, 1, 1, 520, 912), (700, 2, 9, 128, 128), (1000, 1, 2, 600, 1552)]
+         (513, 1, 1, 520, 912), (700, 2, 9, 128, 128), (1000, 1, 2, 600, 1552),
+         # enough tiles for the tile product in each type
+         (33, 1, 1, 8720, 144), (64, 1, 1, 8452, 656), (130, 2, 3, 4360, 528), (257, 1, 1, 4100, 272),
+         (300, 3, 5, 2200, 272), (513, 1, 1, 4099, 1040), (1000, 1, 2, 2600, 912), (2100, 2, 40, 144, 256)]
 
 
 @pytest.mark.parametrize("gather", [False, True])
@@ -239,11 +242,11 @@ def test_gemm_dense_without_offsets():
     assert torch.equal(a, c)
 
 
-@pytest.mark.parametrize("T,E", [(20, 3), (200, 3)])
-def test_gemm_rows_behind_the_last_sequence(T, E):
+@pytest.mark.parametrize("T,E,N", [(20, 3, 144), (200, 3, 144), (200, 3, 2320)])
+def test_gemm_rows_behind_the_last_sequence(T, E, N):
     """offsets that end before T * topk rows: the rows behind stay as they were."""
     r = rng_of("behind", T)
-    N, K, used = 144, 272, T - 7
+    K, used = 272, T - 7
     off = np.array([0, used // 2, used // 2, used], np.int32)
     x8, xs = random_rows(r, T, K)
     w8, ws = random_weights(r, E, 1, N, K)
@@ -257,10 +260,10 @@ def test_gemm_rows_behind_the_last_sequence(T, E):
     assert np.all(np.abs(got[:used] - want) <= mag * sum_bound(K))
 
 
-@pytest.mark.parametrize("T", [5, 70])
-def test_gemm_nan_stays_in_its_row_and_column(T):
+@pytest.mark.parametrize("T,N", [(5, 96), (70, 96), (70, 8464)])
+def test_gemm_nan_stays_in_its_row_and_column(T, N):
     r = rng_of("nan", T)
-    N, K = 96, 400
+    K = 400
     x8, xs = random_rows(r, T, K)
     w8, ws = random_weights(r, 1, 1, N, K)
     x8[2, 390] = 0x7F
@@ -393,8 +396,10 @@ LAYERS = [  # T, E, topk, shared, H, F, renorm, bias
     (1, 4, 2, 0, 256, 512, True, False), (1, 1, 1, 0, 16, 16, True, False), (1, 12, 4, 2, 272, 144, False, True),
     (2, 8, 2, 1, 528, 400, True, True), (3, 60, 8, 4, 256, 208, False, False), (4, 5, 5, 0, 400, 272, True, True),
     (7, 3, 2, 8, 144, 704, False, False), (16, 8, 2, 0, 384, 256, True, False), (17, 8, 2, 1, 384, 256, True, False),
-    (33, 6, 3, 0, 272, 272, False, True), (100, 4, 2, 1, 256, 384, True, True), (16, 200, 8, 1, 128, 64, True, False), (1, 256, 8, 0, 64, 48, False, True), (4, 248, 8, 8, 80, 16, True, True),
-    (16, 8, 8, 8, 64, 272, True, False), (1, 8, 2, 0, 2048, 4096, True, False), (3, 6, 2, 0, 1040, 2064, False, True)]
+    (33, 6, 3, 0, 272, 272, False, True), (100, 4, 2, 1, 256, 384, True, True), (16, 200, 8, 1, 128, 64, True, False),
+    (1, 256, 8, 0, 64, 48, False, True), (4, 248, 8, 8, 80, 16, True, True),
+    (16, 8, 8, 8, 64, 272, True, False), (1, 8, 2, 0, 2048, 4096, True, False), (3, 6, 2, 0, 1040, 2064, False, True),
+    (100, 4, 2, 1, 1040, 272, True, False)]
 
 
 def run_layer(d, bias, E, n_shared, H, F, T, topk, renorm, stream=None):
