@@ -39,7 +39,6 @@ struct Lds {
 };
 constexpr uint32_t kLds = 3 * Lds<128>::kBuffer;
 static_assert(kLds >= 2 * Lds<256>::kBuffer && kLds <= 160 * 1024, "LDS of a workgroup");
-static_assert(kLds >= 256 * (512 + 16) && kLds >= 128 * (1024 + 16), "the output rows fit");
 
 __device__ const u32x4 kZeros = {0, 0, 0, 0};
 
@@ -272,33 +271,42 @@ __device__ __attribute__((always_inline)) inline void store_rows(const char *sme
     }
 }
 
-// The product's tile: put(f) calls f(token, row of the tile, four values) for what the
-// lane holds.
-template <typename F>
+// The product's tile of up to TOK tokens: put(f) calls f(half, token, row of the half, four
+// values) for what the lane holds.  Rows of fp32 are too long for LDS with 256 tokens and
+// leave half by half.
+template <int TOK, typename F>
 __device__ __attribute__((always_inline)) inline void store_product(const Fp8Params &P, const Tile &t, char *smem, F &&put)
 {
     const int size = P.out_dtype == APMOE_F32 ? 4 : 2;
     const int n0 = t.nt * 2 * kHalf;
     if (P.N * size % 16 != 0) {  // rows that do not start on 16 bytes
-        put([&](int tok, int n, const float4v &v) {
-            if (tok < t.M && n0 + n < P.N)
-                store4(P, (size_t)(t.r0 + t.m0 + tok), n0 + n, v);
+        put([&](int h, int tok, int n, const float4v &v) {
+            if (tok < t.M && n0 + h * kHalf + n < P.N)
+                store4(P, (size_t)(t.r0 + t.m0 + tok), n0 + h * kHalf + n, v);
         });
         return;
     }
-    const uint32_t bytes = 2u * kHalf * (uint32_t)size;
-    __syncthreads();  // the last stage is read
-    put([&](int tok, int n, const float4v &v) {
-        char *at = smem + (uint32_t)tok * (bytes + kRowPad) + (uint32_t)(n * size);
-        const u32x4 o = pack4(P.out_dtype, v);
-        if (size == 4)
-            *reinterpret_cast<u32x4 *>(at) = o;
-        else
-            *reinterpret_cast<u32x2 *>(at) = u32x2{o[0], o[1]};
-    });
-    __syncthreads();
-    store_rows(smem, bytes, t.M, static_cast<char *>(P.out) + ((size_t)(t.r0 + t.m0) * P.N + n0) * size,
-               (size_t)P.N * size, (P.N - n0) * size);
+    static_assert(TOK * (2 * kHalf * 2 + kRowPad) <= kLds, "rows of 16-bit values fit");
+    static_assert(TOK * ((TOK <= 128 ? 2 : 1) * kHalf * 4 + kRowPad) <= kLds, "rows of fp32, or their halves, fit");
+    const int halves = TOK <= 128 || size == 2 ? 2 : 1;  // of a pass
+    const uint32_t bytes = (uint32_t)(halves * kHalf * size);
+    for (int h0 = 0; h0 < 2; h0 += halves) {
+        __syncthreads();  // the last stage is read, or the rows of the pass before
+        put([&](int h, int tok, int n, const float4v &v) {
+            if (h < h0 || h >= h0 + halves)
+                return;
+            char *at = smem + (uint32_t)tok * (bytes + kRowPad) + (uint32_t)(((h - h0) * kHalf + n) * size);
+            const u32x4 o = pack4(P.out_dtype, v);
+            if (size == 4)
+                *reinterpret_cast<u32x4 *>(at) = o;
+            else
+                *reinterpret_cast<u32x2 *>(at) = u32x2{o[0], o[1]};
+        });
+        __syncthreads();
+        const int n = n0 + h0 * kHalf;
+        store_rows(smem, bytes, t.M, static_cast<char *>(P.out) + ((size_t)(t.r0 + t.m0) * P.N + n) * size,
+                   (size_t)P.N * size, (P.N - n) * size);
+    }
 }
 
 // 4 weight tiles x TTN token tiles of 16 a wave, one e4m3 MFMA and four additions each
@@ -402,12 +410,12 @@ __device__ __attribute__((always_inline)) inline void tile_fast(const TileParams
     for (int r = 0; r < 4; ++r)
         add(r, TTN - 1);
 
-    store_product(P, t, smem, [&](auto &&put) {
+    store_product<32 * TTN>(P, t, smem, [&](auto &&put) {
 #pragma unroll
         for (int c = 0; c < TTN; ++c)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                put(wt * 16 * TTN + 16 * c + j, (r >> 1) * kHalf + 32 * wr + 16 * (r & 1) + 4 * g, acc[r][c]);
+                put(r >> 1, wt * 16 * TTN + 16 * c + j, 32 * wr + 16 * (r & 1) + 4 * g, acc[r][c]);
     });
 }
 
@@ -552,6 +560,7 @@ __device__ __attribute__((always_inline)) inline void tile_exact(const TileParam
         const int fb = (P.F + kBlk - 1) / kBlk, f0 = t.nt * kHalf + 32 * wr + 4 * g;
         uint32_t *amax = reinterpret_cast<uint32_t *>(smem);  // [4 row groups][TOK], then the 8-bit rows
         char *out8 = smem + 4 * TOK * sizeof(uint32_t);
+        static_assert(4 * TOK * sizeof(uint32_t) + TOK * (kHalf + kRowPad) <= kLds, "the 8-bit rows fit");
         __syncthreads();                                      // the last stage is read
 #pragma unroll
         for (int c = 0; c < TB; ++c) {
@@ -586,14 +595,14 @@ __device__ __attribute__((always_inline)) inline void tile_exact(const TileParam
         store_rows(out8, kHalf, t.M, static_cast<char *>(P.out) + (size_t)(t.r0 + t.m0) * P.F + t.nt * kHalf, P.F,
                    P.F - t.nt * kHalf);
     } else {
-        store_product(P, t, smem, [&](auto &&put) {
+        store_product<TOK>(P, t, smem, [&](auto &&put) {
 #pragma unroll
             for (int c = 0; c < TB; ++c)
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
 #pragma unroll
                     for (int v = 0; v < 16; v += 4)
-                        put(wt * 32 * TB + 32 * c + i, r * kHalf + 32 * wr + 4 * g + 2 * v,
+                        put(r, wt * 32 * TB + 32 * c + i, 32 * wr + 4 * g + 2 * v,
                             float4v{acc[r][c][v], acc[r][c][v + 1], acc[r][c][v + 2], acc[r][c][v + 3]});
         });
     }

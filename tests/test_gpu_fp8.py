@@ -399,7 +399,9 @@ LAYERS = [  # T, E, topk, shared, H, F, renorm, bias
     (33, 6, 3, 0, 272, 272, False, True), (100, 4, 2, 1, 256, 384, True, True), (16, 200, 8, 1, 128, 64, True, False),
     (1, 256, 8, 0, 64, 48, False, True), (4, 248, 8, 8, 80, 16, True, True),
     (16, 8, 8, 8, 64, 272, True, False), (1, 8, 2, 0, 2048, 4096, True, False), (3, 6, 2, 0, 1040, 2064, False, True),
-    (100, 4, 2, 1, 1040, 272, True, False)]
+    (100, 4, 2, 1, 1040, 272, True, False),
+    # more than 150 rows of an expert: their fp32 rows do not fit LDS at once
+    (400, 2, 1, 0, 1552, 272, True, False), (700, 3, 2, 0, 2064, 144, False, True)]
 
 
 def run_layer(d, bias, E, n_shared, H, F, T, topk, renorm, stream=None):
