@@ -1143,8 +1143,8 @@ apmoe_status fp8_args(const uint8_t *x8, const float *x_scale, const uint8_t *w8
                       int32_t N, int32_t K, int32_t gather, const int32_t *perm, const int32_t *offsets, int32_t T,
                       int32_t topk)
 {
-    if (E < 1 || E > APMOE_MAX_EXPERTS || N < 1 || K < 16 || K % 16 != 0 || K > kMaxCols8)
-        return fail(APMOE_INVALID_ARG, "E=%d N=%d K=%d (need 1 <= E <= %d, N >= 1, K%%16==0, 16 <= K <= %d)", E, N, K,
+    if (E < 1 || E > APMOE_MAX_EXPERTS || N < 1 || N > 1 << 30 || K < 16 || K % 16 != 0 || K > kMaxCols8)
+        return fail(APMOE_INVALID_ARG, "E=%d N=%d K=%d (need 1 <= E <= %d, 1 <= N <= 2^30, K%%16==0, 16 <= K <= %d)", E, N, K,
                     APMOE_MAX_EXPERTS, kMaxCols8);
     if (T < 0 || topk < 1 || topk > APMOE_MAX_ASSIGN || (int64_t)T * topk > (int64_t)1 << 30)
         return fail(APMOE_INVALID_ARG, "T=%d topk=%d", T, topk);

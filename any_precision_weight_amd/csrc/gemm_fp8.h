@@ -80,7 +80,8 @@ __device__ inline void store4(const Fp8Params &P, size_t row, int n, const float
     }
 }
 
-// Rows that an expert can have: a token's experts are distinct, so one for each token;
+// Rows that an expert has at most, as a choice of kernels: a token's experts are distinct as
+// the routing gives them, so one for each token (rows beyond that are computed, slower);
 // a single expert has every row.
 inline int most_rows(const Fp8Params &P) { return P.E == 1 ? P.R : P.R / P.topk; }
 
@@ -88,7 +89,10 @@ inline int most_rows(const Fp8Params &P) { return P.E == 1 ? P.R : P.R / P.topk;
 // kStreamMax rows: for each of them its tiles of rows, the last one started.
 long fp8_tiles(const Fp8Params &P, bool act, bool exact);
 
+// A launch has fewer than 2^32 threads.
+constexpr long kMaxTiles = (1l << 23) - 8;
+
 // exact: fp32 sums inside a block (block_product), which fp32 results keep.
-hipError_t launch_fp8_tile(const Fp8Params &P, int most, bool act, bool exact, hipStream_t s);
+hipError_t launch_fp8_tile(const Fp8Params &P, bool act, bool exact, hipStream_t s);
 
 }  // namespace apmoe

@@ -9,6 +9,8 @@
 // Stream product: weights go from HBM to the matrix units through registers, each
 // weight byte read once per 32 rows; a wave holds two 16-row weight tiles, kDepth
 // blocks ahead.  Bound by the weights' bytes.
+#include <limits.h>
+
 #include "gemm_fp8.h"
 #include "launch_fp8.h"
 #include "stream_fp8.h"
@@ -20,7 +22,7 @@ constexpr int kDepth = 2;  // column blocks requested ahead
 constexpr int kStreamWaves = 8;
 constexpr int kStreamRows = 32;  // weight rows of a wave
 
-// blockIdx.x: weight rows, blockIdx.y: expert, blockIdx.z: kStreamMax of its rows.  KS waves
+// blockIdx.x: weight rows, blockIdx.y: expert, blockIdx.z: 16 TT of its rows.  KS waves
 // share a wave's 32 weight rows, a KS-th of the columns each; their sums meet in LDS in the
 // order of the parts.
 template <int KS, int TT>
@@ -102,12 +104,16 @@ __global__ void __launch_bounds__(kStreamWaves *kWave, TT == 1 ? 4 : 2) stream_k
     expert_rows(P, e, r0, m);
     if (m > P.stream_max)
         return;  // the tile product's
-    r0 += kStreamMax * (int)blockIdx.z;
-    m = min(m - kStreamMax * (int)blockIdx.z, kStreamMax);
-    if (TT == 2 && m > 16)
-        stream_tokens<KS, 2>(P, e, r0, m, red);
-    else if (m > 0)
-        stream_tokens<KS, 1>(P, e, r0, m, red);
+    constexpr int kRows = 16 * TT;
+    for (int c = kRows * (int)blockIdx.z; c < m; c += kRows * (int)gridDim.z) {
+        const int n = min(m - c, kRows);
+        if (TT == 2 && n > 16)
+            stream_tokens<KS, 2>(P, e, r0 + c, n, red);
+        else
+            stream_tokens<KS, 1>(P, e, r0 + c, n, red);
+        if (KS > 1)
+            __syncthreads();  // red is read
+    }
 }
 
 // gate_up: a wave holds NP pairs of a tile of 16 gate rows and the tile of the matching up
@@ -196,10 +202,15 @@ __global__ void __launch_bounds__(kStreamWaves / NP *kWave, NP == 2 ? 3 : TT == 
     expert_rows(P, e, r0, m);
     if (m > P.stream_max)
         return;  // the tile product's
-    if (TT == 2 && m > 16)
-        stream_act_tokens<2, NP>(P, e, r0, m, amax);
-    else if (m > 0)
-        stream_act_tokens<1, NP>(P, e, r0, m, amax);
+    constexpr int kRows = 16 * TT;
+    for (int c = 0; c < m; c += kRows) {
+        const int n = min(m - c, kRows);
+        if (TT == 2 && n > 16)
+            stream_act_tokens<2, NP>(P, e, r0 + c, n, amax);
+        else
+            stream_act_tokens<1, NP>(P, e, r0 + c, n, amax);
+        __syncthreads();  // amax is read
+    }
 }
 
 }  // namespace
@@ -214,9 +225,12 @@ hipError_t launch_gemm_fp8(const uint8_t *x8, const float *xs, const uint8_t *w8
     // and over chunks of the rows, fills it although each chunk reads the weights again:
     // 512 rows of fp32, 2048 x 2048 (32 tiles), 30 us as tiles and 26 as chunks, 1024 rows
     // (64 tiles) 32 and 44; 512 rows of fp16 (16 tiles) 31 and 26, 1024 rows (32 tiles) 31 and 43.
-    if (most > kStreamMax && fp8_tiles(P, false, exact) <= (exact ? 32 : 16))
-        P.stream_max = most;
-    const unsigned chunks = (unsigned)((most < P.stream_max ? most : P.stream_max) + kStreamMax - 1) / kStreamMax;
+    const long tiles = fp8_tiles(P, false, exact);
+    if (tiles > kMaxTiles)
+        return hipErrorInvalidValue;
+    const bool tiled = most > kStreamMax && tiles > (exact ? 32 : 16);
+    P.stream_max = tiled ? kStreamMax : INT_MAX;
+    const unsigned chunks = (unsigned)((tiled ? 1 : most) + kStreamMax - 1) / kStreamMax;
     // KS: enough waves to fill the device, 8 on a CU.
     const int active = E < R ? E : R;
     const long waves = (long)active * ((N + kStreamRows - 1) / kStreamRows) * chunks;
@@ -230,7 +244,7 @@ hipError_t launch_gemm_fp8(const uint8_t *x8, const float *xs, const uint8_t *w8
         else
             hipLaunchKernelGGL((stream_kernel<KS, 1>), grid, block, 0, s, P);
     };
-    if (!offsets && R > P.stream_max)
+    if (tiled && !offsets)
         ;  // the one expert is the tile product's
     else if (waves >= 2048 || KB < 4)
         go(std::integral_constant<int, 1>{});
@@ -240,7 +254,7 @@ hipError_t launch_gemm_fp8(const uint8_t *x8, const float *xs, const uint8_t *w8
         go(std::integral_constant<int, 4>{});
     else
         go(std::integral_constant<int, 8>{});
-    const hipError_t e = launch_fp8_tile(P, most, false, exact, s);
+    const hipError_t e = tiled ? launch_fp8_tile(P, false, exact, s) : hipSuccess;
     return e == hipSuccess ? hipGetLastError() : e;
 }
 
@@ -248,19 +262,23 @@ hipError_t launch_gemm_act_fp8(const uint8_t *x8, const float *xs, const uint8_t
                                int K, int gather, const int32_t *perm, const int32_t *offsets, int topk, int R,
                                uint8_t *a8, float *as, hipStream_t s)
 {
-    const Fp8Params P{x8, xs, w8, ws, perm, offsets, a8, as, E, 2 * F, K, topk, gather, 0, R, F, kStreamMax};
+    Fp8Params P{x8, xs, w8, ws, perm, offsets, a8, as, E, 2 * F, K, topk, gather, 0, R, F, kStreamMax};
     const dim3 grid((F + kBlk - 1) / kBlk, E);
     const int most = most_rows(P);
+    const bool tiled = most > kStreamMax;
+    if (tiled && fp8_tiles(P, true, true) > kMaxTiles)
+        return hipErrorInvalidValue;
+    P.stream_max = tiled ? kStreamMax : INT_MAX;
     // Up to 16 rows four waves with two pairs of tiles each, three workgroups on a CU (16 tokens,
     // 8 experts of 2 x 14336 x 4096: 172 us, eight waves with one pair 176); more rows have no
     // registers for that.
-    if (!offsets && R > P.stream_max)
+    if (tiled && !offsets)
         ;  // the one expert is the tile product's
     else if (most > 16)
         hipLaunchKernelGGL((stream_act_kernel<2, 1>), grid, dim3(kStreamWaves * kWave), 0, s, P);
     else
         hipLaunchKernelGGL((stream_act_kernel<1, 2>), grid, dim3(kStreamWaves / 2 * kWave), 0, s, P);
-    const hipError_t e = launch_fp8_tile(P, most, true, true, s);
+    const hipError_t e = tiled ? launch_fp8_tile(P, true, true, s) : hipSuccess;
     return e == hipSuccess ? hipGetLastError() : e;
 }
 

@@ -305,7 +305,7 @@ __device__ __attribute__((always_inline)) inline void store_product(const Fp8Par
         __syncthreads();
         const int n = n0 + h0 * kHalf;
         store_rows(smem, bytes, t.M, static_cast<char *>(P.out) + ((size_t)(t.r0 + t.m0) * P.N + n) * size,
-                   (size_t)P.N * size, (P.N - n) * size);
+                   (size_t)P.N * size, min(P.N - n, 2 * kHalf) * size);
     }
 }
 
@@ -648,14 +648,10 @@ long fp8_tiles(const Fp8Params &P, bool act, bool exact)
     return ((long)(P.R - served) / tok + served) * weight_tiles(P, act);  // ceil(m / tok) = (m - 1) / tok + 1
 }
 
-hipError_t launch_fp8_tile(const Fp8Params &P, int most, bool act, bool exact, hipStream_t s)
+hipError_t launch_fp8_tile(const Fp8Params &P, bool act, bool exact, hipStream_t s)
 {
-    if (most <= P.stream_max)
-        return hipSuccess;
     const TileParams T{P, weight_tiles(P, act)};
     const long grid = (fp8_tiles(P, act, exact) + kXcds - 1) / kXcds * kXcds;
-    if (grid > 0x7FFFFFFFl)
-        return hipErrorInvalidValue;
     if (act)
         hipLaunchKernelGGL((fp8_tile_kernel<true, true>), dim3((unsigned)grid), dim3(kThreads), 0, s, T);
     else if (exact)

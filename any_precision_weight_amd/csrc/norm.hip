@@ -83,6 +83,7 @@ __device__ inline void store8(void *p, size_t at, float (&v)[8])
 
 constexpr int kNoRes = -1;
 constexpr int kNormThreads = 256;
+constexpr uint32_t kNormGrid = 1u << 20;  // workgroups in x; a dimension has fewer than 2^32 threads
 
 // TPR threads hold a row, VPT chunks of 8 columns each (chunk t + v * TPR); a workgroup
 // of max(TPR, 256) threads holds max(1, 256 / TPR) rows.  The row stays in registers
@@ -97,9 +98,9 @@ __global__ void __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) norm_
     constexpr int kRows = NT / TPR;
     constexpr int kWavesPerRow = TPR / kWave;
     const int tid = threadIdx.x, t = tid % TPR;
-    const int row = (int)blockIdx.x * kRows + tid / TPR;
+    const uint32_t row = (blockIdx.y * kNormGrid + blockIdx.x) * kRows + tid / TPR;
     const int chunks = P.H / 8;
-    const bool live = row < P.T;  // the threads of a row past the last one only meet the barrier
+    const bool live = row < (uint32_t)P.T;  // the threads of a row past the last one only meet the barrier
     const size_t base = (size_t)(live ? row : 0) * P.H;
     float h[VPT][8];
     double sum = 0.0;
@@ -208,7 +209,10 @@ hipError_t norm_launch(const NormParams &P, hipStream_t s)
 {
     constexpr int NT = TPR > kNormThreads ? TPR : kNormThreads;
     constexpr int kRows = NT / TPR;
-    hipLaunchKernelGGL((norm_kernel<XT, RT, TPR, VPT>), dim3((P.T + kRows - 1) / kRows), dim3(NT), 0, s, P);
+    const uint32_t blocks = ((uint32_t)P.T + kRows - 1) / kRows;
+    hipLaunchKernelGGL((norm_kernel<XT, RT, TPR, VPT>),
+                       dim3(blocks < kNormGrid ? blocks : kNormGrid, (blocks + kNormGrid - 1) / kNormGrid), dim3(NT), 0,
+                       s, P);
     return hipGetLastError();
 }
 

@@ -481,11 +481,11 @@ apmoe_status apmoe_norm(apmoe_ctx *ctx, const void *x, int32_t x_dtype, const vo
  *   x8 e4m3 [T][K] (gather) or [T*topk][K], x_scale fp32 [rows][ceil(K/128)];
  *   w8 e4m3 [E][N][K], w_scale fp32 [E][ceil(N/128)][ceil(K/128)];
  *   out [T*topk][N] of out_dtype (APMOE_F16, APMOE_BF16, APMOE_F32), RNE.
- * perm and offsets as apmoe_route writes them (with E > 1 an expert has at most T rows:
- * a token's experts are distinct); rows of the output at or past
- * offsets[E] are not written.  A dense product is E = 1, topk = 1 with offsets NULL
+ * perm and offsets as apmoe_route writes them; an expert may also have more than T rows
+ * (a token twice), which is slower.  Rows of the output at or past offsets[E] are not
+ * written.  A dense product is E = 1, topk = 1 with offsets NULL
  * (every row is the one expert's) and gather = 0.
- * Limits: 1 <= E <= 256, N >= 1, K % 16 == 0, 16 <= K < 2^24, 1 <= topk <= 16, T >= 0,
+ * Limits: 1 <= E <= 256, 1 <= N <= 2^30, K % 16 == 0, 16 <= K < 2^24, 1 <= topk <= 16, T >= 0,
  * T * topk <= 2^30.  Errors (nothing enqueued): INVALID_ARG for NULL or misaligned
  * pointers (16 bytes; scales, perm and offsets 4), offsets NULL with E > 1, or bad
  * sizes; UNSUPPORTED for another out_dtype.

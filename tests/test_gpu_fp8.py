@@ -157,6 +157,19 @@ def test_norm_special_rows():
     assert torch.isnan(yz).all()
 
 
+def test_norm_many_short_rows():
+    """More workgroups than one dimension of the grid holds: the same bits as a call on the
+    rows alone."""
+    T, H = (1 << 22) + 5, 8
+    x = torch.randn((T, H), device="cuda").half()
+    gamma = torch.ones(H, device="cuda").half()
+    _, y, q, s = run_norm(x, None, gamma, 1e-5)
+    for at in (slice(0, 64), slice(1 << 21, (1 << 21) + 64), slice(T - 64, T)):
+        _, y1, q1, s1 = run_norm(x[at].clone(), None, gamma, 1e-5)
+        assert torch.equal(y[at], y1) and torch.equal(q[at], q1) and torch.equal(s[at], s1)
+    assert float((y.float() ** 2).mean(dim=1).sub(1).abs().max()) < 0.1
+
+
 # ------------------------------------------------------------------ products
 
 def routing(r, T, topk, E, skew=0.0):
@@ -193,7 +206,7 @@ GEMMS = [(1, 1, 1, 1, 16), (1, 1, 1, 128, 128), (1, 1, 1, 33, 144), (3, 2, 4, 12
          (65, 1, 2, 256, 512), (130, 2, 3, 300, 1040), (257, 1, 1, 260, 384), (300, 3, 5, 272, 272),
          (513, 1, 1, 520, 912), (700, 2, 9, 128, 128), (1000, 1, 2, 600, 1552),
          # enough tiles for the tile product in each type
-         (33, 1, 1, 8720, 144), (64, 1, 1, 8452, 656), (130, 2, 3, 4360, 528), (257, 1, 1, 4100, 272),
+         (33, 1, 1, 8720, 144), (300, 1, 1, 8720, 112), (40, 1, 1, 8720, 16), (64, 1, 1, 8452, 656), (130, 2, 3, 4360, 528), (257, 1, 1, 4100, 272),
          (300, 3, 5, 2200, 272), (513, 1, 1, 4099, 1040), (1000, 1, 2, 2600, 912), (2100, 2, 40, 144, 256)]
 
 
@@ -260,6 +273,33 @@ def test_gemm_rows_behind_the_last_sequence(T, E, N):
     assert np.all(np.abs(got[:used] - want) <= mag * sum_bound(K))
 
 
+@pytest.mark.parametrize("T,N,K", [(12, 96, 144), (12, 96, 2048), (20, 160, 2048), (30, 64, 272), (200, 2336, 272)])
+def test_products_with_a_token_twice_at_an_expert(T, N, K):
+    """Every token with both its assignments at one expert, which then has 2 T rows, more
+    than the routing's distinct experts give."""
+    r = rng_of("twice", T, N, K)
+    E, topk, R = 3, 2, 2 * T
+    perm, off = r.permutation(R).astype(np.int32), np.array([0, 0, R, R], np.int32)
+    x8, xs = random_rows(r, T, K)
+    xs = (xs / np.sqrt(K)).astype(np.float32)
+    w8, ws = random_weights(r, E, 1, N, K)
+    d = [cuda(v) for v in (x8, xs, w8, ws, perm, off)]
+    xv = ref.TABLE[x8] * ref.spread(xs.astype(np.float64), K)
+    out = torch.full((R + 1, N), 7.0, device="cuda")
+    apw.gemm_fp8(ctx(), *d[:4], E, N, K, True, *d[4:], T, topk, out)
+    want, mag = ref.product(xv, [ref.block_values(w8[e], ws[e, 0]) for e in range(E)], perm, off, topk, True)
+    assert np.all(np.abs(np64(out)[:R] - want) <= mag * sum_bound(K)) and (np64(out)[R] == 7.0).all()
+    F = N // 2
+    w8, ws = random_weights(r, E, 2, F, K)
+    a8 = torch.full((R + 1, F), 0x55, dtype=torch.uint8, device="cuda")
+    sc = torch.empty((R + 1, ref.groups(F)), device="cuda")
+    apw.gemm_act_fp8(ctx(), d[0], d[1], cuda(w8), cuda(ws), E, F, K, True, *d[4:], T, topk, a8, sc)
+    wv = [np.concatenate([ref.block_values(w8[e, h * F:(h + 1) * F], ws[e, h]) for h in (0, 1)]) for e in range(E)]
+    a, err = act_bounds(*ref.product(xv, wv, perm, off, topk, True), F, K)
+    check_rows8(a, err, a8[:R], sc[:R], F)
+    assert (codes(a8[R:]) == 0x55).all()
+
+
 @pytest.mark.parametrize("T,N", [(5, 96), (70, 96), (70, 8464)])
 def test_gemm_nan_stays_in_its_row_and_column(T, N):
     r = rng_of("nan", T)
@@ -304,7 +344,8 @@ def check_rows8(a, err, q, s, C):
 
 
 ACTS = [(1, 1, 1, 16, 16), (1, 1, 1, 128, 128), (3, 2, 4, 144, 240), (16, 2, 8, 272, 528), (33, 1, 1, 704, 256),
-        (40, 4, 6, 384, 400), (130, 2, 3, 208, 1040), (300, 1, 2, 400, 272), (600, 2, 5, 256, 512)]
+        (40, 4, 6, 384, 400), (130, 2, 3, 208, 1040), (300, 1, 2, 400, 272), (600, 2, 5, 256, 512),
+        (50, 1, 1, 32, 16), (300, 1, 1, 144, 112)]
 
 
 @pytest.mark.parametrize("gather", [True, False])
