@@ -229,7 +229,8 @@ hipError_t launch_gemm_fp8(const uint8_t *x8, const float *xs, const uint8_t *w8
     if (tiles > kMaxTiles)
         return hipErrorInvalidValue;
     const bool tiled = most > kStreamMax && tiles > (exact ? 32 : 16);
-    P.stream_max = tiled ? kStreamMax : INT_MAX;
+    const bool alone = tiled && E == 1;  // the one expert is the tile product's, whatever rows it has
+    P.stream_max = alone ? 0 : tiled ? kStreamMax : INT_MAX;
     const unsigned chunks = (unsigned)((tiled ? 1 : most) + kStreamMax - 1) / kStreamMax;
     // KS: enough waves to fill the device, 8 on a CU.
     const int active = E < R ? E : R;
@@ -244,8 +245,8 @@ hipError_t launch_gemm_fp8(const uint8_t *x8, const float *xs, const uint8_t *w8
         else
             hipLaunchKernelGGL((stream_kernel<KS, 1>), grid, block, 0, s, P);
     };
-    if (tiled && !offsets)
-        ;  // the one expert is the tile product's
+    if (alone)
+        ;
     else if (waves >= 2048 || KB < 4)
         go(std::integral_constant<int, 1>{});
     else if (waves >= 1024 || KB < 8)
@@ -268,12 +269,13 @@ hipError_t launch_gemm_act_fp8(const uint8_t *x8, const float *xs, const uint8_t
     const bool tiled = most > kStreamMax;
     if (tiled && fp8_tiles(P, true, true) > kMaxTiles)
         return hipErrorInvalidValue;
-    P.stream_max = tiled ? kStreamMax : INT_MAX;
+    const bool alone = tiled && E == 1;
+    P.stream_max = alone ? 0 : tiled ? kStreamMax : INT_MAX;
     // Up to 16 rows four waves with two pairs of tiles each, three workgroups on a CU (16 tokens,
     // 8 experts of 2 x 14336 x 4096: 172 us, eight waves with one pair 176); more rows have no
     // registers for that.
-    if (tiled && !offsets)
-        ;  // the one expert is the tile product's
+    if (alone)
+        ;
     else if (most > 16)
         hipLaunchKernelGGL((stream_act_kernel<2, 1>), grid, dim3(kStreamWaves * kWave), 0, s, P);
     else

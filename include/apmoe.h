@@ -475,7 +475,7 @@ apmoe_status apmoe_norm(apmoe_ctx *ctx, const void *x, int32_t x_dtype, const vo
  *               sum_{c in 128-column block b} x8[s][c] * w8[e][n][c],
  * s = perm[r] / topk when gather != 0, else r; each block's sum is scaled and added in
  * fp32.  The sum inside a block is an fp32 one, except for experts of more than 32 rows
- * with a 16-bit out: there it comes from the e4m3 matrix instruction, which cuts a
+ * (with E = 1: calls of more than 32 rows) with a 16-bit out: there it comes from the e4m3 matrix instruction, which cuts a
  * product off at 2^-13 of the largest one among 8 neighbours (1.5e-5 of the result in
  * norm for normally distributed operands, at most 2^-10 of the sum of the magnitudes).
  *   x8 e4m3 [T][K] (gather) or [T*topk][K], x_scale fp32 [rows][ceil(K/128)];
