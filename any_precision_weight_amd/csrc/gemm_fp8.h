@@ -16,10 +16,11 @@ struct Fp8Params {
     float *os;               // scales of a8
     int E, N, K, topk, gather, out_dtype, R;
     int F;  // with the activation: N = 2 F
-    int stream_max;  // experts of at most so many rows take the stream product, the others the tile product
+    int stream_max;  // experts of more rows are the tile product's
 };
 
-// Rows of an expert up to which the stream product reads its weights once.
+// Rows of an expert up to which the stream product reads its weights once; with more the
+// product has tiles to choose (share_rows).
 constexpr int kStreamMax = 32;
 
 __device__ inline void expert_rows(const Fp8Params &P, int e, int &r0, int &m)
@@ -86,7 +87,7 @@ __device__ inline void store4(const Fp8Params &P, size_t row, int n, const float
 inline int most_rows(const Fp8Params &P) { return P.E == 1 ? P.R : P.R / P.topk; }
 
 // Upper bound of the tile product's workgroups where it takes experts of more than
-// kStreamMax rows: for each of them its tiles of rows, the last one started.
+// P.stream_max rows: for each of them its tiles of rows, the last one started.
 long fp8_tiles(const Fp8Params &P, bool act, bool exact);
 
 // A launch has fewer than 2^32 threads.

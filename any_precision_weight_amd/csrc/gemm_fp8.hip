@@ -21,6 +21,7 @@ namespace {
 constexpr int kDepth = 2;  // column blocks requested ahead
 constexpr int kStreamWaves = 8;
 constexpr int kStreamRows = 32;  // weight rows of a wave
+constexpr int kCus = 256;
 
 // blockIdx.x: weight rows, blockIdx.y: expert, blockIdx.z: 16 TT of its rows.  KS waves
 // share a wave's 32 weight rows, a KS-th of the columns each; their sums meet in LDS in the
@@ -200,8 +201,6 @@ __global__ void __launch_bounds__(kStreamWaves / NP *kWave, NP == 2 ? 3 : TT == 
     const int e = blockIdx.y;
     int r0, m;
     expert_rows(P, e, r0, m);
-    if (m > P.stream_max)
-        return;  // the tile product's
     constexpr int kRows = 16 * TT;
     for (int c = 0; c < m; c += kRows) {
         const int n = min(m - c, kRows);
@@ -213,6 +212,38 @@ __global__ void __launch_bounds__(kStreamWaves / NP *kWave, NP == 2 ? 3 : TT == 
     }
 }
 
+// Which experts the tile product takes: those of more than P.stream_max rows; the stream
+// product has the others.  tile: it takes any.  false: more tiles than a launch can hold.
+//
+// The product.  A few tiles leave most of the device idle, and the stream product, split
+// over K and over chunks of the rows, fills it although each chunk reads the weights again:
+// 512 rows to fp32, 2048 x 2048 (32 tiles), 30 us as tiles and 26 as chunks, 1024 rows (64
+// tiles) 32 and 44; 512 rows to fp16 (16 tiles) 31 and 26, 1024 rows (32 tiles) 31 and 43.
+// With tiles, all experts take them from 8 rows an expert on average: a launch less, and the
+// stream product of up to 32 rows is no faster (8 experts of 4096 x 7168, 128 tokens of 2,
+// 127 us with both and 61 with tiles alone; 60 of 2048 x 1408, 512 tokens of 4, 80 and 38).
+// Below that the experts have a few rows each and stream (64 tokens of those 60: 35 and 38),
+// but for the ones that an uneven routing made long.
+//
+// gate_up, whose stream product is not split over K.  More than 32 rows take tiles (E = 1,
+// 48 rows of 2 x 2048 x 4096: 77 us streamed, 33 as tiles), and more than 16 where every CU
+// has one at most (24 rows of that one expert 69 and 31; 8 experts of 2 x 2048 x 7168, 32
+// tokens of 2, 128 tiles, 82 and 56; of 2 x 4096 x 4096, 256 tiles, 53 and 67).
+bool share_rows(Fp8Params &P, int most, bool act, bool exact, bool &tile)
+{
+    P.stream_max = 0;
+    const long tiles = fp8_tiles(P, act, exact);
+    if (act)
+        tile = most > kStreamMax || (most > 16 && tiles < kCus);
+    else
+        tile = most > kStreamMax && tiles > (exact ? 32 : 16);
+    if (!tile)
+        P.stream_max = INT_MAX;
+    else if (!act && P.E > 1 && P.R < 8l * P.E)
+        P.stream_max = kStreamMax;
+    return !tile || tiles <= kMaxTiles;
+}
+
 }  // namespace
 
 hipError_t launch_gemm_fp8(const uint8_t *x8, const float *xs, const uint8_t *w8, const float *ws, int E, int N, int K,
@@ -221,17 +252,10 @@ hipError_t launch_gemm_fp8(const uint8_t *x8, const float *xs, const uint8_t *w8
 {
     Fp8Params P{x8, xs, w8, ws, perm, offsets, out, nullptr, E, N, K, topk, gather, out_dtype, R, 0, kStreamMax};
     const int most = most_rows(P);
-    // So few tiles leave most of the device idle, and the stream product, split over K
-    // and over chunks of the rows, fills it although each chunk reads the weights again:
-    // 512 rows of fp32, 2048 x 2048 (32 tiles), 30 us as tiles and 26 as chunks, 1024 rows
-    // (64 tiles) 32 and 44; 512 rows of fp16 (16 tiles) 31 and 26, 1024 rows (32 tiles) 31 and 43.
-    const long tiles = fp8_tiles(P, false, exact);
-    if (tiles > kMaxTiles)
+    bool tile;
+    if (!share_rows(P, most, false, exact, tile))
         return hipErrorInvalidValue;
-    const bool tiled = most > kStreamMax && tiles > (exact ? 32 : 16);
-    const bool alone = tiled && E == 1;  // the one expert is the tile product's, whatever rows it has
-    P.stream_max = alone ? 0 : tiled ? kStreamMax : INT_MAX;
-    const unsigned chunks = (unsigned)((tiled ? 1 : most) + kStreamMax - 1) / kStreamMax;
+    const unsigned chunks = (unsigned)((tile ? 1 : most) + kStreamMax - 1) / kStreamMax;
     // KS: enough waves to fill the device, 8 on a CU.
     const int active = E < R ? E : R;
     const long waves = (long)active * ((N + kStreamRows - 1) / kStreamRows) * chunks;
@@ -245,8 +269,8 @@ hipError_t launch_gemm_fp8(const uint8_t *x8, const float *xs, const uint8_t *w8
         else
             hipLaunchKernelGGL((stream_kernel<KS, 1>), grid, block, 0, s, P);
     };
-    if (alone)
-        ;
+    if (P.stream_max == 0)
+        ;  // all are the tile product's
     else if (waves >= 2048 || KB < 4)
         go(std::integral_constant<int, 1>{});
     else if (waves >= 1024 || KB < 8)
@@ -255,7 +279,7 @@ hipError_t launch_gemm_fp8(const uint8_t *x8, const float *xs, const uint8_t *w8
         go(std::integral_constant<int, 4>{});
     else
         go(std::integral_constant<int, 8>{});
-    const hipError_t e = tiled ? launch_fp8_tile(P, false, exact, s) : hipSuccess;
+    const hipError_t e = tile ? launch_fp8_tile(P, false, exact, s) : hipSuccess;
     return e == hipSuccess ? hipGetLastError() : e;
 }
 
@@ -266,22 +290,22 @@ hipError_t launch_gemm_act_fp8(const uint8_t *x8, const float *xs, const uint8_t
     Fp8Params P{x8, xs, w8, ws, perm, offsets, a8, as, E, 2 * F, K, topk, gather, 0, R, F, kStreamMax};
     const dim3 grid((F + kBlk - 1) / kBlk, E);
     const int most = most_rows(P);
-    const bool tiled = most > kStreamMax;
-    if (tiled && fp8_tiles(P, true, true) > kMaxTiles)
+    bool tile;
+    if (!share_rows(P, most, true, true, tile))
         return hipErrorInvalidValue;
-    const bool alone = tiled && E == 1;
-    P.stream_max = alone ? 0 : tiled ? kStreamMax : INT_MAX;
     // Up to 16 rows four waves with two pairs of tiles each, three workgroups on a CU (16 tokens,
     // 8 experts of 2 x 14336 x 4096: 172 us, eight waves with one pair 176); more rows have no
     // registers for that.
-    if (alone)
-        ;
-    else if (most > 16)
+    if (tile) {
+        const hipError_t e = launch_fp8_tile(P, true, true, s);
+        if (e != hipSuccess)
+            return e;
+    } else if (most > 16) {
         hipLaunchKernelGGL((stream_act_kernel<2, 1>), grid, dim3(kStreamWaves * kWave), 0, s, P);
-    else
+    } else {
         hipLaunchKernelGGL((stream_act_kernel<1, 2>), grid, dim3(kStreamWaves / 2 * kWave), 0, s, P);
-    const hipError_t e = tiled ? launch_fp8_tile(P, true, true, s) : hipSuccess;
-    return e == hipSuccess ? hipGetLastError() : e;
+    }
+    return hipGetLastError();
 }
 
 }  // namespace apmoe

@@ -644,7 +644,7 @@ static int weight_tiles(const Fp8Params &P, bool act)
 long fp8_tiles(const Fp8Params &P, bool act, bool exact)
 {
     const int tok = exact ? kTileTok<true> : kTileTok<false>;
-    const int served = P.E < P.R / (kStreamMax + 1) ? P.E : P.R / (kStreamMax + 1);
+    const int served = P.E < P.R / (P.stream_max + 1) ? P.E : P.R / (P.stream_max + 1);
     return ((long)(P.R - served) / tok + served) * weight_tiles(P, act);  // ceil(m / tok) = (m - 1) / tok + 1
 }
 
