@@ -2,11 +2,12 @@
 //
 // A few tokens read every chosen expert's weights for a handful of rows: the layer is
 // bound by those bytes and, on small experts, by the time its launches take to begin
-// and end.  Two launches do it, three where the router is large:
+// and end.  Three launches do it:
 //
-//   few_logits      (large routers) one wave for each (token, expert): the fp64 logit.
-//   few_gate_up     every workgroup selects the experts itself (from the logits, or by
-//                   computing them: a small router costs less than a launch), finds the
+//   few_logits      one wave for each (token, expert): the fp64 logit.  (Every workgroup of
+//                   few_gate_up computing them saves the launch and costs more even with 8
+//                   experts: one token of 2048 x 2048 22.4 us against 20.7, two 31.5 and 25.8.)
+//   few_gate_up     every workgroup selects the experts itself from the logits, finds the
 //                   expert of its slot and multiplies that expert's gate and up rows by
 //                   all T tokens at once -- the 16 columns of a matrix product hold
 //                   them, chosen or not -- and stores the rows of the tokens that chose
@@ -145,7 +146,7 @@ __device__ inline void write_choices(const FewParams &P, const double *zs, const
 // as many, each with 32 values, stored in fp32 (a32) and quantised by few_down.  (Also
 // measured: four waves sharing a pair's columns, quantised by the last workgroup of a
 // group: slower, each workgroup pays for its selection, 133 -> 147 us.)
-template <int NW, int NP, bool FUSED>
+template <int NW, int NP>
 __global__ void __launch_bounds__(NW *kWave, NP == 2 ? 3 : 4) few_gate_up(const FewParams P)
 {
     extern __shared__ __attribute__((aligned(16))) char smem[];
@@ -164,16 +165,8 @@ __global__ void __launch_bounds__(NW *kWave, NP == 2 ? 3 : 4) few_gate_up(const 
         flags[i] = 0;
     for (int i = tid; i < P.T * P.kt; i += NT)
         ids[i] = 0;
-    if constexpr (FUSED) {
-        for (int i = wave; i < P.T * P.Er; i += NW) {
-            const double z = logit(P, i / P.Er, i % P.Er, lane);
-            if (lane == 0)
-                zs[i] = z;
-        }
-    } else {
-        for (int i = tid; i < P.T * P.Er; i += NT)
-            zs[i] = P.z[i];
-    }
+    for (int i = tid; i < P.T * P.Er; i += NT)
+        zs[i] = P.z[i];
     __syncthreads();
     choose(P, zs, ids, NT);
     __syncthreads();
@@ -425,21 +418,15 @@ __global__ void __launch_bounds__(kThreads) few_down(const FewParams P)
 hipError_t launch_few_layer(FewParams P, hipStream_t s)
 {
     const size_t zbytes = (size_t)P.T * P.Er * sizeof(double);
-    const bool fused = (long)P.T * P.Er * P.H <= kFewFusedRouter;
     const bool quant = few_quantises_late(P.T, P.topk, P.kt, P.Er, P.F);
     P.slots = few_slots(P.T, P.topk, P.kt, P.Er);
-    if (!fused)
-        hipLaunchKernelGGL(few_logits, dim3((P.T * P.Er + 3) / 4), dim3(256), 0, s, P);
+    hipLaunchKernelGGL(few_logits, dim3((P.T * P.Er + 3) / 4), dim3(256), 0, s, P);
     const int per = quant ? 32 : kBlk;
     const dim3 grid((P.F + per - 1) / per, P.slots + 1), block((quant ? 2 : 4) * kWave);
-    if (quant && fused)
-        hipLaunchKernelGGL((few_gate_up<2, 1, true>), grid, block, zbytes, s, P);
-    else if (quant)
-        hipLaunchKernelGGL((few_gate_up<2, 1, false>), grid, block, zbytes, s, P);
-    else if (fused)
-        hipLaunchKernelGGL((few_gate_up<4, 2, true>), grid, block, zbytes, s, P);
+    if (quant)
+        hipLaunchKernelGGL((few_gate_up<2, 1>), grid, block, zbytes, s, P);
     else
-        hipLaunchKernelGGL((few_gate_up<4, 2, false>), grid, block, zbytes, s, P);
+        hipLaunchKernelGGL((few_gate_up<4, 2>), grid, block, zbytes, s, P);
     const size_t red = kWaves * 256 * sizeof(float);
     const size_t q = (size_t)P.T * P.kt * ((quant ? P.F : 0) + 4 * ((P.F + kBlk - 1) / kBlk));
     const size_t lds = q > red ? q : red;

@@ -220,16 +220,25 @@ template <int XT, int RT>
 hipError_t norm_shape(const NormParams &P, hipStream_t s)
 {
     const int chunks = P.H / 8;
+    // Few rows are a matter of latency: more threads a row (bf16 with an fp32 residual, both
+    // outputs, 128 rows of 1024 3.4 us against 4.7, of 8192 6.1 against 8.5; 512 rows 4.4 and
+    // 5.1, 14.0 and 15.4).  Many take the threads that are all in use and have more loads in
+    // flight each (2048 rows of 4096 22 us against 28, 8192 rows of 4096 87 and 126, 5.3 TB/s).
+    const bool few = P.T <= 512;
     if (chunks <= 64)
         return norm_launch<XT, RT, 64, 1>(P, s);
-    if (chunks <= 128)
+    if (chunks <= 128 && !few)
         return norm_launch<XT, RT, 64, 2>(P, s);
     if (chunks <= 256)
         return norm_launch<XT, RT, 256, 1>(P, s);
-    if (chunks <= 512)
+    if (chunks <= 512 && !few)
         return norm_launch<XT, RT, 256, 2>(P, s);
-    if (chunks <= 1024)
+    if (chunks <= 1024 && !few)
         return norm_launch<XT, RT, 256, 4>(P, s);
+    if (chunks <= 1024)
+        return norm_launch<XT, RT, 1024, 1>(P, s);
+    if (chunks <= 2048)
+        return norm_launch<XT, RT, 1024, 2>(P, s);
     if (chunks <= 4096)
         return norm_launch<XT, RT, 1024, 4>(P, s);
     return norm_launch<XT, RT, 1024, 8>(P, s);

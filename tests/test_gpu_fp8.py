@@ -92,7 +92,9 @@ def check_norm(x, res, gamma, eps, got):
 
 
 NORM_SHAPES = [(1, 8), (1, 128), (3, 136), (5, 504), (2, 520), (7, 704), (4, 1032), (3, 2048), (2, 2056), (3, 4096),
-               (2, 4104), (1, 8192), (2, 8200), (1, 32768), (2, 32776), (1, 65536), (333, 264), (1025, 64)]
+               (2, 4104), (1, 8192), (2, 8200), (1, 32768), (2, 32776), (1, 65536), (333, 264), (1025, 64),
+               # above 512 rows
+               (515, 8), (515, 520), (517, 1016), (513, 1032), (514, 2056), (519, 4104), (513, 8200)]
 
 
 @pytest.mark.parametrize("T,H", NORM_SHAPES)
