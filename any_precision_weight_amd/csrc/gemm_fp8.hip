@@ -8,7 +8,9 @@
 //
 // Stream product: weights go from HBM to the matrix units through registers, each
 // weight byte read once per 32 rows; a wave holds two 16-row weight tiles, kDepth
-// blocks ahead.  Bound by the weights' bytes.
+// blocks ahead.  Bound by the weights' bytes (gate_up of 16 tokens, 8 experts of 2 x 14336 x
+// 4096: 157 us, 6.0 TB/s), where they are few by the latency of a wave's blocks (6144 x 4096
+// for 8 tokens 11 us, 2.3 TB/s).
 #include <limits.h>
 
 #include "gemm_fp8.h"

@@ -19,7 +19,9 @@
 // fp16 MFMAs on converted operands for sums that stay in fp32 or are quantised again
 // (tile_exact).  What bounds them is how many instructions a SIMD takes: a vector
 // instruction holds it for about 4 clocks and an MFMA for 8, so beside a 32-clock MFMA
-// there is room for 6 others.
+// there is room for 6 others.  Measured: 4096 x 6144 x 4096 to fp16 120 us, 1.71 PFLOP/s;
+// through fp16 products 8 experts of 4096 x 14336 with 4096 rows, unevenly, 541 us, 0.89, and
+// gate_up of the same layer's 8192 rows 1.8 ms, 1.07.
 #include "gemm_fp8.h"
 
 namespace apmoe {

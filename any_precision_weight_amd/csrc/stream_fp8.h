@@ -20,7 +20,7 @@ struct StreamStage {
 // scales by block.  The blocks are requested D ahead of their products, into registers,
 // starting with block rot of the range: workgroups that start at different columns do
 // not ask the same memory channels all at once (rows are a multiple of a large power of
-// two apart; 4.2 -> 4.5 TB/s).  K's last block may be shorter than 128, a multiple of
+// two apart; 4.2 -> 4.5 TB/s where it was first measured).  K's last block may be shorter than 128, a multiple of
 // 16: the lanes past it give zeros.
 template <int NR, int TT, int D>
 __device__ __attribute__((always_inline)) inline void stream_product(const uint8_t *const (&wbase)[NR], const uint32_t (&wo)[NR][2],
