@@ -91,7 +91,7 @@ inline int most_rows(const Fp8Params &P) { return P.E == 1 ? P.R : P.R / P.topk;
 long fp8_tiles(const Fp8Params &P, bool act, bool exact);
 
 // A launch has fewer than 2^32 threads.
-constexpr long kMaxTiles = (1l << 23) - 8;
+constexpr long kMaxTiles = (1l << 23) - 256;
 
 // exact: fp32 sums inside a block (block_product), which fp32 results keep.
 hipError_t launch_fp8_tile(const Fp8Params &P, bool act, bool exact, hipStream_t s);

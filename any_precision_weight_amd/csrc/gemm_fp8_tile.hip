@@ -29,6 +29,7 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kHalf = 128;  // weight rows of a half
+constexpr int kXcdCus = 32;
 constexpr int kGroup = 8;   // weight tiles that share their token tiles through an XCD's L2
 constexpr uint32_t kStageW = 2 * kHalf * kBlk;
 // LDS of tiles of TOK tokens: NB buffers, each a stage and its tokens' scales.  A stage is
@@ -57,6 +58,10 @@ struct Tile {
 // order: groups of kGroup weight tiles, in a group the token tiles of every served
 // expert, then the group's weight tiles.  XCD x (workgroups b with b % 8 = x) takes the
 // x-th eighth.  Lane l counts the token tiles of experts 4l .. 4l+3.
+//
+// A CU holds one workgroup, so an XCD works in rounds of kXcdCus tiles.  Where the last
+// round would leave half of the CUs idle its tiles are split into 2 or 4 parts of their
+// tokens, of not less than 64.
 __device__ inline bool resolve(const TileParams &T, int tok, Tile &t)
 {
     const Fp8Params &P = T.p;
@@ -79,13 +84,18 @@ __device__ inline bool resolve(const TileParams &T, int tok, Tile &t)
     }
     const int MT = __builtin_amdgcn_readlane(incl, kWave - 1);
     const int total = MT * T.NT, per = (total + kXcds - 1) / kXcds;
-    const int local = (int)blockIdx.x / kXcds, l = ((int)blockIdx.x % kXcds) * per + local;
-    if (local >= per || l >= total)
+    const int first = ((int)blockIdx.x % kXcds) * per, local = (int)blockIdx.x / kXcds;
+    const int mine = max(0, min(per, total - first)), rem = mine % kXcdCus;
+    const int parts = tok >= 256 && 4 * rem <= kXcdCus ? 4 : 2 * rem <= kXcdCus ? 2 : 1;
+    const int over = local - (mine - rem);  // workgroup of the last round
+    if (over >= parts * rem)
         return false;
+    const int l = first + (over < 0 ? local : mine - rem + over / parts);
+    const int size = over < 0 ? tok : tok / parts, part = over < 0 ? 0 : over % parts;
     const int k = l / (kGroup * MT);
     const int gs = min(kGroup, T.NT - kGroup * k);
-    const int rem = l - k * kGroup * MT;
-    const int u = rem / gs;
+    const int at_l = l - k * kGroup * MT;
+    const int u = at_l / gs;
     const int at = (int)__builtin_ctzll(__ballot(incl > u));  // the lane with token tile u
     int v = u - __builtin_amdgcn_readlane(incl - sum, at), e = 4 * at;
     int r0 = __builtin_amdgcn_readlane(o[0], at), r1 = __builtin_amdgcn_readlane(o[1], at);
@@ -99,8 +109,9 @@ __device__ inline bool resolve(const TileParams &T, int tok, Tile &t)
             r1 = __builtin_amdgcn_readlane(o[i + 2], at);
         }
     }
-    t = Tile{e, r0, v * tok, min(tok, r1 - r0 - v * tok), k * kGroup + rem % gs};
-    return true;
+    const int m0 = v * tok + part * size;
+    t = Tile{e, r0, m0, min(size, r1 - r0 - m0), k * kGroup + at_l % gs};
+    return t.M > 0;
 }
 
 // A pointer that is the same in every lane, in scalar registers.
@@ -653,7 +664,8 @@ long fp8_tiles(const Fp8Params &P, bool act, bool exact)
 hipError_t launch_fp8_tile(const Fp8Params &P, bool act, bool exact, hipStream_t s)
 {
     const TileParams T{P, weight_tiles(P, act)};
-    const long grid = (fp8_tiles(P, act, exact) + kXcds - 1) / kXcds * kXcds;
+    const long round = kXcds * kXcdCus;  // the last one whole: its tiles may be split
+    const long grid = (fp8_tiles(P, act, exact) + round - 1) / round * round;
     if (act)
         hipLaunchKernelGGL((fp8_tile_kernel<true, true>), dim3((unsigned)grid), dim3(kThreads), 0, s, T);
     else if (exact)
