@@ -86,9 +86,12 @@ __device__ inline void store4(const Fp8Params &P, size_t row, int n, const float
 // a single expert has every row.
 inline int most_rows(const Fp8Params &P) { return P.E == 1 ? P.R : P.R / P.topk; }
 
-// Upper bound of the tile product's workgroups where it takes experts of more than
-// P.stream_max rows: for each of them its tiles of rows, the last one started.
-long fp8_tiles(const Fp8Params &P, bool act, bool exact);
+// Tokens of a tile: 128 where the products of a stage stay in registers.
+constexpr int fp8_tile_tokens(bool exact) { return exact ? 128 : 256; }
+
+// Upper bound of the tiles of `tok` rows for experts of more than P.stream_max rows: for each
+// of them the last one started, times the tiles of weights.
+long fp8_tiles(const Fp8Params &P, bool act, int tok);
 
 // A launch has fewer than 2^32 threads.
 constexpr long kMaxTiles = (1l << 23) - 256;

@@ -13,6 +13,8 @@
 // for 8 tokens 11 us, 2.3 TB/s).
 #include <limits.h>
 
+#include <algorithm>
+
 #include "gemm_fp8.h"
 #include "launch_fp8.h"
 #include "stream_fp8.h"
@@ -218,9 +220,11 @@ __global__ void __launch_bounds__(kStreamWaves / NP *kWave, NP == 2 ? 3 : TT == 
 // product has the others.  tile: it takes any.  false: more tiles than a launch can hold.
 //
 // The product.  A few tiles leave most of the device idle, and the stream product, split
-// over K and over chunks of the rows, fills it although each chunk reads the weights again:
-// 512 rows to fp32, 2048 x 2048 (32 tiles), 30 us as tiles and 26 as chunks, 1024 rows (64
-// tiles) 32 and 44; 512 rows to fp16 (16 tiles) 31 and 26, 1024 rows (32 tiles) 31 and 43.
+// over K and over chunks of 32 rows, fills it although each chunk reads the weights again.
+// Up to 64 chunks of 256 weight rows (32 with a 16-bit out, whose tiles are faster) it is
+// ahead: to fp32, 256 rows of 2048 x 2048 (64 chunks) 20 us as tiles and 17 as chunks, 64 of
+// 6144 x 4096 (48) 33 and 26, 512 of 2048 x 2048 (128) 21 and 26, 128 of 6144 x 4096 (96) 34
+// and 44; to fp16, 128 rows of 2048 x 2048 (32) 14.5 and 12.3, 192 (48) 14.5 and 17.
 // With tiles, all experts take them from 8 rows an expert on average: a launch less, and the
 // stream product of up to 32 rows is no faster (8 experts of 4096 x 7168, 128 tokens of 2,
 // 127 us with both and 61 with tiles alone; 60 of 2048 x 1408, 512 tokens of 4, 80 and 38).
@@ -234,11 +238,11 @@ __global__ void __launch_bounds__(kStreamWaves / NP *kWave, NP == 2 ? 3 : TT == 
 bool share_rows(Fp8Params &P, int most, bool act, bool exact, bool &tile)
 {
     P.stream_max = 0;
-    const long tiles = fp8_tiles(P, act, exact);
+    const long tiles = fp8_tiles(P, act, fp8_tile_tokens(exact));
     if (act)
         tile = most > kStreamMax || (most > 16 && tiles < kCus);
     else
-        tile = most > kStreamMax && tiles > (exact ? 32 : 16);
+        tile = most > kStreamMax && fp8_tiles(P, act, kStreamMax) > (exact ? 64 : 32);
     if (!tile)
         P.stream_max = INT_MAX;
     else if (!act && P.E > 1 && P.R < 8l * P.E)
@@ -262,7 +266,8 @@ hipError_t launch_gemm_fp8(const uint8_t *x8, const float *xs, const uint8_t *w8
     // 47, 26, 16, 10.9 us; 28672 x 4096, 896 waves, 47, 29, 32, 36; 8 experts of 4096 x 2048,
     // 1024 waves, 23, 14.8, 17, 21; 60 of 2048 x 1408, 3840 waves, 31, 31, 30, 40).
     const int active = E < R ? E : R;
-    const long waves = (long)active * ((N + kStreamRows - 1) / kStreamRows) * chunks;
+    const long parts = std::min((long)active * chunks, (long)(R - active) / kStreamMax + active);  // that have rows
+    const long waves = parts * ((N + kStreamRows - 1) / kStreamRows);
     const int KB = (K + kBlk - 1) / kBlk;
     auto go = [&](auto ks) {
         constexpr int KS = decltype(ks)::value;

@@ -621,16 +621,12 @@ __device__ __attribute__((always_inline)) inline void tile_exact(const TileParam
     }
 }
 
-// Tokens of a tile: 128 where the products of a stage stay in registers.
-template <bool EXACT>
-constexpr int kTileTok = EXACT ? 128 : 256;
-
 template <bool EXACT, bool ACT>
 __global__ void __launch_bounds__(kThreads) fp8_tile_kernel(const TileParams T)
 {
     __shared__ __attribute__((aligned(1024))) char smem[kLds];
     Tile t = {0, 0, 0, 0, 0};
-    if (!resolve(T, kTileTok<EXACT>, t))
+    if (!resolve(T, fp8_tile_tokens(EXACT), t))
         return;
     if constexpr (EXACT) {
         if (t.M > 64)
@@ -654,9 +650,8 @@ static int weight_tiles(const Fp8Params &P, bool act)
     return act ? (P.F + kHalf - 1) / kHalf : (P.N + 2 * kHalf - 1) / (2 * kHalf);
 }
 
-long fp8_tiles(const Fp8Params &P, bool act, bool exact)
+long fp8_tiles(const Fp8Params &P, bool act, int tok)
 {
-    const int tok = exact ? kTileTok<true> : kTileTok<false>;
     const int served = P.E < P.R / (P.stream_max + 1) ? P.E : P.R / (P.stream_max + 1);
     return ((long)(P.R - served) / tok + served) * weight_tiles(P, act);  // ceil(m / tok) = (m - 1) / tok + 1
 }
@@ -665,7 +660,7 @@ hipError_t launch_fp8_tile(const Fp8Params &P, bool act, bool exact, hipStream_t
 {
     const TileParams T{P, weight_tiles(P, act)};
     const long round = kXcds * kXcdCus;  // the last one whole: its tiles may be split
-    const long grid = (fp8_tiles(P, act, exact) + round - 1) / round * round;
+    const long grid = (fp8_tiles(P, act, fp8_tile_tokens(exact)) + round - 1) / round * round;
     if (act)
         hipLaunchKernelGGL((fp8_tile_kernel<true, true>), dim3((unsigned)grid), dim3(kThreads), 0, s, T);
     else if (exact)
