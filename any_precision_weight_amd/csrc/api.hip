@@ -1295,7 +1295,11 @@ apmoe_status apmoe_moe_workspace_fp8(apmoe_ctx *ctx, const apmoe_fp8_experts *ex
     apmoe_status s = fp8_layer_sizes(ex, T, topk, n_shared);
     if (s != APMOE_OK)
         return s;
-    *bytes = ws_layout8(T, topk + n_shared, ex->E, ex->H, ex->F).total;
+    // a few tokens may need more than some more tokens: a workspace serves smaller batches too
+    const size_t all = ws_layout8(T, topk + n_shared, ex->E, ex->H, ex->F).total;
+    const int t = T < apmoe::kFewTokens ? T : apmoe::kFewTokens;
+    const size_t few = ws_layout8(t, topk + n_shared, ex->E, ex->H, ex->F).total;
+    *bytes = all > few ? all : few;
     return ok();
 }
 

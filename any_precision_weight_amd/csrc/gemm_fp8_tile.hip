@@ -19,8 +19,8 @@
 // fp16 MFMAs on converted operands for sums that stay in fp32 or are quantised again
 // (tile_exact).  What bounds them is how many instructions a SIMD takes: a vector
 // instruction holds it for about 4 clocks and an MFMA for 8, so beside a 32-clock MFMA
-// there is room for 6 others.  Measured: 4096 x 6144 x 4096 to fp16 120 us, 1.71 PFLOP/s;
-// through fp16 products 8 experts of 4096 x 14336 with 4096 rows, unevenly, 541 us, 0.89, and
+// there is room for 6 others.  Measured: 4096 x 6144 x 4096 to fp16 107 us, 1.93 PFLOP/s;
+// through fp16 products 8 experts of 4096 x 14336 with 4096 rows, unevenly, 518 us, 0.93, and
 // gate_up of the same layer's 8192 rows 1.8 ms, 1.07.
 #include "gemm_fp8.h"
 
@@ -61,7 +61,8 @@ struct Tile {
 //
 // A CU holds one workgroup, so an XCD works in rounds of kXcdCus tiles.  Where the last
 // round would leave half of the CUs idle its tiles are split into 2 or 4 parts of their
-// tokens, of not less than 64.
+// tokens, of not less than 64 (a part of half the tokens takes 0.62 of the time): 4096 x 6144
+// x 4096, 1.5 rounds, 120 -> 107 us; 256 rows of it, 24 tiles, 51 -> 26.
 __device__ inline bool resolve(const TileParams &T, int tok, Tile &t)
 {
     const Fp8Params &P = T.p;

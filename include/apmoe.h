@@ -525,7 +525,7 @@ typedef struct apmoe_fp8_experts {
     const float *down_scale;
 } apmoe_fp8_experts;
 
-/* Device workspace bytes of apmoe_moe_forward_fp8.  Host only. */
+/* Device workspace bytes of apmoe_moe_forward_fp8 for T tokens or fewer.  Host only. */
 apmoe_status apmoe_moe_workspace_fp8(apmoe_ctx *ctx, const apmoe_fp8_experts *ex, int32_t T, int32_t topk,
                                      int32_t n_shared, size_t *bytes);
 

@@ -58,6 +58,10 @@ def test_gemm_refusals(kw, status):
     assert call("apmoe_gemm_fp8", *gemm_args(**kw)) == status
 
 
+def test_gemm_of_too_many_weight_rows():
+    assert call("apmoe_gemm_fp8", *gemm_args(N=(1 << 30) + 1)) == apw.INVALID_ARG
+
+
 def test_gemm_of_no_rows():
     assert call("apmoe_gemm_fp8", *gemm_args(T=0)) == apw.OK
 
@@ -113,6 +117,16 @@ def test_layer_workspace():
     assert call("apmoe_moe_workspace_fp8", CTX, None, 1, 2, 1, ctypes.byref(n)) == apw.INVALID_ARG
     assert call("apmoe_moe_workspace_fp8", CTX, ctypes.byref(ex), 1, 2, 1, None) == apw.INVALID_ARG
     assert call("apmoe_moe_forward_fp8", *layer_args(T=0)) == apw.OK
+
+
+def test_layer_workspace_of_a_batch_serves_smaller_ones():
+    n = ctypes.c_size_t()
+    for ex in (desc(), desc(H=96, F=64), desc(E=256, H=16, F=1024)):
+        sizes = []
+        for T in range(40):
+            assert call("apmoe_moe_workspace_fp8", CTX, ctypes.byref(ex), T, 2, 1, ctypes.byref(n)) == apw.OK
+            sizes.append(n.value)
+        assert sizes == sorted(sizes)
 
 
 class HostCtx:

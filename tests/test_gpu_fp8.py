@@ -606,6 +606,59 @@ def test_norm_then_layer_then_norm():
         check_norm(out, mid, gamma, 1e-5, (None, x2, None, None))
 
 
+# ------------------------------------------------------------------ offsets past 32 bits
+
+def codes_on_gpu(seed, *shape):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    c = torch.randint(0, 255, shape, dtype=torch.uint8, device="cuda", generator=g)
+    return c.masked_fill_(c == 0x7F, 0x7E)  # no NaN code
+
+
+def check_part(x8, xs, w8, ws, got, K):
+    """got = rows of x8 times rows of w8 (one 128-row block of scales each) to fp32."""
+    x, w = ref.TABLE[codes(x8)] * ref.spread(np64(xs), K), ref.TABLE[codes(w8)] * ref.spread(np64(ws)[None], K)
+    assert np.all(np.abs(np64(got) - x @ w.T) <= (np.abs(x) @ np.abs(w).T) * sum_bound(K))
+
+
+@pytest.mark.parametrize("N", [48, 8720])
+def test_gemm_rows_past_32_bits(N):
+    """x8 (N = 48) or out (N = 8720) longer than 2^32 elements."""
+    R, K = (70016, 65536) if N == 48 else (500032, 16)
+    x8, w8 = codes_on_gpu(1, R, K), codes_on_gpu(2, 1, N, K)
+    xs = torch.rand((R, ref.groups(K)), device="cuda") * 2.0 ** -9
+    ws = torch.rand((1, ref.groups(N), ref.groups(K)), device="cuda") * 2.0 ** -9
+    out = torch.empty((R, N), device="cuda")
+    apw.gemm_fp8(ctx(), x8, xs, w8, ws, 1, N, K, False, None, None, R, 1, out)
+    torch.cuda.synchronize()
+    for rows in (slice(0, 8), slice(R - 8, R)):
+        check_part(x8[rows], xs[rows], w8[0, N - 16:], ws[0, -1], out[rows, N - 16:], K)
+
+
+@pytest.mark.parametrize("T", [6, 70])
+def test_gemm_weights_past_32_bits(T):
+    E, N, K = 3, 20096, 73728
+    x8, w8 = codes_on_gpu(3, T, K), codes_on_gpu(4, E, N, K)
+    xs = torch.rand((T, ref.groups(K)), device="cuda") * 2.0 ** -9
+    ws = torch.rand((E, ref.groups(N), ref.groups(K)), device="cuda") * 2.0 ** -9
+    off = torch.tensor([0, 1, 2, T], dtype=torch.int32, device="cuda")
+    out = torch.empty((T, N), device="cuda")
+    apw.gemm_fp8(ctx(), x8, xs, w8, ws, E, N, K, False, torch.arange(T, dtype=torch.int32, device="cuda"), off, T, 1,
+                 out)
+    torch.cuda.synchronize()
+    for e, rows in ((0, slice(0, 1)), (1, slice(1, 2)), (2, slice(T - 4, T))):
+        check_part(x8[rows], xs[rows], w8[e, N - 16:], ws[e, -1], out[rows, N - 16:], K)
+
+
+def test_norm_rows_past_32_bits():
+    T, H = 70016, 65536
+    x = torch.empty((T, H), dtype=torch.float16, device="cuda").normal_()
+    gamma = torch.ones(H, dtype=torch.float16, device="cuda")
+    _, _, q, s = run_norm(x, None, gamma, 1e-5, want_y=False)
+    for at in (slice(0, 4), slice(T - 4, T)):
+        _, _, q1, s1 = run_norm(x[at].clone(), None, gamma, 1e-5, want_y=False)
+        assert torch.equal(q[at], q1) and torch.equal(s[at], s1)
+
+
 def test_same_bits_again():
     """No atomics: the same inputs give the same bits."""
     r = rng_of("again")
