@@ -16,11 +16,10 @@ struct Fp8Params {
     float *os;               // scales of a8
     int E, N, K, topk, gather, out_dtype, R;
     int F;  // with the activation: N = 2 F
-    int stream_max;  // experts of more rows are the tile product's
 };
 
 // Rows of an expert up to which the stream product reads its weights once; with more the
-// product has tiles to choose (share_rows).
+// tile product is a choice (takes_tiles).
 constexpr int kStreamMax = 32;
 
 __device__ inline void expert_rows(const Fp8Params &P, int e, int &r0, int &m)
@@ -89,12 +88,9 @@ inline int most_rows(const Fp8Params &P) { return P.E == 1 ? P.R : P.R / P.topk;
 // Tokens of a tile: 128 where the products of a stage stay in registers.
 constexpr int fp8_tile_tokens(bool exact) { return exact ? 128 : 256; }
 
-// Upper bound of the tiles of `tok` rows for experts of more than P.stream_max rows: for each
-// of them the last one started, times the tiles of weights.
+// Upper bound of the tiles of `tok` rows: for each expert that may have rows the last one
+// started, times the tiles of weights.
 long fp8_tiles(const Fp8Params &P, bool act, int tok);
-
-// A launch has fewer than 2^32 threads.
-constexpr long kMaxTiles = (1l << 23) - 256;
 
 // exact: fp32 sums inside a block (block_product), which fp32 results keep.
 hipError_t launch_fp8_tile(const Fp8Params &P, bool act, bool exact, hipStream_t s);

@@ -11,8 +11,6 @@
 // blocks ahead.  Bound by the weights' bytes (gate_up of 16 tokens, 8 experts of 2 x 14336 x
 // 4096: 157 us, 6.0 TB/s), where they are few by the latency of a wave's blocks (6144 x 4096
 // for 8 tokens 11 us, 2.3 TB/s).
-#include <limits.h>
-
 #include <algorithm>
 
 #include "gemm_fp8.h"
@@ -107,8 +105,6 @@ __global__ void __launch_bounds__(kStreamWaves *kWave, TT == 1 ? 4 : 2) stream_k
     const int e = blockIdx.y;
     int r0, m;
     expert_rows(P, e, r0, m);
-    if (m > P.stream_max)
-        return;  // the tile product's
     constexpr int kRows = 16 * TT;
     for (int c = kRows * (int)blockIdx.z; c < m; c += kRows * (int)gridDim.z) {
         const int n = min(m - c, kRows);
@@ -216,38 +212,29 @@ __global__ void __launch_bounds__(kStreamWaves / NP *kWave, NP == 2 ? 3 : TT == 
     }
 }
 
-// Which experts the tile product takes: those of more than P.stream_max rows; the stream
-// product has the others.  tile: it takes any.  false: more tiles than a launch can hold.
+// Whether a call takes the tile product or the stream product.
 //
-// The product.  A few tiles leave most of the device idle, and the stream product, split
-// over K and over chunks of 32 rows, fills it although each chunk reads the weights again.
-// Up to 64 chunks of 256 weight rows (32 with a 16-bit out, whose tiles are faster) it is
-// ahead: to fp32, 256 rows of 2048 x 2048 (64 chunks) 20 us as tiles and 17 as chunks, 64 of
-// 6144 x 4096 (48) 33 and 26, 512 of 2048 x 2048 (128) 21 and 26, 128 of 6144 x 4096 (96) 34
-// and 44; to fp16, 128 rows of 2048 x 2048 (32) 14.5 and 12.3, 192 (48) 14.5 and 17.
-// With tiles, all experts take them from 8 rows an expert on average: a launch less, and the
-// stream product of up to 32 rows is no faster (8 experts of 4096 x 7168, 128 tokens of 2,
-// 127 us with both and 61 with tiles alone; 60 of 2048 x 1408, 512 tokens of 4, 80 and 38).
-// Below that the experts have a few rows each and stream (64 tokens of those 60: 35 and 38),
-// but for the ones that an uneven routing made long.
+// The product.  Few tiles leave most of the device idle, and the stream product, split over
+// K and over chunks of 32 rows, fills it although each chunk reads the weights again.  Up to
+// 64 chunks of 256 weight rows (32 with a 16-bit out, whose tiles are faster) it is ahead: to
+// fp32, 256 rows of 2048 x 2048 (64 chunks) 20 us as tiles and 17 as chunks, 64 of 6144 x 4096
+// (48) 33 and 26, 512 of 2048 x 2048 (128) 21 and 26, 128 of 6144 x 4096 (96) 34 and 44; to
+// fp16, 128 rows of 2048 x 2048 (32) 14.5 and 12.3, 192 (48) 14.5 and 17.  With more and above
+// 32 tokens tiles: 8 experts of 4096 x 7168, 128 tokens of 2, 61 us against 127.  Experts with
+// a few rows each stream a little faster if the routing is even (60 of 2048 x 1408, 64 tokens
+// of 4, 35 us against 40), and much slower if it is not, when few experts' waves are left
+// (the same with most of the experts idle 40 against 16; 64 of 1024 x 2048, 64 tokens of 2,
+// 44 against 20).
 //
 // gate_up, whose stream product is not split over K.  More than 32 rows take tiles (E = 1,
 // 48 rows of 2 x 2048 x 4096: 77 us streamed, 33 as tiles), and more than 16 where every CU
 // has one at most (24 rows of that one expert 69 and 31; 8 experts of 2 x 2048 x 7168, 32
 // tokens of 2, 128 tiles, 82 and 56; of 2 x 4096 x 4096, 256 tiles, 53 and 67).
-bool share_rows(Fp8Params &P, int most, bool act, bool exact, bool &tile)
+bool takes_tiles(const Fp8Params &P, int most, bool act, bool exact)
 {
-    P.stream_max = 0;
-    const long tiles = fp8_tiles(P, act, fp8_tile_tokens(exact));
     if (act)
-        tile = most > kStreamMax || (most > 16 && tiles < kCus);
-    else
-        tile = most > kStreamMax && fp8_tiles(P, act, kStreamMax) > (exact ? 64 : 32);
-    if (!tile)
-        P.stream_max = INT_MAX;
-    else if (!act && P.E > 1 && P.R < 8l * P.E)
-        P.stream_max = kStreamMax;
-    return !tile || tiles <= kMaxTiles;
+        return most > kStreamMax || (most > 16 && fp8_tiles(P, act, fp8_tile_tokens(exact)) < kCus);
+    return most > kStreamMax && fp8_tiles(P, act, kStreamMax) > (exact ? 64 : 32);
 }
 
 }  // namespace
@@ -256,12 +243,11 @@ hipError_t launch_gemm_fp8(const uint8_t *x8, const float *xs, const uint8_t *w8
                            int gather, const int32_t *perm, const int32_t *offsets, int topk, int R, void *out,
                            int out_dtype, bool exact, hipStream_t s)
 {
-    Fp8Params P{x8, xs, w8, ws, perm, offsets, out, nullptr, E, N, K, topk, gather, out_dtype, R, 0, kStreamMax};
+    const Fp8Params P{x8, xs, w8, ws, perm, offsets, out, nullptr, E, N, K, topk, gather, out_dtype, R, 0};
     const int most = most_rows(P);
-    bool tile;
-    if (!share_rows(P, most, false, exact, tile))
-        return hipErrorInvalidValue;
-    const unsigned chunks = (unsigned)((tile ? 1 : most) + kStreamMax - 1) / kStreamMax;
+    if (takes_tiles(P, most, false, exact))
+        return launch_fp8_tile(P, false, exact, s);
+    const unsigned chunks = (unsigned)(most + kStreamMax - 1) / kStreamMax;
     // KS: enough waves to fill the device, 8 on a CU (KS = 1, 2, 4, 8: 6144 x 4096, 192 waves,
     // 47, 26, 16, 10.9 us; 28672 x 4096, 896 waves, 47, 29, 32, 36; 8 experts of 4096 x 2048,
     // 1024 waves, 23, 14.8, 17, 21; 60 of 2048 x 1408, 3840 waves, 31, 31, 30, 40).
@@ -278,9 +264,7 @@ hipError_t launch_gemm_fp8(const uint8_t *x8, const float *xs, const uint8_t *w8
         else
             hipLaunchKernelGGL((stream_kernel<KS, 1>), grid, block, 0, s, P);
     };
-    if (P.stream_max == 0)
-        ;  // all are the tile product's
-    else if (waves >= 2048 || KB < 4)
+    if (waves >= 2048 || KB < 4)
         go(std::integral_constant<int, 1>{});
     else if (waves >= 768 || KB < 8)
         go(std::integral_constant<int, 2>{});
@@ -288,32 +272,25 @@ hipError_t launch_gemm_fp8(const uint8_t *x8, const float *xs, const uint8_t *w8
         go(std::integral_constant<int, 4>{});
     else
         go(std::integral_constant<int, 8>{});
-    const hipError_t e = tile ? launch_fp8_tile(P, false, exact, s) : hipSuccess;
-    return e == hipSuccess ? hipGetLastError() : e;
+    return hipGetLastError();
 }
 
 hipError_t launch_gemm_act_fp8(const uint8_t *x8, const float *xs, const uint8_t *w8, const float *ws, int E, int F,
                                int K, int gather, const int32_t *perm, const int32_t *offsets, int topk, int R,
                                uint8_t *a8, float *as, hipStream_t s)
 {
-    Fp8Params P{x8, xs, w8, ws, perm, offsets, a8, as, E, 2 * F, K, topk, gather, 0, R, F, kStreamMax};
+    const Fp8Params P{x8, xs, w8, ws, perm, offsets, a8, as, E, 2 * F, K, topk, gather, 0, R, F};
     const dim3 grid((F + kBlk - 1) / kBlk, E);
     const int most = most_rows(P);
-    bool tile;
-    if (!share_rows(P, most, true, true, tile))
-        return hipErrorInvalidValue;
+    if (takes_tiles(P, most, true, true))
+        return launch_fp8_tile(P, true, true, s);
     // Up to 16 rows four waves with two pairs of tiles each, three workgroups on a CU (16 tokens,
     // 8 experts of 2 x 14336 x 4096: 172 us, eight waves with one pair 176); more rows have no
     // registers for that.
-    if (tile) {
-        const hipError_t e = launch_fp8_tile(P, true, true, s);
-        if (e != hipSuccess)
-            return e;
-    } else if (most > 16) {
+    if (most > 16)
         hipLaunchKernelGGL((stream_act_kernel<2, 1>), grid, dim3(kStreamWaves * kWave), 0, s, P);
-    } else {
+    else
         hipLaunchKernelGGL((stream_act_kernel<1, 2>), grid, dim3(kStreamWaves / 2 * kWave), 0, s, P);
-    }
     return hipGetLastError();
 }
 

@@ -1,4 +1,4 @@
-// gemm_fp8_tile.hip -- the e4m3 product of experts with many rows: LDS tiles of weights
+// gemm_fp8_tile.hip -- the e4m3 product of calls with many rows: LDS tiles of weights
 // and tokens, matrix units fed from them.
 //
 // Tile: 256 weight rows in two halves of 128 (with the activation: 128 gate rows and the
@@ -30,6 +30,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kHalf = 128;  // weight rows of a half
 constexpr int kXcdCus = 32;
+constexpr long kMaxTiles = (1l << 23) - 256;  // a launch has fewer than 2^32 threads
 constexpr int kGroup = 8;   // weight tiles that share their token tiles through an XCD's L2
 constexpr uint32_t kStageW = 2 * kHalf * kBlk;
 // LDS of tiles of TOK tokens: NB buffers, each a stage and its tokens' scales.  A stage is
@@ -55,7 +56,7 @@ struct Tile {
 };
 
 // Workgroup -> tile, in scalar registers; every wave computes the same answer.  Tiles in
-// order: groups of kGroup weight tiles, in a group the token tiles of every served
+// order: groups of kGroup weight tiles, in a group the token tiles of every
 // expert, then the group's weight tiles.  XCD x (workgroups b with b % 8 = x) takes the
 // x-th eighth.  Lane l counts the token tiles of experts 4l .. 4l+3.
 //
@@ -74,7 +75,7 @@ __device__ inline bool resolve(const TileParams &T, int tok, Tile &t)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int m = o[i + 1] - o[i];
-        n[i] = m > P.stream_max ? (m + tok - 1) / tok : 0;
+        n[i] = m > 0 ? (m + tok - 1) / tok : 0;
         sum += n[i];
     }
     int incl = sum;
@@ -653,15 +654,17 @@ static int weight_tiles(const Fp8Params &P, bool act)
 
 long fp8_tiles(const Fp8Params &P, bool act, int tok)
 {
-    const int served = P.E < P.R / (P.stream_max + 1) ? P.E : P.R / (P.stream_max + 1);
+    const int served = P.E < P.R ? P.E : P.R;
     return ((long)(P.R - served) / tok + served) * weight_tiles(P, act);  // ceil(m / tok) = (m - 1) / tok + 1
 }
 
 hipError_t launch_fp8_tile(const Fp8Params &P, bool act, bool exact, hipStream_t s)
 {
     const TileParams T{P, weight_tiles(P, act)};
-    const long round = kXcds * kXcdCus;  // the last one whole: its tiles may be split
-    const long grid = (fp8_tiles(P, act, fp8_tile_tokens(exact)) + round - 1) / round * round;
+    const long tiles = fp8_tiles(P, act, fp8_tile_tokens(exact)), round = kXcds * kXcdCus;
+    if (tiles > kMaxTiles)
+        return hipErrorInvalidValue;
+    const long grid = (tiles + round - 1) / round * round;  // the last round whole: its tiles may be split
     if (act)
         hipLaunchKernelGGL((fp8_tile_kernel<true, true>), dim3((unsigned)grid), dim3(kThreads), 0, s, T);
     else if (exact)
