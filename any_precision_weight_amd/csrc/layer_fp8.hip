@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(NW *kWave, NP == 2 ? 3 : 4) few_gate_up(const 
 struct DownStage {
     Frag8 a, b;
     float sw, f;
-    bool chosen, lo, hi;  // whether the token chose the expert; whether b.lo / b.hi are its columns
+    bool chosen, lo, hi;  // whether the token chose the expert; whether b.lo / b.hi are columns below F
 };
 
 // blockIdx.x: 16 columns of the output.  QUANT: a32 is quantised into LDS first.
@@ -359,12 +359,12 @@ __global__ void __launch_bounds__(kThreads) few_down(const FewParams P)
         s.a.lo = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(wb + (uint32_t)(j % 8) * (uint32_t)F + col));
         s.a.hi = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(wb + (uint32_t)(8 + j % 8) * (uint32_t)F + col));
         s.sw = P.down_s[((size_t)e * nbk + n0 / kBlk) * FB + kb];
-        // a token that did not choose the expert has zeros there; what is loaded for it is
-        // another row's (no request is skipped: stream_product)
+        // what is loaded for a token that did not choose the expert is another row's (no
+        // request is skipped: stream_product)
         const int r = rows[ai][j], rc = max(r, 0), c = kb * kBlk + 16 * g;
         s.chosen = r >= 0;
-        s.lo = r >= 0 && c < F;
-        s.hi = r >= 0 && c + 64 < F;
+        s.lo = c < F;
+        s.hi = c + 64 < F;
         const char *q8 = QUANT ? smem + rc * F : reinterpret_cast<const char *>(P.a8) + (size_t)rc * F;
         s.b.lo = *reinterpret_cast<const u32x4 *>(q8 + (c < F ? c : 0));
         s.b.hi = *reinterpret_cast<const u32x4 *>(q8 + (c + 64 < F ? c + 64 : 0));
@@ -378,10 +378,12 @@ __global__ void __launch_bounds__(kThreads) few_down(const FewParams P)
             b.hi[i] = s.hi ? s.b.hi[i] : 0u;
         }
         const float4v p = block_product(to_frag16(whole_rows(s.a)), to_frag16(b));
-        const float f = s.chosen ? s.f * s.sw : 0.f;
+        const float f = s.f * s.sw;
+        // selected, not multiplied by zero: a NaN weight or scale of an expert is not for the
+        // tokens that did not choose it
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            acc[i] = __builtin_fmaf(p[i], f, acc[i]);
+            acc[i] = s.chosen ? __builtin_fmaf(p[i], f, acc[i]) : acc[i];
     };
     if (n > 0) {
         constexpr int D = kDownDepth;

@@ -507,6 +507,36 @@ def test_layer_with_a_nan_token(T):
     assert np.all(np.abs(got[:T] - want) <= bound)
 
 
+@pytest.mark.parametrize("part", ["gate_up", "down", "down_scale"])
+@pytest.mark.parametrize("T,H,F", [(3, 272, 144), (16, 272, 144), (3, 1040, 8208), (24, 272, 144)])
+def test_layer_nan_weights_stay_with_their_expert(T, H, F, part):
+    """A NaN in an expert's weights is for the tokens that chose it alone: the others' bits
+    are those of the call without it.  With 8208 values of F the activation is quantised by
+    gate_up, with 144 by down."""
+    r = rng_of("nan-expert", T, H, F, part)
+    E, topk = 6, 2
+    d = layer_inputs(r, E, 0, H, F, T)
+    z = d["x"].astype(np.float64) @ d["wr"].astype(np.float64).T
+    chosen = np.argsort(-z, axis=1, kind="stable")[:, :topk]
+    e = next(e for e in range(E) if 0 < (chosen == e).any(axis=1).sum() < T)
+    mine = (chosen == e).any(axis=1)
+    before, _ = run_layer(d, None, E, 0, H, F, T, topk, True)
+    cols = np.zeros(H, bool)
+    if part == "gate_up":  # one value of the activation, and so its group: every output
+        d["w1"][e, 5, 7] = 0x7F
+        cols[:] = True
+    elif part == "down":
+        d["w2"][e, 40, F - 3] = 0xFF
+        cols[40] = True
+    else:
+        d["s2"][e, 0, 0, -1] = np.nan
+        cols[:128] = True
+    got, _ = run_layer(d, None, E, 0, H, F, T, topk, True)
+    want = before.copy()
+    want[np.ix_(mine, cols)] = np.nan
+    np.testing.assert_array_equal(got, want)
+
+
 @pytest.mark.parametrize("T", [1, 4, 16, 20])
 def test_layer_ties_go_to_the_lower_expert(T):
     """Identical router rows: every token takes experts 0 .. topk-1."""
