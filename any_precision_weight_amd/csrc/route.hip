@@ -74,7 +74,6 @@ __device__ __attribute__((always_inline)) inline void route_token(const uint16_t
 
     // top-k: each lane owns experts lane, lane+64, ...
     unsigned taken = 0;  // bit i: expert lane + 64*i selected
-    double zsel[APMOE_MAX_TOPK];
     int esel[APMOE_MAX_TOPK];
     for (int j = 0; j < topk; ++j) {
         double bz = -INFINITY;
@@ -100,21 +99,18 @@ __device__ __attribute__((always_inline)) inline void route_token(const uint16_t
         }
         if (be % kWave == lane)
             taken |= 1u << (be / kWave);
-        zsel[j] = bz;
         esel[j] = be;
     }
     // Softmax weights, one lane per term: lane j < topk takes choice j's exponential;
     // the denominator is those (renormalize) or every expert's exponential, lane u
-    // summing experts u, u + 64, ..., reduced in a fixed tree and taken from lane 0.
-    const double zmax = zsel[0];
-    double zl = zsel[0];
+    // summing experts u, u + 64, ..., reduced in a fixed tree and taken from lane 0.  The
+    // logits are those of the formula: a NaN among them makes the weights NaN.
     int el = esel[0];
 #pragma unroll
     for (int j = 1; j < APMOE_MAX_TOPK; ++j)
-        if (j < topk && j == lane) {
-            zl = zsel[j];
+        if (j < topk && j == lane)
             el = esel[j];
-        }
+    const double zmax = zs[esel[0]], zl = zs[el];
     const double ex = lane < topk ? exp(zl - zmax) : 0.0;
     double term = 0.0;
     if (renormalize) {

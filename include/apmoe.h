@@ -259,9 +259,11 @@ apmoe_status apmoe_page_in(apmoe_ctx *ctx, apmoe_table *tbl, int32_t layer, int3
  * Router (Section 2.1: the router weights E experts and keeps the top K).
  *   x [T][H] fp16, w_router [E][H] fp16 (E routed experts), bias [E] fp32 or NULL.
  *   logit z[t][e] = sum_h x*w in fp64 (exact fp16 products), then + bias[e].
- *   topk_ids [T][topk] : experts by descending logit, ties to the lower index.
+ *   topk_ids [T][topk] : experts by descending logit, ties to the lower index; a NaN
+ *                        logit compares as -infinity, so the ids of a token are distinct.
  *   topk_w   [T][topk] : fp32; renormalize != 0: softmax over the selected
- *                        logits; else the full softmax over E, at the selected.
+ *                        logits; else the full softmax over E, at the selected.  A NaN
+ *                        among those logits makes the token's weights NaN.
  *   Shared experts (Table 1 lists "+4" / "+1" experts visited by every token):
  *   experts E .. E+n_shared-1 have no router row; the pages give no gate for them,
  *   so they follow the topk routed experts in every token's row with weight 1.

@@ -491,6 +491,64 @@ def test_route_with_a_nan_token(T):
     assert int(offsets[-1]) == T * topk
 
 
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("T", [2, 24, 300])
+def test_route_nan_logits(T, renorm):
+    """NaN logits of some experts: they are chosen last, the lowest index first, and the
+    softmax takes them as they are: a chosen one makes the weights NaN, one that is not
+    chosen only the full softmax's."""
+    r = rng_of("route-nan-logits", T)
+    H, E, topk = 64, 6, 3
+    x, wr = r.normal(size=(T, H)).astype(np.float16), r.normal(size=(E, H)).astype(np.float16)
+    z = x.astype(np.float64) @ wr.astype(np.float64).T
+    for nan in ([4], [1, 2, 4, 5]):
+        bias = np.zeros(E, np.float32)
+        bias[nan] = np.nan
+        ids, perm, inv = (torch.full((T * topk,), -1, dtype=torch.int32, device="cuda") for _ in range(3))
+        w = torch.empty((T, topk), device="cuda")
+        counts, offsets = (torch.empty(n, dtype=torch.int32, device="cuda") for n in (E, E + 1))
+        apw.route(ctx(), cuda(x), cuda(wr), cuda(bias), T, H, E, topk, renorm, ids, w, counts, offsets, perm, inv)
+        torch.cuda.synchronize()
+        ids, w = ids.view(T, topk).cpu().numpy(), w.cpu().numpy()
+        zn = z.copy()
+        zn[:, nan] = -np.inf
+        want = np.argsort(-zn, axis=1, kind="stable")[:, :topk]
+        np.testing.assert_array_equal(ids, want)
+        if renorm and nan == [4]:
+            p = np.exp(np.take_along_axis(z, want, 1) - z[:, [0, 1, 2, 3, 5]].max(axis=1, keepdims=True))
+            # fp64 sums of 64 terms and one rounding to fp32
+            np.testing.assert_allclose(w, p / p.sum(axis=1, keepdims=True), rtol=2.0 ** -23)
+        else:
+            assert np.isnan(w).all()
+
+
+@pytest.mark.parametrize("T", [2, 24, 300])
+def test_layer_nan_logits(T):
+    """The same rule in the layer, below and above 16 tokens: an expert whose logit is NaN
+    and that is not chosen is as one at -infinity; a chosen one makes the output NaN; one
+    at -infinity that is chosen has weight 0."""
+    r = rng_of("layer-nan-logits", T)
+    E, topk, H, F = 6, 3, 272, 144
+    d = layer_inputs(r, E, 0, H, F, T)
+    low = np.zeros(E, np.float32)
+    low[[4]] = -np.inf
+    want, bound = layer_ref(d, low, E, 0, H, F, T, topk, True)
+    got, _ = run_layer(d, low, E, 0, H, F, T, topk, True)
+    assert np.all(np.abs(got - want) <= bound)
+    nan = low.copy()
+    nan[4] = np.nan
+    again, _ = run_layer(d, nan, E, 0, H, F, T, topk, True)
+    np.testing.assert_array_equal(again, got)
+    assert np.isnan(run_layer(d, nan, E, 0, H, F, T, topk, False)[0]).all()
+    low[[1, 2, 5]] = -np.inf
+    want, bound = layer_ref(d, low, E, 0, H, F, T, topk, True)
+    got, _ = run_layer(d, low, E, 0, H, F, T, topk, True)
+    assert np.all(np.abs(got - want) <= bound)
+    nan = low.copy()
+    nan[1] = np.nan  # the third choice of every token
+    assert np.isnan(run_layer(d, nan, E, 0, H, F, T, topk, True)[0]).all()
+
+
 @pytest.mark.parametrize("T", [1, 3, 20])
 def test_layer_with_a_nan_token(T):
     """A NaN in one token leaves the other tokens' outputs as they are."""
