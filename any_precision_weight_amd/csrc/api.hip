@@ -1346,11 +1346,22 @@ apmoe_status apmoe_moe_forward_fp8(apmoe_ctx *ctx, const apmoe_fp8_experts *ex, 
         const hipError_t few = apmoe::launch_few_layer(p, st);
         return few == hipSuccess ? ok() : hip_fail(few, "few-token layer launch");
     }
-    s = apmoe_route(ctx, x, w_router, bias, T, H, E - n_shared, topk, n_shared, renormalize, ids, tw, counts, offsets,
-                    perm, inv, stream);
-    if (s != APMOE_OK)
-        return s;
-    hipError_t e = apmoe::launch_gemm_act_fp8(x8, x_scale, ex->gate_up, ex->gate_up_scale, E, F, H, 1, perm, offsets,
+    hipError_t e = hipSuccess;
+    if (T <= apmoe::kFewTokens) {
+        // without the context's counter: calls of so few tokens may run at the same time on
+        // one context, whichever launches they take
+        e = apmoe::launch_route_topk(x, w_router, bias, T, H, E - n_shared, topk, n_shared, renormalize, ids, tw, st);
+        if (e == hipSuccess)
+            e = apmoe::launch_route_sort(ids, T * kt, E, counts, offsets, perm, inv, st);
+        if (e != hipSuccess)
+            return hip_fail(e, "route launch");
+    } else {
+        s = apmoe_route(ctx, x, w_router, bias, T, H, E - n_shared, topk, n_shared, renormalize, ids, tw, counts,
+                        offsets, perm, inv, stream);
+        if (s != APMOE_OK)
+            return s;
+    }
+    e = apmoe::launch_gemm_act_fp8(x8, x_scale, ex->gate_up, ex->gate_up_scale, E, F, H, 1, perm, offsets,
                                               kt, T * kt, a8, as, st);
     if (e == hipSuccess)
         e = apmoe::launch_gemm_fp8(a8, as, ex->down, ex->down_scale, E, H, F, 0, perm, offsets, kt, T * kt, y,

@@ -544,7 +544,8 @@ apmoe_status apmoe_moe_workspace_fp8(apmoe_ctx *ctx, const apmoe_fp8_experts *ex
  * aligned.  Every limit of the steps is checked before the first launch.  The call
  * enqueues only kernel launches on `stream`, so it can be captured in a HIP graph; two
  * calls (or two captured graphs) that may run at the same time need a workspace each,
- * and, as for apmoe_route, a context each (above 16 tokens).
+ * and above 16 tokens, as for apmoe_route, a context each; calls of up to 16 tokens use
+ * no counter of the context, whichever launches they take.
  */
 apmoe_status apmoe_moe_forward_fp8(apmoe_ctx *ctx, const apmoe_fp8_experts *ex, const uint16_t *x, const uint8_t *x8,
                                    const float *x_scale, const uint16_t *w_router, const float *bias, int32_t T,

@@ -663,6 +663,56 @@ def test_layer_on_two_streams_with_a_workspace_and_context_each():
     ctxs[1].close()
 
 
+@pytest.mark.parametrize("T,E,topk,H,F", [(8, 256, 4, 64, 64), (16, 8, 8, 64, 13056), (3, 8, 2, 256, 384)])
+def test_few_token_layers_at_once_on_one_context(T, E, topk, H, F):
+    """Up to 16 tokens two calls, or two captured graphs, may run at the same time on one
+    context with a workspace each; with 256 experts, or with scales of the activation that
+    LDS does not hold, they route in launches of their own."""
+    r = rng_of("one-context", T, E, F)
+    d = layer_inputs(r, E, 0, H, F, T)
+    ex = apw.Fp8Experts(cuda(d["w1"]), cuda(d["s1"]), cuda(d["w2"]), cuda(d["s2"]))
+    n = apw.moe_workspace_fp8(ctx(), ex, T, topk)
+    streams, calls, outs, wants = [torch.cuda.Stream() for _ in range(2)], [], [], []
+    for i in range(2):
+        o = layer_inputs(rng_of("one-context", T, E, F, i), 1, 0, H, 16, T)
+        args = [cuda(o["x"]), cuda(o["x8"]), cuda(o["xs"]), cuda(d["wr"]), None]
+        ws = torch.full((n,), 0xA5, dtype=torch.uint8, device="cuda")
+        out = torch.empty((T, H), dtype=torch.float16, device="cuda")
+
+        def call(args=args, ws=ws, out=out, s=streams[i]):
+            apw.moe_forward_fp8(ctx(), ex, *args, T, topk, True, ws, out, stream=s)
+        call()
+        torch.cuda.synchronize()
+        calls.append(call)
+        outs.append(out)
+        wants.append(out.clone())
+    assert not torch.equal(wants[0], wants[1])
+    for _ in range(30):
+        calls[0]()
+        calls[1]()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, wants):
+        assert torch.equal(o, w)
+        o.fill_(float("nan"))
+    graphs = []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=streams[i]):
+            calls[i]()
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for o in outs:
+            o.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, wants):
+            assert torch.equal(o, w)
+
+
 def test_norm_then_layer_then_norm():
     """The calls as a decode step makes them: norm with the residual -> layer on its two
     outputs -> the next norm adds the layer's output to the residual."""
