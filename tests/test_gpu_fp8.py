@@ -713,6 +713,34 @@ def test_few_token_layers_at_once_on_one_context(T, E, topk, H, F):
             assert torch.equal(o, w)
 
 
+@pytest.mark.parametrize("T", [1, 4, 16, 24])
+def test_layer_of_an_unfused_context_is_its_steps(T, monkeypatch):
+    """A context made under APMOE_UNFUSED=1 runs every step in its own launches, a few
+    tokens too: the bits of the route, the two products (to fp32) and the combine."""
+    monkeypatch.setenv("APMOE_UNFUSED", "1")
+    c = apw.Context(0)
+    r = rng_of("unfused", T)
+    E, topk, shared, H, F = 8, 2, 1, 272, 400
+    Et, kt, R = E + shared, topk + shared, T * (topk + shared)
+    d = layer_inputs(r, E, shared, H, F, T)
+    w1, s1, w2, s2, x, x8, xs, wr = (cuda(d[k]) for k in ("w1", "s1", "w2", "s2", "x", "x8", "xs", "wr"))
+    ex = apw.Fp8Experts(w1, s1, w2, s2)
+    ws = torch.empty(apw.moe_workspace_fp8(c, ex, T, topk, n_shared=shared), dtype=torch.uint8, device="cuda")
+    out, want = (torch.empty((T, H), dtype=torch.float16, device="cuda") for _ in range(2))
+    apw.moe_forward_fp8(c, ex, x, x8, xs, wr, None, T, topk, True, ws, out, n_shared=shared)
+    ids, perm, inv = (torch.empty(R, dtype=torch.int32, device="cuda") for _ in range(3))
+    w, y = torch.empty((T, kt), device="cuda"), torch.empty((R, H), device="cuda")
+    counts, off = (torch.empty(n, dtype=torch.int32, device="cuda") for n in (Et, Et + 1))
+    a8, sc = torch.empty((R, F), dtype=torch.uint8, device="cuda"), torch.empty((R, ref.groups(F)), device="cuda")
+    apw.route(c, x, wr, None, T, H, E, topk, True, ids, w, counts, off, perm, inv, n_shared=shared)
+    apw.gemm_act_fp8(c, x8, xs, w1, s1, Et, F, H, True, perm, off, T, kt, a8, sc)
+    apw.gemm_fp8(c, a8, sc, w2, s2, Et, H, F, False, perm, off, T, kt, y)
+    apw.combine(c, y, apw.F32, w, inv, T, kt, H, want)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    c.close()
+
+
 def test_norm_then_layer_then_norm():
     """The calls as a decode step makes them: norm with the residual -> layer on its two
     outputs -> the next norm adds the layer's output to the residual."""
