@@ -1339,7 +1339,7 @@ apmoe_status apmoe_moe_forward_fp8(apmoe_ctx *ctx, const apmoe_fp8_experts *ex, 
     if (dev.status() != APMOE_OK)
         return dev.status();
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-    if (ctx->fuse && apmoe::few_layer_fits(T, kt, E - n_shared, F)) {
+    if (ctx->fuse && apmoe::few_layer_fits(T, topk, kt, E - n_shared, H, F)) {
         const apmoe::FewParams p{x, x8, x_scale, w_router, bias, ex->gate_up, ex->gate_up_scale, ex->down,
                                  ex->down_scale, T, topk, kt, E - n_shared, H, F, renormalize,
                                  reinterpret_cast<double *>(w + L.z), ids, tw, a8, as, y, out, 0};

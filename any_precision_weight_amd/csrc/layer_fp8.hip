@@ -19,10 +19,9 @@
 //                   workgroup.
 //
 // Nothing is counted or waited for between workgroups.  Measured: one token, 8 of 60 + 4
-// experts of 1408 x 2048, 29.8 us (2 + 15 + 11 in the kernels, 2.3 TB/s: latency); four tokens,
-// 8 experts of 14336 x 4096, 173 to 199 us by the experts they reach (5.7 TB/s).  Against the
-// route, products and combine in launches of their own: one token of those small experts 31
-// against 54 us, 16 tokens of 60 of them 113 and 122, 16 tokens of 8 large ones 278 and 267.
+// experts of 1408 x 2048, 29.8 us (2 + 15 + 11 in the kernels at best, 2.3 TB/s: latency);
+// four tokens, 8 experts of 14336 x 4096, 173 to 199 us by the experts they reach (5.7 TB/s).
+// few_layer_fits has both sides of the choice against the steps' own launches.
 #include "gemm_fp8.h"
 #include "layer_fp8.h"
 #include "stream_fp8.h"

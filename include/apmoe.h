@@ -533,11 +533,12 @@ apmoe_status apmoe_moe_workspace_fp8(apmoe_ctx *ctx, const apmoe_fp8_experts *ex
 
 /*
  * Whole layer on e4m3 experts: apmoe_route on x, apmoe_gemm_act_fp8 on (x8, x_scale),
- * apmoe_gemm_fp8 into fp32 (with the sums of a 16-bit out), apmoe_combine.  Up to 16
- * tokens (T * E^2 up to 2^18) take three launches: the logits (summed in another order
- * than apmoe_route's), the selection inside the gate_up launch, then down with the sum
- * over the experts, in the order of the experts, in its accumulators; with a context
- * made under APMOE_UNFUSED=1 they take the steps' own launches too.  x fp16 [T][H] is what
+ * apmoe_gemm_fp8 into fp32 (with the sums of a 16-bit out), apmoe_combine.  Most batches of
+ * up to 16 tokens (a rule on tokens, experts and sizes) take three launches: the logits
+ * (summed in another order than apmoe_route's), the selection inside the gate_up launch,
+ * then down with the sum over the experts, in the order of the experts, in its
+ * accumulators; with a context made under APMOE_UNFUSED=1 they take the steps' own launches
+ * too.  A token's last bits may so depend on the batch that it is in.  x fp16 [T][H] is what
  * the router reads, x8 and x_scale the same rows in 8 bits (apmoe_norm gives both); out
  * fp16 [T][H].
  * The first E - n_shared experts are the routed ones (w_router rows, bias as in
