@@ -1148,6 +1148,8 @@ apmoe_status fp8_args(const uint8_t *x8, const float *x_scale, const uint8_t *w8
                     APMOE_MAX_EXPERTS, kMaxCols8);
     if (T < 0 || topk < 1 || topk > APMOE_MAX_ASSIGN || (int64_t)T * topk > (int64_t)1 << 30)
         return fail(APMOE_INVALID_ARG, "T=%d topk=%d", T, topk);
+    if (!apmoe::fp8_tiles_fit(E, N, T * topk))
+        return fail(APMOE_INVALID_ARG, "T=%d topk=%d E=%d N=%d: more than 2^30 tiles", T, topk, E, N);
     if (!offsets && E != 1)
         return fail(APMOE_INVALID_ARG, "offsets is NULL with %d experts", E);
     if (T == 0)
@@ -1201,9 +1203,14 @@ apmoe_status fp8_layer_sizes(const apmoe_fp8_experts *ex, int32_t T, int32_t top
                     ex->F, APMOE_MAX_EXPERTS, kMaxCols8);
     if (n_shared < 0 || n_shared > APMOE_MAX_SHARED || n_shared >= ex->E)
         return fail(APMOE_INVALID_ARG, "n_shared=%d with %d experts", n_shared, ex->E);
-    if (T < 0 || topk < 1 || topk > APMOE_MAX_TOPK || topk > ex->E - n_shared ||
-        (int64_t)T * (topk + n_shared) > (int64_t)1 << 30)
-        return fail(APMOE_INVALID_ARG, "T=%d topk=%d", T, topk);
+    if (T < 0 || T >= 1 << 24 || topk < 1 || topk > APMOE_MAX_TOPK || topk > ex->E - n_shared)
+        return fail(APMOE_INVALID_ARG, "T=%d topk=%d (need 0 <= T < 2^24, 1 <= topk <= min(%d, routed experts))", T,
+                    topk, APMOE_MAX_TOPK);
+    if ((int64_t)T * ex->H >= (int64_t)1 << 35)  // the combine has a thread for 8 values
+        return fail(APMOE_INVALID_ARG, "T=%d H=%d (need T * H < 2^35)", T, ex->H);
+    const int R = T * (topk + n_shared);  // below 2^28
+    if (!apmoe::fp8_tiles_fit(ex->E, 2l * ex->F, R) || !apmoe::fp8_tiles_fit(ex->E, ex->H, R))
+        return fail(APMOE_INVALID_ARG, "T=%d topk=%d E=%d H=%d F=%d: more than 2^30 tiles", T, topk, ex->E, ex->H, ex->F);
     return ok();
 }
 

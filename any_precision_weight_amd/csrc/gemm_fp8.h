@@ -2,6 +2,7 @@
 #pragma once
 
 #include "fp8.h"
+#include "launch_fp8.h"
 
 namespace apmoe {
 
@@ -86,10 +87,9 @@ __device__ inline void store4(const Fp8Params &P, size_t row, int n, const float
 inline int most_rows(const Fp8Params &P) { return P.E == 1 ? P.R : P.R / P.topk; }
 
 // Tokens of a tile: 128 where the products of a stage stay in registers.
-constexpr int fp8_tile_tokens(bool exact) { return exact ? 128 : 256; }
+constexpr int fp8_tile_tokens(bool exact) { return exact ? kMinTileTokens : 256; }
 
-// Upper bound of the tiles of `tok` rows: for each expert that may have rows the last one
-// started, times the tiles of weights.
+// Upper bound of the tiles of `tok` rows: of the rows times of the weights.
 long fp8_tiles(const Fp8Params &P, bool act, int tok);
 
 // exact: fp32 sums inside a block (block_product), which fp32 results keep.

@@ -22,6 +22,8 @@
 // there is room for 6 others.  Measured: 4096 x 6144 x 4096 to fp16 107 us, 1.93 PFLOP/s;
 // through fp16 products 8 experts of 4096 x 14336 with 4096 rows, unevenly, 518 us, 0.93, and
 // gate_up of the same layer's 8192 rows 1.8 ms, 1.07.
+#include <algorithm>
+
 #include "gemm_fp8.h"
 
 namespace apmoe {
@@ -30,7 +32,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kHalf = 128;  // weight rows of a half
 constexpr int kXcdCus = 32;
-constexpr long kMaxTiles = (1l << 23) - 256;  // a launch has fewer than 2^32 threads
+constexpr int kGridX = 1 << 20;  // workgroups in x: a dimension has fewer than 2^32 threads
 constexpr int kGroup = 8;   // weight tiles that share their token tiles through an XCD's L2
 constexpr uint32_t kStageW = 2 * kHalf * kBlk;
 // LDS of tiles of TOK tokens: NB buffers, each a stage and its tokens' scales.  A stage is
@@ -86,7 +88,8 @@ __device__ inline bool resolve(const TileParams &T, int tok, Tile &t)
     }
     const int MT = __builtin_amdgcn_readlane(incl, kWave - 1);
     const int total = MT * T.NT, per = (total + kXcds - 1) / kXcds;
-    const int first = ((int)blockIdx.x % kXcds) * per, local = (int)blockIdx.x / kXcds;
+    const int block = (int)(blockIdx.y * kGridX + blockIdx.x);
+    const int first = (block % kXcds) * per, local = block / kXcds;
     const int mine = max(0, min(per, total - first)), rem = mine % kXcdCus;
     const int parts = tok >= 256 && 4 * rem <= kXcdCus ? 4 : 2 * rem <= kXcdCus ? 2 : 1;
     const int over = local - (mine - rem);  // workgroup of the last round
@@ -654,23 +657,21 @@ static int weight_tiles(const Fp8Params &P, bool act)
 
 long fp8_tiles(const Fp8Params &P, bool act, int tok)
 {
-    const int served = P.E < P.R ? P.E : P.R;
-    return ((long)(P.R - served) / tok + served) * weight_tiles(P, act);  // ceil(m / tok) = (m - 1) / tok + 1
+    return fp8_token_tiles(P.E, P.R, tok) * weight_tiles(P, act);
 }
 
 hipError_t launch_fp8_tile(const Fp8Params &P, bool act, bool exact, hipStream_t s)
 {
     const TileParams T{P, weight_tiles(P, act)};
     const long tiles = fp8_tiles(P, act, fp8_tile_tokens(exact)), round = kXcds * kXcdCus;
-    if (tiles > kMaxTiles)
-        return hipErrorInvalidValue;
-    const long grid = (tiles + round - 1) / round * round;  // the last round whole: its tiles may be split
+    const long blocks = (tiles + round - 1) / round * round;  // the last round whole: its tiles may be split
+    const dim3 grid((unsigned)std::min(blocks, (long)kGridX), (unsigned)((blocks + kGridX - 1) / kGridX));
     if (act)
-        hipLaunchKernelGGL((fp8_tile_kernel<true, true>), dim3((unsigned)grid), dim3(kThreads), 0, s, T);
+        hipLaunchKernelGGL((fp8_tile_kernel<true, true>), grid, dim3(kThreads), 0, s, T);
     else if (exact)
-        hipLaunchKernelGGL((fp8_tile_kernel<true, false>), dim3((unsigned)grid), dim3(kThreads), 0, s, T);
+        hipLaunchKernelGGL((fp8_tile_kernel<true, false>), grid, dim3(kThreads), 0, s, T);
     else
-        hipLaunchKernelGGL((fp8_tile_kernel<false, false>), dim3((unsigned)grid), dim3(kThreads), 0, s, T);
+        hipLaunchKernelGGL((fp8_tile_kernel<false, false>), grid, dim3(kThreads), 0, s, T);
     return hipGetLastError();
 }
 

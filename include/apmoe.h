@@ -489,7 +489,8 @@ apmoe_status apmoe_norm(apmoe_ctx *ctx, const void *x, int32_t x_dtype, const vo
  * written.  A dense product is E = 1, topk = 1 with offsets NULL
  * (every row is the one expert's) and gather = 0.
  * Limits: 1 <= E <= 256, 1 <= N <= 2^30, K % 16 == 0, 16 <= K < 2^24, 1 <= topk <= 16, T >= 0,
- * T * topk <= 2^30.  Errors (nothing enqueued): INVALID_ARG for NULL or misaligned
+ * T * topk <= 2^30, and at most 2^30 tiles: (T * topk / 128 + E) * ceil(N / 256) <= 2^30
+ * always fits.  Errors (nothing enqueued): INVALID_ARG for NULL or misaligned
  * pointers (16 bytes; scales, perm and offsets 4), offsets NULL with E > 1, or bad
  * sizes; UNSUPPORTED for another out_dtype.
  */
@@ -506,7 +507,8 @@ apmoe_status apmoe_gemm_fp8(apmoe_ctx *ctx, const uint8_t *x8, const float *x_sc
  *   [E][2][ceil(F/128)][ceil(K/128)]: each half has blocks of its own (the layout of a
  *   [2F][K] matrix where F % 128 == 0);
  *   a8 e4m3 [T*topk][F], a_scale fp32 [T*topk][ceil(F/128)].
- * F % 16 == 0, 16 <= F < 2^24; other arguments, limits and errors as apmoe_gemm_fp8.
+ * F % 16 == 0, 16 <= F < 2^24; other arguments, limits (N = 2F) and errors as
+ * apmoe_gemm_fp8.
  */
 apmoe_status apmoe_gemm_act_fp8(apmoe_ctx *ctx, const uint8_t *x8, const float *x_scale, const uint8_t *w8,
                                 const float *w_scale, int32_t E, int32_t F, int32_t K, int32_t gather,
@@ -544,7 +546,8 @@ apmoe_status apmoe_moe_workspace_fp8(apmoe_ctx *ctx, const apmoe_fp8_experts *ex
  * The first E - n_shared experts are the routed ones (w_router rows, bias as in
  * apmoe_route), the last n_shared see every token with weight 1.
  * ws is caller-owned device memory of at least apmoe_moe_workspace_fp8 bytes, 256-byte
- * aligned.  Every limit of the steps is checked before the first launch.  The call
+ * aligned.  Limits: T < 2^24, T * H < 2^35 and those of the steps, all checked before the
+ * first launch (a refused call enqueues nothing).  The call
  * enqueues only kernel launches on `stream`, so it can be captured in a HIP graph; two
  * calls (or two captured graphs) that may run at the same time need a workspace each,
  * and above 16 tokens, as for apmoe_route, a context each; calls of up to 16 tokens use

@@ -62,6 +62,27 @@ def test_gemm_of_too_many_weight_rows():
     assert call("apmoe_gemm_fp8", *gemm_args(N=(1 << 30) + 1)) == apw.INVALID_ARG
 
 
+@pytest.mark.parametrize("kw", [dict(E=256, N=1 << 30, T=8192, topk=1), dict(N=1 << 30, T=1 << 17), dict(N=1 << 20, T=1 << 29)])
+def test_products_of_too_many_tiles(kw):
+    assert call("apmoe_gemm_fp8", *gemm_args(**kw)) == apw.INVALID_ARG
+    assert b"tiles" in apw.lib().apmoe_last_error()
+    assert call("apmoe_gemm_act_fp8", *gemm_args(**dict(kw, E=256, N=(1 << 24) - 128, T=1 << 20, dt=A))) == apw.INVALID_ARG
+    assert b"tiles" in apw.lib().apmoe_last_error()
+
+
+@pytest.mark.parametrize("ex,kw", [
+    (dict(E=256, H=16, F=(1 << 24) - 128), dict(T=1 << 18, topk=8)), (dict(E=256, H=(1 << 24) - 128, F=16), dict(T=1 << 22)),
+    ({}, dict(T=1 << 24)), (dict(H=1 << 20), dict(T=1 << 15)), ({}, dict(T=1 << 28, topk=1, shared=0))])
+def test_layer_size_limits_come_before_the_first_launch(ex, kw):
+    """Of the workspace too: sizes that the layer refuses have none."""
+    assert call("apmoe_moe_forward_fp8", *layer_args(desc(**ex), ws_bytes=(1 << 63) - 1, **kw)) == apw.INVALID_ARG
+    assert b"T=" in apw.lib().apmoe_last_error()
+    n = ctypes.c_size_t()
+    a = dict(dict(topk=2, shared=1), **kw)
+    assert call("apmoe_moe_workspace_fp8", CTX, ctypes.byref(desc(**ex)), a["T"], a["topk"], a["shared"],
+                ctypes.byref(n)) == apw.INVALID_ARG
+
+
 def test_gemm_of_no_rows():
     assert call("apmoe_gemm_fp8", *gemm_args(T=0)) == apw.OK
 

@@ -800,6 +800,29 @@ def test_gemm_rows_past_32_bits(N):
         check_part(x8[rows], xs[rows], w8[0, N - 16:], ws[0, -1], out[rows, N - 16:], K)
 
 
+def test_gemm_of_more_tiles_than_a_grid_dimension_holds():
+    """2^30 rows, the most that a call takes: 2^23 tiles of 128, each row checked."""
+    R, K = 1 << 30, 16
+    x8 = torch.empty((R, K), dtype=torch.uint8, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(5)
+    part = 1 << 25
+    for r in range(0, R, part):
+        x8[r:r + part] = torch.randint(0, 127, (part, K), dtype=torch.uint8, device="cuda", generator=g)
+    w8 = codes_on_gpu(6, 1, 1, K)
+    xs = torch.empty((R, 1), device="cuda").uniform_(0.5, 1.0, generator=g)
+    ws = torch.full((1, 1, 1), 2.0 ** -9, device="cuda")
+    out = torch.full((R, 1), float("nan"), device="cuda")
+    apw.gemm_fp8(ctx(), x8, xs, w8, ws, 1, 1, K, False, None, None, R, 1, out)
+    torch.cuda.synchronize()
+    table = torch.from_numpy(ref.TABLE).cuda()
+    w = table[w8.view(-1).long()] * 2.0 ** -9
+    part = 1 << 22
+    for r in range(0, R, part):
+        v = table[x8[r:r + part].int()] * xs[r:r + part].double()
+        want, mag = (v * w).sum(dim=1), (v * w).abs().sum(dim=1)
+        assert bool(((out[r:r + part, 0].double() - want).abs() <= mag * sum_bound(K)).all()), r
+
+
 @pytest.mark.parametrize("T", [6, 70])
 def test_gemm_weights_past_32_bits(T):
     E, N, K = 3, 20096, 73728
