@@ -376,10 +376,10 @@ def _load_types() -> None:
 def _arg(ctx: Context, t, name: str, n: int, types) -> int | None:
     """Pointer of an argument of n elements.  A tensor must have one of the types, be
     contiguous, lie on the context's device and hold at least n elements; None and raw
-    pointers are passed on."""
+    pointers (int) are passed on, without these checks."""
     if t is None or isinstance(t, int):
         return t
-    if t.dtype not in types or not t.is_contiguous() or t.numel() < n:
+    if n < 0 or t.dtype not in types or not t.is_contiguous() or t.numel() < n:
         raise ValueError(f"{name}: need {n} contiguous elements of {' / '.join(map(str, types))}, got "
                          f"{tuple(t.shape)} of {t.dtype}{'' if t.is_contiguous() else ', not contiguous'}")
     if t.get_device() != ctx.device:
@@ -394,11 +394,12 @@ def _stream_of(ctx: Context, stream) -> int | None:
 
 
 def _types(t, name: str):
-    """(number of the type in the C ABI, the type as a tuple) of a floating tensor."""
+    """(number of the type in the C ABI, the type as a tuple) of a floating tensor: the
+    arguments whose type a call takes from them must be tensors."""
     _load_types()
-    d = _float_ids.get(t.dtype)
+    d = _float_ids.get(getattr(t, "dtype", None))
     if d is None:
-        raise ValueError(f"{name}: {t.dtype} is not float16, bfloat16 or float32")
+        raise ValueError(f"{name}: need a tensor of float16, bfloat16 or float32, got {getattr(t, 'dtype', type(t))}")
     return d, (t.dtype,)
 
 
@@ -407,7 +408,7 @@ def norm(ctx: Context, x, residual, residual_out, gamma, eps: float, T: int, H: 
     """Root-mean-square norm of x + residual (residual None: of x).  residual_out gets
     the sum (it may be residual), y the norm in x's type and / or y8, y_scale the norm
     as e4m3 with a scale for each 128 columns.  Types are the tensors' own: float16,
-    bfloat16 or float32."""
+    bfloat16 or float32 (so x and residual must be tensors, no raw pointers)."""
     xt, xtypes = _types(x, "x")
     rt, rtypes = (0, xtypes) if residual is None else _types(residual, "residual")
     n = T * H
@@ -431,7 +432,7 @@ def _fp8_inputs(ctx, x8, x_scale, w8, w_scale, E, rows, n_scale, K, perm, offset
 def gemm_fp8(ctx: Context, x8, x_scale, w8, w_scale, E: int, N: int, K: int, gather: bool, perm, offsets, T: int,
              topk: int, out, stream=None) -> None:
     """The experts' product on e4m3 operands with fp32 scales (x_scale by 128 columns,
-    w_scale by 128 x 128 block); out's type is its tensor's.  Dense: E = topk = 1,
+    w_scale by 128 x 128 block); out is a tensor, whose type is taken.  Dense: E = topk = 1,
     gather False, perm and offsets None."""
     xp, xsp, wp, wsp, pp, op = _fp8_inputs(ctx, x8, x_scale, w8, w_scale, E, N, -(-N // 128), K, perm, offsets, T,
                                            topk, gather)
@@ -491,6 +492,8 @@ def moe_forward_fp8(ctx: Context, experts: Fp8Experts, x, x8, x_scale, w_router,
     """Whole layer on e4m3 experts: x fp16 is what the router reads, x8 / x_scale the
     same rows in 8 bits (norm gives both).  ws: a byte tensor of moe_workspace_fp8 bytes."""
     import torch
+    if not isinstance(ws, torch.Tensor):
+        raise ValueError(f"ws: need a byte tensor, got {type(ws)}")
     if experts.device != ctx.device:
         raise ValueError(f"the experts are on cuda:{experts.device}, the context on cuda:{ctx.device}")
     E, H = experts.E, experts.H

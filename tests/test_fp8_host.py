@@ -176,6 +176,33 @@ def test_binding_refuses_wrong_tensors():
         apw.norm(other, x, None, None, gamma, 1e-5, 4, 64, y, stream=_NoStream())
 
 
+def test_binding_refuses_what_has_no_type_or_size():
+    """Arguments whose type or size is the tensor's own must be tensors; sizes that wrap
+    around in 32 bits are refused."""
+    c, s = HostCtx(), _NoStream()
+    x, gamma = torch.zeros((4, 64), dtype=torch.float16), torch.ones(64, dtype=torch.float16)
+    y = torch.empty_like(x)
+    for bad in (A, None, [1.0], np.zeros((4, 64), np.float16)):
+        with pytest.raises(ValueError, match="x: need a tensor"):
+            apw.norm(c, bad, None, None, gamma, 1e-5, 4, 64, y, stream=s)
+        with pytest.raises(ValueError, match="out: need a tensor"):
+            apw.gemm_fp8(c, A, A, A, A, 1, 64, 64, False, None, None, 4, 1, bad, stream=s)
+    with pytest.raises(ValueError, match="residual: need a tensor"):
+        apw.norm(c, x, A, A, gamma, 1e-5, 4, 64, y, stream=s)
+    for T in (-1, 4 - 2 ** 32):
+        with pytest.raises(ValueError, match="x: need"):
+            apw.norm(c, x, None, None, gamma, 1e-5, T, 64, y, stream=s)
+    gu, dn = torch.zeros((2, 64, 64), dtype=torch.uint8), torch.zeros((2, 64, 32), dtype=torch.uint8)
+    ex = apw.Fp8Experts(gu, torch.ones((2, 2, 1, 1)), dn, torch.ones((2, 1, 1)))
+    x8, xs, wr = torch.zeros((4, 64), dtype=torch.uint8), torch.ones((4, 1)), torch.zeros((2, 64), dtype=torch.float16)
+    ws = torch.empty(1 << 16, dtype=torch.uint8)
+    for bad in (A, None):
+        with pytest.raises(ValueError, match="ws: need a byte tensor"):
+            apw.moe_forward_fp8(c, ex, x, x8, xs, wr, None, 4, 1, True, bad, y, stream=s)
+    with pytest.raises(ValueError, match="w_router: need"):
+        apw.moe_forward_fp8(c, ex, x, x8, xs, wr, None, 4, 1, True, ws, y, stream=s, n_shared=2 ** 32)
+
+
 class _NoStream:
     cuda_stream = 0
 
