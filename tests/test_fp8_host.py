@@ -9,6 +9,7 @@ import torch
 
 import any_precision_weight_amd as apw
 import fp8_ref as ref
+import fp8_tiles as tiles
 
 CTX = 0x1000
 A = 0x10000000  # 16-byte aligned; never dereferenced
@@ -245,3 +246,39 @@ def test_quant_of_zeros_and_short_groups():
     v[0, 129] = -3.5
     q, s = ref.quant(v)
     assert q[0, 129] == -448.0 and s[0, 1] == np.float32(3.5 / 448.0)
+
+
+# ------------------------------------------------------------------ the tile product's cases
+
+def tile_cases():
+    for loads, N, _ in tiles.GEMMS:
+        yield loads, N, False, True
+        yield loads, N, False, False
+    for loads, F, _ in tiles.ACTS:
+        yield loads, 2 * F, True, True
+
+
+def test_tile_cases_cover_every_row_once():
+    for loads, N, act, exact in tile_cases():
+        off = tiles.offsets_of(loads)
+        seen = np.zeros((off[-1], tiles.weight_tiles(N, act)), int)
+        for e, r0, rows, nt, _, _ in tiles.forms(off, N, act, exact):
+            assert off[e] <= r0 and r0 + rows <= off[e + 1]
+            seen[r0:r0 + rows, nt] += 1
+        assert (seen == 1).all()
+
+
+def test_tile_cases_reach_every_form():
+    """Every width of each kernel in whole tiles, of a whole round and of a last one, and
+    in its parts, with more column blocks than the pipeline has buffers (three at most)."""
+    reached = {}
+    for loads, N, act, exact in tile_cases():
+        off = tiles.offsets_of(loads)
+        assert tiles.takes_tiles(len(loads), N, off[-1], 1, act, exact)
+        for _, _, rows, _, parts, whole in tiles.forms(off, N, act, exact):
+            reached.setdefault((act, exact), set()).add((tiles.width(rows, exact), parts, whole))
+    assert {(256, 1, True), (256, 1, False), (128, 1, False), (128, 2, False), (64, 1, True), (64, 1, False),
+            (64, 4, False), (64, 2, False)} <= reached[False, False]
+    for kernel in ((False, True), (True, True)):
+        assert {(128, 1, True), (128, 1, False), (64, 1, True), (64, 1, False), (64, 2, False)} <= reached[kernel]
+    assert all(K > 3 * 128 and K % 128 for _, _, K in tiles.GEMMS + tiles.ACTS)

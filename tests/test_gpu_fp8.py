@@ -23,6 +23,7 @@ import torch
 
 import any_precision_weight_amd as apw
 import fp8_ref as ref
+import fp8_tiles as tiles
 from gpu_util import ctx
 
 pytestmark = pytest.mark.gpu
@@ -770,6 +771,154 @@ def test_norm_then_layer_then_norm():
         mid = (attn.float() + res0)
         assert torch.equal(res, out.float() + mid)
         check_norm(out, mid, gamma, 1e-5, (None, x2, None, None))
+
+
+
+# ------------------------------------------------------------------ the tile product's forms
+
+def tile_operands(r, loads, N, K, halves=1, normal=False):
+    """Rows and weights of experts with the given numbers of rows, in any order of tokens
+    (gathered).  normal: normally distributed values as e4m3 with their scales."""
+    off = np.array(tiles.offsets_of(loads), np.int32)
+    R, E = int(off[-1]), len(loads)
+    perm = r.permutation(R).astype(np.int32)
+    if normal:
+        q, xs = ref.quant(r.normal(size=(R, K)))
+        x8, xs = ref.encode(q), xs.astype(np.float32)
+        w = r.normal(size=(E, N, K)) * 0.02
+        nb, kb = ref.groups(N), ref.groups(K)
+        ws = np.empty((E, 1, nb, kb), np.float32)
+        w8 = np.empty((E, N, K), np.uint8)
+        for i in range(nb):
+            for j in range(kb):
+                b = (slice(None), slice(i * 128, (i + 1) * 128), slice(j * 128, (j + 1) * 128))
+                sc = (np.abs(w[b]).max(axis=(1, 2)) / 448.0).astype(np.float32)
+                ws[:, 0, i, j] = sc
+                w8[b] = ref.encode(ref.e4m3_round(w[b] / sc[:, None, None].astype(np.float64)))
+    else:
+        x8, xs = random_rows(r, R, K)
+        w8, ws = random_weights(r, E, halves, N // halves, K)
+        if halves == 2:
+            xs = (xs / np.sqrt(K)).astype(np.float32)
+    xv = ref.TABLE[x8] * ref.spread(xs.astype(np.float64), K)
+    rows = N // halves
+    wv = [np.concatenate([ref.block_values(w8[e, h * rows:(h + 1) * rows], ws[e, h]) for h in range(halves)])
+          for e in range(E)]
+    return R, E, [cuda(v) for v in (x8, xs, w8, ws, perm, off)], ref.product(xv, wv, perm, off, 1, True)
+
+
+@pytest.mark.parametrize("loads,N,K", tiles.GEMMS)
+def test_gemm_tiles(loads, N, K):
+    """Every width of the tile product in whole tiles and in the parts of a last round, the
+    whole output; the same bits again."""
+    R, E, d, (want, mag) = tile_operands(rng_of("tiles", N, K), loads, N, K)
+    for t in ("f32", "f16", "bf16"):
+        outs = []
+        for _ in range(3):
+            out = torch.full((R + 1, N), 7.0, dtype=TORCH[t], device="cuda")
+            apw.gemm_fp8(ctx(), *d[:4], E, N, K, True, *d[4:], R, 1, out)
+            outs.append(out)
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+        bound = mag * (sum_bound(K) + (0.0 if t == "f32" else 2.0 ** -10))
+        bound = bound + (np.abs(want) + bound) * HALF_STEP[t] + SMALLEST[t]
+        assert np.all(np.abs(np64(outs[0][:R]) - want) <= bound), t
+        assert bool((outs[0][R:] == 7.0).all())
+
+
+@pytest.mark.parametrize("loads,F,K", tiles.ACTS)
+def test_gemm_act_tiles(loads, F, K):
+    R, E, d, (gu, mag) = tile_operands(rng_of("act-tiles", F, K), loads, 2 * F, K, halves=2)
+    outs = []
+    for _ in range(3):
+        a8 = torch.full((R + 1, F), 0x55, dtype=torch.uint8, device="cuda")
+        sc = torch.full((R + 1, ref.groups(F)), -1.0, device="cuda")
+        apw.gemm_act_fp8(ctx(), *d[:4], E, F, K, True, *d[4:], R, 1, a8, sc)
+        outs.append((a8, sc))
+    torch.cuda.synchronize()
+    for a8, sc in outs[1:]:
+        assert torch.equal(a8, outs[0][0]) and torch.equal(sc, outs[0][1])
+    a8, sc = outs[0]
+    check_rows8(*act_bounds(gu, mag, F, K), a8[:R], sc[:R], F)
+    assert (codes(a8[R:]) == 0x55).all() and (np64(sc[R:]) == -1.0).all()
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("loads,N,K", [tiles.GEMMS[0], tiles.GEMMS[2], tiles.GEMMS[3]])
+def test_gemm_16_bit_outputs_in_norm(loads, N, K, t):
+    """What the e4m3 instruction leaves of normally distributed operands' products: an error
+    d of 1.5e-5 of the result in norm.  The output, rounded to a step u, differs from the
+    rounded 64-bit value by u with probability |d| / u, so the difference has the mean square
+    E[u] E|d| (d and the value independent): u <= 2 HALF_STEP |v|, E|v| = 0.8 and E|d| = 0.8 of
+    their norms.  Twice the 1.5e-5 is allowed."""
+    R, E, d, (want, _) = tile_operands(rng_of("in-norm", N, K), loads, N, K, normal=True)
+    out = torch.empty((R, N), dtype=TORCH[t], device="cuda")
+    apw.gemm_fp8(ctx(), *d[:4], E, N, K, True, *d[4:], R, 1, out)
+    rounded = torch.from_numpy(want).to(TORCH[t]).double().numpy()
+    rel = np.linalg.norm(np64(out) - rounded) / np.linalg.norm(want)
+    assert rel <= np.sqrt(2 * HALF_STEP[t] * 0.64 * 3e-5), rel
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("T,N", [(70, 8464), (1100, 8720)])
+def test_gemm_16_bit_nan_stays_in_its_row_and_column(T, N, t):
+    r = rng_of("nan-16", T, t)
+    K = 400
+    x8, xs = random_rows(r, T, K)
+    w8, ws = random_weights(r, 1, 1, N, K)
+    x8[T - 3, 390] = 0x7F
+    w8[0, 140, 3] = 0xFF
+    out = torch.empty((T, N), dtype=TORCH[t], device="cuda")
+    apw.gemm_fp8(ctx(), *(cuda(v) for v in (x8, xs, w8, ws)), 1, N, K, False, None, None, T, 1, out)
+    want = torch.zeros((T, N), dtype=torch.bool, device="cuda")
+    want[T - 3], want[:, 140] = True, True
+    assert torch.equal(out.isnan(), want)
+
+
+def test_layer_tiles():
+    """A layer whose down product runs 256-token tiles to fp32 (their rows leave LDS half by
+    half): against 64 bits, and against its steps with fp32 sums, from which the e4m3
+    instruction's sums differ as test_gemm_16_bit_outputs_in_norm says."""
+    r = rng_of("layer-tiles")
+    T, E, H, F = 1100, 2, 8720, 272
+    d = layer_inputs(r, E, 0, H, F, T)
+    z = d["x"].astype(np.float64) @ d["wr"].astype(np.float64).T
+    chosen = np.argmax(z, axis=1)
+    loads = np.bincount(chosen, minlength=E).tolist()
+    assert any(f[2] > 128 and f[4] == 1 for f in tiles.forms(tiles.offsets_of(loads), H, False, False))
+    got, (ex, args, _, out) = run_layer(d, None, E, 0, H, F, T, 1, True)
+    xv = ref.TABLE[d["x8"]] * ref.spread(d["xs"].astype(np.float64), H)
+    for e in range(E):
+        t = np.nonzero(chosen == e)[0]
+        w1 = np.concatenate([ref.block_values(d["w1"][e, h * F:(h + 1) * F], d["s1"][e, h]) for h in (0, 1)])
+        w2 = ref.block_values(d["w2"][e], d["s2"][e, 0])
+        a, err = act_bounds(xv[t] @ w1.T, np.abs(xv[t]) @ np.abs(w1).T, F, H)
+        q, s = ref.quant(a)
+        sv = ref.spread(s, F)
+        step = 2 * np.maximum(np.exp2(np.floor(np.log2(np.maximum(np.abs(a / sv), 2.0 ** -6)))) * 2.0 ** -4, 2.0 ** -10)
+        flips = np.abs(a / sv - q) >= step / 2 - err / sv - np.abs(a / sv) * 2.0 ** -21
+        top = np.stack([err[:, g * 128:(g + 1) * 128].max(axis=1) for g in range(ref.groups(F))], axis=1)
+        slack = np.where(flips, step, 0.0) * sv + np.abs(q * sv) * 2.0 ** -21 + ref.spread(top, F)
+        want = (q * sv) @ w2.T
+        bound = (np.abs(q * sv) @ np.abs(w2).T) * (sum_bound(F) + 2.0 ** -22 + 2.0 ** -10) + slack @ np.abs(w2).T
+        bound += (np.abs(want) + bound) * 2.0 ** -11 + 2.0 ** -25
+        assert np.all(np.abs(got[t] - want) <= bound)
+    x, x8, xs, wr, _ = args
+    w1, s1, w2, s2 = ex.tensors
+    ids, perm, inv = (torch.empty(T, dtype=torch.int32, device="cuda") for _ in range(3))
+    w, y = torch.empty((T, 1), device="cuda"), torch.empty((T, H), device="cuda")
+    counts, off = (torch.empty(n, dtype=torch.int32, device="cuda") for n in (E, E + 1))
+    a8, sc = torch.empty((T, F), dtype=torch.uint8, device="cuda"), torch.empty((T, ref.groups(F)), device="cuda")
+    steps = torch.empty((T, H), dtype=torch.float16, device="cuda")
+    apw.route(ctx(), x, wr, None, T, H, E, 1, True, ids, w, counts, off, perm, inv)
+    apw.gemm_act_fp8(ctx(), x8, xs, w1, s1, E, F, H, True, perm, off, T, 1, a8, sc)
+    apw.gemm_fp8(ctx(), a8, sc, w2, s2, E, H, F, False, perm, off, T, 1, y)
+    apw.combine(ctx(), y, apw.F32, w, inv, T, 1, H, steps)
+    diff = (out[:T].double() - steps.double()).norm() / steps.double().norm()
+    # the codes here are uniform, not normal.  A group of 8 products loses at most 8 * 2^-13 of its
+    # largest, a group's largest is no more than its root of squares, and the groups' signs are
+    # independent: 2^-10 in norm; the two roundings to fp16 differ by at most 2 * 2^-11
+    assert float(diff) <= 2.0 ** -9, float(diff)
 
 
 # ------------------------------------------------------------------ offsets past 32 bits

@@ -22,6 +22,7 @@ import pytest
 import torch
 
 import any_precision_weight_amd as apw
+import fp8_tiles as tiles
 import synth
 import synth.gpu
 from any_precision_weight_amd.resident import ResidentWeights
@@ -82,3 +83,76 @@ def test_safe_wait_build_gives_identical_bits(name):
     print(f"{name}: counts {a['counts'].tolist()}: identical", flush=True)
     tbl_safe.close()
     rw.close()
+
+
+def _fp8_weights(g, E, halves, rows, K):
+    c = torch.randint(0, 127, (E, halves * rows, K), dtype=torch.uint8, device="cuda", generator=g)
+    s = torch.rand((E, halves, -(-rows // 128), -(-K // 128)), device="cuda", generator=g)
+    return c, s * 2.0 ** -14
+
+
+def _both(call):
+    """The outputs of a call by each build, as bytes."""
+    outs = []
+    for c in (ctx(), safe_ctx()):
+        o = call(c)
+        torch.cuda.synchronize()
+        outs.append([t.view(torch.uint8) for t in o])
+    return zip(*outs)
+
+
+@pytest.mark.parametrize("case", range(len(tiles.GEMMS)))
+def test_safe_wait_build_gives_identical_bits_in_the_8_bit_product(case):
+    loads, N, K = tiles.GEMMS[case]
+    g = torch.Generator(device="cuda").manual_seed(case)
+    E, off = len(loads), torch.tensor(tiles.offsets_of(loads), dtype=torch.int32, device="cuda")
+    R = sum(loads)
+    x8 = _fp8_weights(g, 1, 1, R, K)[0][0]
+    xs = torch.rand((R, -(-K // 128)), device="cuda", generator=g)
+    w8, ws = _fp8_weights(g, E, 1, N, K)
+    for dt in (torch.float32, torch.float16, torch.bfloat16):
+        def call(c):
+            out = torch.full((R, N), -1.0, dtype=dt, device="cuda")
+            apw.gemm_fp8(c, x8, xs, w8, ws, E, N, K, False, None, off, R, 1, out)
+            return [out]
+        assert all(torch.equal(a, b) for a, b in _both(call)), dt
+
+
+@pytest.mark.parametrize("case", range(len(tiles.ACTS)))
+def test_safe_wait_build_gives_identical_bits_in_the_8_bit_gate_up(case):
+    loads, F, K = tiles.ACTS[case]
+    g = torch.Generator(device="cuda").manual_seed(case)
+    E, off = len(loads), torch.tensor(tiles.offsets_of(loads), dtype=torch.int32, device="cuda")
+    R = sum(loads)
+    x8 = _fp8_weights(g, 1, 1, R, K)[0][0]
+    xs = torch.rand((R, -(-K // 128)), device="cuda", generator=g)
+    w8, ws = _fp8_weights(g, E, 2, F, K)
+
+    def call(c):
+        a8 = torch.full((R, F), 0x55, dtype=torch.uint8, device="cuda")
+        sc = torch.full((R, -(-F // 128)), -1.0, device="cuda")
+        apw.gemm_act_fp8(c, x8, xs, w8, ws, E, F, K, False, None, off, R, 1, a8, sc)
+        return [a8, sc]
+    assert all(torch.equal(a, b) for a, b in _both(call))
+
+
+@pytest.mark.parametrize("T,E,topk,H,F", [(1, 8, 2, 1040, 400), (16, 8, 2, 1040, 4112), (40, 8, 2, 1040, 4112),
+                                          (1100, 2, 1, 8720, 272)])
+def test_safe_wait_build_gives_identical_bits_in_the_8_bit_layer(T, E, topk, H, F):
+    g = torch.Generator(device="cuda").manual_seed(T)
+    ex = apw.Fp8Experts(*_fp8_weights(g, E, 2, F, H), *_fp8_weights(g, E, 1, H, F))
+    x = torch.randn((T, H), device="cuda", generator=g).half()
+    wr = (torch.randn((E, H), device="cuda", generator=g) * 0.05).half()
+    gamma = torch.ones(H, dtype=torch.float16, device="cuda")
+
+    def call(c):
+        x8 = torch.empty((T, H), dtype=torch.uint8, device="cuda")
+        xs = torch.empty((T, -(-H // 128)), device="cuda")
+        y, out = torch.empty_like(x), torch.full((T, H), -1.0, dtype=torch.float16, device="cuda")
+        ws = torch.full((apw.moe_workspace_fp8(c, ex, T, topk),), 0xA5, dtype=torch.uint8, device="cuda")
+        apw.norm(c, x, None, None, gamma, 1e-5, T, H, y, x8, xs)
+        apw.moe_forward_fp8(c, ex, y, x8, xs, wr, None, T, topk, True, ws, out)
+        return [x8, xs, y, out]
+    pairs = list(_both(call))
+    assert all(torch.equal(a, b) for a, b in pairs)
+    assert bool(pairs[3][0].view(torch.float16).isfinite().all())
