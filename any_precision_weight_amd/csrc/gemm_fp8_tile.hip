@@ -17,11 +17,18 @@
 //
 // Two kernels (block_product has the reason): e4m3 MFMAs for 16-bit outputs (tile_fast),
 // fp16 MFMAs on converted operands for sums that stay in fp32 or are quantised again
-// (tile_exact).  What bounds them is how many instructions a SIMD takes: a vector
-// instruction holds it for about 4 clocks and an MFMA for 8, so beside a 32-clock MFMA
-// there is room for 6 others.  Measured: 4096 x 6144 x 4096 to fp16 107 us, 1.93 PFLOP/s;
-// through fp16 products 8 experts of 4096 x 14336 with 4096 rows, unevenly, 518 us, 0.93, and
-// gate_up of the same layer's 8192 rows 1.8 ms, 1.07.
+// (tile_exact).  A vector instruction holds a SIMD for about 4 clocks and an MFMA for 8, so
+// beside a 32-clock MFMA there is room for 6 others (they have 6.5 and 7.1).  Measured: 4096
+// x 6144 x 4096 to fp16 107 to 115 us, 1.8 to 1.9 PFLOP/s; through fp16 products 8 experts of
+// 4096 x 14336 with 4096 rows, unevenly, 518 to 526 us, 0.92, and gate_up of the same layer's
+// 8192 rows 1.8 ms, 1.07.
+//
+// What bounds them is that a CU holds one workgroup, two waves a SIMD, which do not cover
+// each other's waits: the matrix units are busy for 37, 50 and 56 % of the SIMDs' cycles in
+// these three, a wave stands at a wait or the barrier for 40, 32 and 32 % of its time, and for
+// 30, 29 and 28 % it has an instruction ready while the SIMD takes the other wave's.  The
+// copies alone are not it: without any the first takes 92 us of 108 and the second 428 of
+// 526, with copies that always find their lines in the L2 104 and 462.
 #include <algorithm>
 
 #include "gemm_fp8.h"

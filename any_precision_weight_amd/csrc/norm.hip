@@ -92,7 +92,7 @@ constexpr uint32_t kNormGrid = 1u << 20;  // workgroups in x; a dimension has fe
 // of max(TPR, 256) threads holds max(1, 256 / TPR) rows.  The row stays in registers
 // between the sum and the output, so x and the residual are read once.  The sum of
 // squares and y are fp64: squares of fp32 / bf16 values leave fp32's range, and a value
-// next to a border of e4m3 then rounds as the formula says.  fp64 runs at the rate of
+// next to a border of e4m3 then rounds as its quotient in fp32 does.  fp64 runs at the rate of
 // unpacked fp32 here and the kernel is bound by memory.
 template <int XT, int RT, int TPR, int VPT>
 __global__ void __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) norm_kernel(const NormParams P)

@@ -459,8 +459,8 @@ apmoe_status apmoe_moe_forward_noalloc(apmoe_ctx *ctx, const apmoe_table *tbl, i
  *   is then looked at); y [T][H] of x_dtype (may be x) or NULL; y8 e4m3 [T][H] and
  *   y_scale fp32 [T][ceil(H/128)], both NULL or both set.  At least one of y, y8.
  * The norm is that of the stored h.  The mean and y are computed in fp64 (squares of
- * large values stay finite, and y8 rounds as the formula says).  A row with a NaN
- * gives NaN.  Types: APMOE_F16, APMOE_BF16, APMOE_F32, any mixture.
+ * large values stay finite); y8 is rounded from y / s in fp32.  A row with a NaN gives
+ * NaN.  Types: APMOE_F16, APMOE_BF16, APMOE_F32, any mixture.
  * Limits: H % 8 == 0, 8 <= H <= 65536, T >= 0, eps >= 0 and finite.  Buffers other
  * than the two pairs named must not overlap.  Errors (nothing enqueued): INVALID_ARG
  * for NULL or misaligned pointers (16 bytes; y_scale 4) or bad sizes, UNSUPPORTED for
@@ -540,7 +540,8 @@ apmoe_status apmoe_moe_workspace_fp8(apmoe_ctx *ctx, const apmoe_fp8_experts *ex
  * (summed in another order than apmoe_route's), the selection inside the gate_up launch,
  * then down with the sum over the experts, in the order of the experts, in its
  * accumulators; with a context made under APMOE_UNFUSED=1 they take the steps' own launches
- * too.  A token's last bits may so depend on the batch that it is in.  x fp16 [T][H] is what
+ * too.  A token's last bits may so depend on the batch that it is in; a caller who wants
+ * fp32 sums in down whatever the batch makes the steps' calls.  x fp16 [T][H] is what
  * the router reads, x8 and x_scale the same rows in 8 bits (apmoe_norm gives both); out
  * fp16 [T][H].
  * The first E - n_shared experts are the routed ones (w_router rows, bias as in
