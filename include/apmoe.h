@@ -457,7 +457,7 @@ apmoe_status apmoe_moe_forward_noalloc(apmoe_ctx *ctx, const apmoe_table *tbl, i
  *   x [T][H] of x_dtype; gamma [H] of x_dtype; residual and residual_out [T][H] of
  *   res_dtype, both NULL or both set (the same buffer updates it in place; res_dtype
  *   is then looked at); y [T][H] of x_dtype (may be x) or NULL; y8 e4m3 [T][H] and
- *   y_scale fp32 [T][ceil(H/128)], both NULL or both set.  At least one of y, y8.
+ *   y_scale fp32 [T][ceil(H/128)], both NULL or both set.  At least one of y, y8 (T > 0).
  * The norm is that of the stored h.  The mean and y are computed in fp64 (squares of
  * large values stay finite); y8 is rounded from y / s in fp32.  A row with a NaN gives
  * NaN.  Types: APMOE_F16, APMOE_BF16, APMOE_F32, any mixture.

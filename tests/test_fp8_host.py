@@ -204,6 +204,24 @@ def test_binding_refuses_what_has_no_type_or_size():
         apw.moe_forward_fp8(c, ex, x, x8, xs, wr, None, 4, 1, True, ws, y, stream=s, n_shared=2 ** 32)
 
 
+def test_binding_with_no_rows():
+    """Empty batches, whose tensors have no address, are calls that do nothing."""
+    c, s = HostCtx(), _NoStream()
+    e = lambda dt, *shape: torch.empty(shape, dtype=dt)
+    f16, u8, f32, i32 = torch.float16, torch.uint8, torch.float32, torch.int32
+    x, gamma = e(f16, 0, 64), torch.ones(64, dtype=f16)
+    apw.norm(c, x, None, None, gamma, 1e-5, 0, 64, e(f16, 0, 64), stream=s)
+    apw.norm(c, x, e(f32, 0, 64), e(f32, 0, 64), gamma, 1e-5, 0, 64, None, e(u8, 0, 64), e(f32, 0, 1), stream=s)
+    x8, xs, perm, off = e(u8, 0, 64), e(f32, 0, 1), e(i32, 0), torch.zeros(3, dtype=i32)
+    gu, dn = torch.zeros((2, 64, 64), dtype=u8), torch.zeros((2, 64, 32), dtype=u8)
+    s1, s2 = torch.ones((2, 2, 1, 1)), torch.ones((2, 1, 1))
+    apw.gemm_fp8(c, x8, xs, gu, s1, 2, 64, 64, True, perm, off, 0, 1, e(f16, 0, 64), stream=s)
+    apw.gemm_act_fp8(c, x8, xs, gu, s1, 2, 32, 64, True, perm, off, 0, 1, e(u8, 0, 32), e(f32, 0, 1), stream=s)
+    ex = apw.Fp8Experts(gu, s1, dn, s2)
+    ws = e(u8, apw.moe_workspace_fp8(c, ex, 0, 1))
+    apw.moe_forward_fp8(c, ex, x, x8, xs, torch.zeros((2, 64), dtype=f16), None, 0, 1, True, ws, e(f16, 0, 64), stream=s)
+
+
 class _NoStream:
     cuda_stream = 0
 
