@@ -987,6 +987,53 @@ def test_gemm_weights_past_32_bits(T):
         check_part(x8[rows], xs[rows], w8[e, N - 16:], ws[e, -1], out[rows, N - 16:], K)
 
 
+def most_columns(seed, T, rows, halves=1):
+    """Operands with nearly the most columns (the last block short), the rows of x zero but
+    for 12 blocks over the whole length, which alone count: (operands, values of x and of w
+    in those columns)."""
+    K = (1 << 24) - 144
+    KB = ref.groups(K)
+    blocks = sorted({0, 1, 2, KB - 2, KB - 1} | {(i * KB) // 8 + i for i in range(1, 8)})
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x8 = torch.zeros((T, K), dtype=torch.uint8, device="cuda")
+    cols = torch.cat([torch.arange(b * 128, min(K, b * 128 + 128), device="cuda") for b in blocks])
+    x8[:, cols] = codes_on_gpu(seed, T, cols.numel())
+    w8 = torch.empty((1, rows, K), dtype=torch.uint8, device="cuda")
+    for r in range(rows):
+        w8[0, r] = codes_on_gpu(seed + 1 + r, K)
+    xs = torch.rand((T, KB), device="cuda", generator=g) * 2.0 ** -9
+    ws = torch.rand((halves, ref.groups(rows // halves), KB), device="cuda", generator=g) * 2.0 ** -9
+    b = cols // 128
+    x = ref.TABLE[codes(x8[:, cols])] * np64(xs[:, b])
+    row = torch.arange(rows, device="cuda")
+    w = ref.TABLE[codes(w8[0][:, cols])] * np64(ws[row // (rows // halves), (row % (rows // halves)) // 128][:, b])
+    return K, (x8, xs, w8, ws), x, w, (128 + 2 * len(blocks) + 11) * 2.0 ** -23
+
+
+@pytest.mark.parametrize("T,N,t", [(3, 40, "f32"), (40, 40, "f16"), (1100, 256, "f16"), (1100, 256, "f32")])
+def test_gemm_of_the_most_columns(T, N, t):
+    K, d, x, w, bound = most_columns(7, T, N)
+    out = torch.empty((T, N), dtype=TORCH[t], device="cuda")
+    apw.gemm_fp8(ctx(), *d, 1, N, K, False, None, None, T, 1, out)
+    want, mag = x @ w.T, np.abs(x) @ np.abs(w).T
+    bound = mag * (bound + (2.0 ** -10 if t == "f16" and T > 32 else 0.0))
+    assert np.all(np.abs(np64(out) - want) <= bound + (np.abs(want) + bound) * HALF_STEP[t] + SMALLEST[t])
+
+
+@pytest.mark.parametrize("T", [3, 20, 40])
+def test_gemm_act_of_the_most_columns(T):
+    F = 16
+    K, d, x, w, bound = most_columns(9, T, 2 * F, halves=2)
+    a8 = torch.empty((T, F), dtype=torch.uint8, device="cuda")
+    sc = torch.empty((T, 1), device="cuda")
+    apw.gemm_act_fp8(ctx(), *d, 1, F, K, False, None, None, T, 1, a8, sc)
+    gu, mag = x @ w.T, np.abs(x) @ np.abs(w).T
+    g, u, s = gu[:, :F], gu[:, F:], ref.silu(gu[:, :F])
+    dg, du = mag[:, :F] * bound, mag[:, F:] * bound
+    err = 1.1 * dg * (np.abs(u) + du) + np.abs(s) * du + np.abs(s * u) * 2.0 ** -20 + 2.0 ** -100 * np.abs(u)
+    check_rows8(s * u, err, a8, sc, F)
+
+
 def test_norm_rows_past_32_bits():
     T, H = 70016, 65536
     x = torch.empty((T, H), dtype=torch.float16, device="cuda").normal_()
