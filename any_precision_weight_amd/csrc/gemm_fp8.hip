@@ -216,25 +216,26 @@ __global__ void __launch_bounds__(kStreamWaves / NP *kWave, NP == 2 ? 3 : TT == 
 //
 // The product.  Few tiles leave most of the device idle, and the stream product, split over
 // K and over chunks of 32 rows, fills it although each chunk reads the weights again.  Up to
-// 64 chunks of 256 weight rows (32 with a 16-bit out, whose tiles are faster) it is ahead: to
-// fp32, 256 rows of 2048 x 2048 (64 chunks) 20 us as tiles and 17 as chunks, 64 of 6144 x 4096
-// (48) 33 and 26, 512 of 2048 x 2048 (128) 21 and 26, 128 of 6144 x 4096 (96) 34 and 44; to
-// fp16, 128 rows of 2048 x 2048 (32) 14.5 and 12.3, 192 (48) 14.5 and 17.  With more and above
-// 32 tokens tiles: 8 experts of 4096 x 7168, 128 tokens of 2, 61 us against 127.  Experts with
-// a few rows each stream a little faster if the routing is even (60 of 2048 x 1408, 64 tokens
-// of 4, 35 us against 40), and much slower if it is not, when few experts' waves are left
-// (the same with most of the experts idle 40 against 16; 64 of 1024 x 2048, 64 tokens of 2,
-// 44 against 20).
+// 64 chunks of 256 weight rows it is ahead (weights from HBM, to bf16 as chunks and as tiles,
+// us; to fp32 the tiles are up to 5 slower): 64 rows of 6144 x 4096 (48 chunks) 26 and 38, 128
+// of 4096 x 14336 (64) 70 and 116, 512 of 1024 x 8192 (64) 44 and 58, 64 tokens of 2 of 8
+// experts of 1024 x 2048 (44) 10 and 17; 256 rows of 2048 x 2048 (64) 17 and 15.3, to fp32 17
+// and 20.  With more and above 32 tokens tiles: 128 rows of 6144 x 4096 (96 chunks) 43 and 37,
+// 192 of 4096 x 14336 (96) 131 and 113, 8 experts of 4096 x 7168, 128 tokens of 2, 127 and 61.
+// Experts with a few rows each stream a little faster if the routing is even (60 of 2048 x
+// 1408, 64 tokens of 4, 35 us against 40), and much slower if it is not, when few experts'
+// waves are left (the same with most of the experts idle 40 against 16; 64 of 1024 x 2048, 64
+// tokens of 2, 44 against 20).
 //
 // gate_up, whose stream product is not split over K.  More than 32 rows take tiles (E = 1,
 // 48 rows of 2 x 2048 x 4096: 77 us streamed, 33 as tiles), and more than 16 where every CU
 // has one at most (24 rows of that one expert 69 and 31; 8 experts of 2 x 2048 x 7168, 32
 // tokens of 2, 128 tiles, 82 and 56; of 2 x 4096 x 4096, 256 tiles, 53 and 67).
-bool takes_tiles(const Fp8Params &P, int most, bool act, bool exact)
+bool takes_tiles(const Fp8Params &P, int most, bool act)
 {
     if (act)
-        return most > kStreamMax || (most > 16 && fp8_tiles(P, act, fp8_tile_tokens(exact)) < kCus);
-    return most > kStreamMax && fp8_tiles(P, act, kStreamMax) > (exact ? 64 : 32);
+        return most > kStreamMax || (most > 16 && fp8_tiles(P, act, fp8_tile_tokens(true)) < kCus);
+    return most > kStreamMax && fp8_tiles(P, act, kStreamMax) > 64;
 }
 
 }  // namespace
@@ -245,7 +246,7 @@ hipError_t launch_gemm_fp8(const uint8_t *x8, const float *xs, const uint8_t *w8
 {
     const Fp8Params P{x8, xs, w8, ws, perm, offsets, out, nullptr, E, N, K, topk, gather, out_dtype, R, 0};
     const int most = most_rows(P);
-    if (takes_tiles(P, most, false, exact))
+    if (takes_tiles(P, most, false))
         return launch_fp8_tile(P, false, exact, s);
     const unsigned chunks = (unsigned)(most + kStreamMax - 1) / kStreamMax;
     // KS: enough waves to fill the device, 8 on a CU (KS = 1, 2, 4, 8: 6144 x 4096, 192 waves,
@@ -282,7 +283,7 @@ hipError_t launch_gemm_act_fp8(const uint8_t *x8, const float *xs, const uint8_t
     const Fp8Params P{x8, xs, w8, ws, perm, offsets, a8, as, E, 2 * F, K, topk, gather, 0, R, F};
     const dim3 grid((F + kBlk - 1) / kBlk, E);
     const int most = most_rows(P);
-    if (takes_tiles(P, most, true, true))
+    if (takes_tiles(P, most, true))
         return launch_fp8_tile(P, true, true, s);
     // Up to 16 rows four waves with two pairs of tiles each, three workgroups on a CU (16 tokens,
     // 8 experts of 2 x 14336 x 4096: 172 us, eight waves with one pair 176); more rows have no

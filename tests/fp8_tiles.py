@@ -16,7 +16,7 @@ def weight_tiles(N: int, act: bool) -> int:
     return cdiv(N // 2, 128) if act else cdiv(N, 256)
 
 
-def takes_tiles(E: int, N: int, T: int, topk: int, act: bool, exact: bool) -> bool:
+def takes_tiles(E: int, N: int, T: int, topk: int, act: bool) -> bool:
     R = T * topk
     most, served = (R if E == 1 else T), min(E, R)
 
@@ -24,7 +24,7 @@ def takes_tiles(E: int, N: int, T: int, topk: int, act: bool, exact: bool) -> bo
         return ((R - served) // tok + served) * weight_tiles(N, act)
     if act:
         return most > 32 or (most > 16 and tiles(128) < 256)
-    return most > 32 and tiles(32) > (64 if exact else 32)
+    return most > 32 and tiles(32) > 64
 
 
 def forms(offsets, N: int, act: bool, exact: bool):

@@ -292,7 +292,7 @@ def test_tile_cases_reach_every_form():
     reached = {}
     for loads, N, act, exact in tile_cases():
         off = tiles.offsets_of(loads)
-        assert tiles.takes_tiles(len(loads), N, off[-1], 1, act, exact)
+        assert tiles.takes_tiles(len(loads), N, off[-1], 1, act)
         for _, _, rows, _, parts, whole in tiles.forms(off, N, act, exact):
             reached.setdefault((act, exact), set()).add((tiles.width(rows, exact), parts, whole))
     assert {(256, 1, True), (256, 1, False), (128, 1, False), (128, 2, False), (64, 1, True), (64, 1, False),
