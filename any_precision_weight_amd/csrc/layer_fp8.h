@@ -60,6 +60,9 @@ inline bool few_quantises_late(int T, int topk, int kt, int Er, int F)
 //   768 x 2048 (8 a token) 27 and 64; 4 tokens of the first 183 and 197, of the second 53 and
 //   109; 16 of the second 108 and 119.
 // They lose to them where
+//   - a selection is long: up to 393216 comparisons (256 experts of 768 x 2048, 2 a token: 4
+//     tokens 68 and 93, 6, 393216, 88 and 96, 8 108 and 99; 160 of 1536 x 5120, 1 a token, 12
+//     tokens 137 and 246);
 //   - the selections add up: up to 192 million comparisons in all workgroups (128 experts of
 //     768 x 2048, 8 a token: 14 tokens 124 and 129, 16 tokens, 201 million, 151 and 132; 160
 //     experts of 1536 x 5120, 6 a token, 10 tokens, 184 million, 310 and 331);
@@ -70,7 +73,7 @@ inline bool few_quantises_late(int T, int topk, int kt, int Er, int F)
 inline bool few_layer_fits(int T, int topk, int kt, int Er, int H, int F)
 {
     const long slots = few_slots(T, topk, kt, Er), compares = few_compares(T, Er);
-    return T <= kFewTokens && (long)T * kt * 4 * ((F + 127) / 128) <= kFewRows8 && compares <= 256 * 1024 &&
+    return T <= kFewTokens && (long)T * kt * 4 * ((F + 127) / 128) <= kFewRows8 && compares <= 384 * 1024 &&
            slots * ((F + 127) / 128) * compares <= 192 * 1000 * 1000 && (T < 12 || slots * H * F < 1l << 28);
 }
 

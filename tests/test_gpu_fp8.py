@@ -470,6 +470,16 @@ def test_layer(T, E, topk, shared, H, F, renorm, has_bias):
     assert np.all(err <= bound), float((err / bound).max())
 
 
+@pytest.mark.parametrize("T,E,topk,H,F", [(5, 256, 8, 128, 272), (6, 256, 1, 64, 48), (15, 160, 2, 80, 144)])
+def test_layer_long_selections(T, E, topk, H, F):
+    """Near the most comparisons that the few-token launches take (T * E^2 of 384000)."""
+    r = rng_of("long", T, E)
+    d = layer_inputs(r, E, 0, H, F, T)
+    want, bound = layer_ref(d, None, E, 0, H, F, T, topk, True)
+    got, _ = run_layer(d, None, E, 0, H, F, T, topk, True)
+    assert np.all(np.abs(got - want) <= bound)
+
+
 @pytest.mark.parametrize("T", [5, 300])
 def test_route_with_a_nan_token(T):
     """A token whose logits are all NaN still gets distinct experts (the lowest ones), so
