@@ -20,7 +20,7 @@ SAFE_LIB_PATH = os.path.join(_HERE, "libapmoe_safe.so")
 
 OK, INVALID_ARG, UNSUPPORTED, NOT_RESIDENT, HIP_ERROR, OUT_OF_MEMORY = range(6)
 GATE_UP, DOWN = 0, 1
-F16, F32, BF16 = 0, 1, 2
+F16, F32, BF16, E4M3 = 0, 1, 2, 3
 MIN_BITS, MAX_BITS, PLANES = 3, 8, 8
 
 EXPORTED = [
@@ -31,7 +31,7 @@ EXPORTED = [
     "apmoe_gemm_act", "apmoe_act",
     "apmoe_combine", "apmoe_moe_workspace", "apmoe_moe_forward", "apmoe_page_out", "apmoe_page_in",
     "apmoe_moe_forward_noalloc", "apmoe_norm", "apmoe_gemm_fp8", "apmoe_gemm_act_fp8", "apmoe_moe_workspace_fp8",
-    "apmoe_moe_forward_fp8",
+    "apmoe_moe_forward_fp8", "apmoe_kv_append", "apmoe_attn_workspace", "apmoe_attn_decode", "apmoe_attn_prefill",
 ]
 
 
@@ -55,6 +55,21 @@ class Fp8Desc(ctypes.Structure):
         ("E", ctypes.c_int32), ("H", ctypes.c_int32), ("F", ctypes.c_int32),
         ("gate_up", ctypes.c_void_p), ("gate_up_scale", ctypes.c_void_p),
         ("down", ctypes.c_void_p), ("down_scale", ctypes.c_void_p),
+    ]
+
+
+class KvCacheDesc(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("page", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+    ]
+
+
+class KvBatchDesc(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("max_len", ctypes.c_int32),
+        ("pages", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("q_offsets", ctypes.c_void_p),
     ]
 
 
@@ -131,6 +146,14 @@ def _declare(L):
         "apmoe_gemm_act_fp8": (S, [P, P, P, P, P, I32, I32, I32, I32, P, P, I32, I32, P, P, P]),
         "apmoe_moe_workspace_fp8": (S, [P, ctypes.POINTER(Fp8Desc), I32, I32, I32, ctypes.POINTER(SZ)]),
         "apmoe_moe_forward_fp8": (S, [P, ctypes.POINTER(Fp8Desc), P, P, P, P, P, I32, I32, I32, I32, P, SZ, P, P]),
+        "apmoe_kv_append": (S, [P, ctypes.POINTER(KvCacheDesc), ctypes.POINTER(KvBatchDesc), P, I64, P, I64, P, I64, I32,
+                                I32, P, I32, I32, I32, P, P]),
+        "apmoe_attn_workspace": (S, [P, ctypes.POINTER(KvCacheDesc), ctypes.POINTER(KvBatchDesc), I32,
+                                     ctypes.POINTER(SZ)]),
+        "apmoe_attn_decode": (S, [P, ctypes.POINTER(KvCacheDesc), ctypes.POINTER(KvBatchDesc), P, I64, I32, I32, F32_,
+                                  I32, I32, P, SZ, P, P, P, P]),
+        "apmoe_attn_prefill": (S, [P, ctypes.POINTER(KvCacheDesc), ctypes.POINTER(KvBatchDesc), P, I64, I32, I32, F32_,
+                                   I32, I32, P, SZ, P, P, P, P]),
         "apmoe_page_out": (S, [P, P, I32, I32, I32, I32, ctypes.POINTER(P), P, P, P]),
         "apmoe_page_in": (S, [P, P, I32, I32, I32, I32, ctypes.POINTER(P), ctypes.POINTER(P), P, P, P]),
     }
@@ -506,6 +529,136 @@ def moe_forward_fp8(ctx: Context, experts: Fp8Experts, x, x8, x_scale, w_router,
                                        _arg(ctx, ws, "ws", 0, (torch.uint8,)), ws.numel(),
                                        _arg(ctx, out, "out", T * H, f16), _stream_of(ctx, stream)),
            "apmoe_moe_forward_fp8", ctx.L)
+
+
+# --------------------------------------------------------------------------- paged key-value cache
+
+class KvCache:
+    """A pool of pages of the key-value cache: k and v of n_pages * kv_heads * page *
+    head_dim elements (any shape that begins with n_pages), float16, bfloat16, or e4m3
+    (float8_e4m3fn or uint8) with float32 scales of n_pages * kv_heads * page elements.
+    Holds the tensors, so they live as long as it does."""
+
+    def __init__(self, k, v, page: int, kv_heads: int, head_dim: int, k_scale=None, v_scale=None):
+        _load_types()
+        e4m3 = k.dtype in _e4m3_types
+        if not e4m3 and _float_ids.get(k.dtype) not in (F16, BF16):
+            raise ValueError(f"k: need float16, bfloat16 or e4m3, got {k.dtype}")
+        if e4m3 and (k_scale is None or v_scale is None):
+            raise ValueError("an e4m3 cache needs k_scale and v_scale")
+        self.n_pages, self.page, self.kv_heads, self.head_dim = k.shape[0], page, kv_heads, head_dim
+        self.device = k.get_device()
+        self.tensors = (k, v, k_scale, v_scale)
+        rows = self.n_pages * kv_heads * page
+        types = _e4m3_types if e4m3 else (k.dtype,)
+        d = KvCacheDesc()
+        d.dtype = E4M3 if e4m3 else _float_ids[k.dtype]
+        d.n_pages, d.page, d.kv_heads, d.head_dim = self.n_pages, page, kv_heads, head_dim
+        d.k = _arg(self, k, "k", rows * head_dim, types)
+        d.v = _arg(self, v, "v", rows * head_dim, types)
+        if e4m3:
+            d.k_scale = _arg(self, k_scale, "k_scale", rows, _f32)
+            d.v_scale = _arg(self, v_scale, "v_scale", rows, _f32)
+        self.desc = d
+        self.ref = ctypes.byref(d)
+
+
+class KvBatch:
+    """The sequences of a call: pages int32 [B][max_pages], lens int32 [B] (this call's
+    tokens included), T rows, q_offsets int32 [B + 1] (None: one row a sequence), max_len
+    a bound of the lengths (0: what the pages hold).  Holds the tensors."""
+
+    def __init__(self, pages, lens, T: int, q_offsets=None, max_len: int = 0):
+        _load_types()
+        if pages.dim() != 2 or pages.shape[0] != lens.numel():
+            raise ValueError(f"pages {tuple(pages.shape)} and lens {tuple(lens.shape)} are not [B][max_pages], [B]")
+        self.B, self.T = pages.shape[0], T
+        self.device = pages.get_device()
+        self.tensors = (pages, lens, q_offsets)
+        d = KvBatchDesc()
+        d.B, d.T, d.max_pages, d.max_len = self.B, T, pages.shape[1], max_len
+        d.pages = _arg(self, pages, "pages", pages.numel(), _i32)
+        d.lens = _arg(self, lens, "lens", self.B, _i32)
+        d.q_offsets = _arg(self, q_offsets, "q_offsets", self.B + 1, _i32)
+        self.desc = d
+        self.ref = ctypes.byref(d)
+
+
+def _kv_on(ctx: Context, cache: KvCache, batch: KvBatch) -> None:
+    for name, o in (("cache", cache), ("batch", batch)):
+        if o.device != ctx.device:
+            raise ValueError(f"the {name} is on cuda:{o.device}, the context on cuda:{ctx.device}")
+
+
+def _matrix(ctx: Context, t, name: str, T: int, width: int, types):
+    """(pointer, stride) of a 2-dimensional tensor of at least T rows and `width` dense
+    columns; rows may be apart."""
+    if t.dtype not in types or t.dim() != 2 or t.shape[0] < T or t.shape[1] != width or \
+            (width > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: need [{T}][{width}] of {' / '.join(map(str, types))} with dense rows, got "
+                         f"{tuple(t.shape)} of {t.dtype}, strides {tuple(t.stride())}")
+    if t.get_device() != ctx.device:
+        raise ValueError(f"{name} is on {t.device}, the context on cuda:{ctx.device}")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), width)
+
+
+def kv_append(ctx: Context, cache: KvCache, batch: KvBatch, q, k, v, q_heads: int, rope, rot: int, interleaved: bool,
+              q_out, stream=None) -> None:
+    """Position rotation of the new rows' queries and keys (rope float32 [n_pos][rot]: a
+    position's cosines, then its sines; None with rot 0), keys and values into the cache.
+    q [T][q_heads * D], k, v [T][kv_heads * D], rows may be apart; q_out [T][q_heads * D].
+    q and q_out None with q_heads 0."""
+    _kv_on(ctx, cache, batch)
+    T, D, kw = batch.T, cache.head_dim, cache.kv_heads * cache.head_dim
+    dt, types = _types(k, "k")
+    qp = (None, 0) if q is None else _matrix(ctx, q, "q", T, q_heads * D, types)
+    kp, vp = _matrix(ctx, k, "k", T, kw, types), _matrix(ctx, v, "v", T, kw, types)
+    n_pos = 0
+    if rope is not None:
+        if rope.dim() != 2 or rope.shape[1] != rot:
+            raise ValueError(f"rope: need [positions][{rot}], got {tuple(rope.shape)}")
+        n_pos = rope.shape[0]
+    _check(ctx.L.apmoe_kv_append(ctx.handle, cache.ref, batch.ref, *qp, *kp, *vp, dt, q_heads,
+                                 _arg(ctx, rope, "rope", n_pos * rot, _f32), n_pos, rot, int(interleaved),
+                                 _arg(ctx, q_out, "q_out", T * q_heads * D, types), _stream_of(ctx, stream)),
+           "apmoe_kv_append", ctx.L)
+
+
+def attn_workspace(ctx: Context, cache: KvCache, batch: KvBatch, q_heads: int) -> int:
+    n = ctypes.c_size_t()
+    _check(ctx.L.apmoe_attn_workspace(ctx.handle, cache.ref, batch.ref, q_heads, ctypes.byref(n)),
+           "apmoe_attn_workspace", ctx.L)
+    return n.value
+
+
+def _attn(fn: str, ctx, cache, batch, q, q_heads, scale, window, sinks, ws, out, out8, out_scale, stream) -> None:
+    import torch
+    if not isinstance(ws, torch.Tensor):
+        raise ValueError(f"ws: need a byte tensor, got {type(ws)}")
+    _kv_on(ctx, cache, batch)
+    dt, types = _types(q, "q")
+    n = batch.T * q_heads * cache.head_dim
+    qp = _matrix(ctx, q, "q", batch.T, q_heads * cache.head_dim, types)
+    _check(getattr(ctx.L, fn)(ctx.handle, cache.ref, batch.ref, *qp, dt, q_heads, scale, window, sinks,
+                              _arg(ctx, ws, "ws", 0, (torch.uint8,)), ws.numel(), _arg(ctx, out, "out", n, types),
+                              _arg(ctx, out8, "out8", n, _e4m3_types),
+                              _arg(ctx, out_scale, "out_scale", n // 128, _f32), _stream_of(ctx, stream)), fn, ctx.L)
+
+
+def attn_decode(ctx: Context, cache: KvCache, batch: KvBatch, q, q_heads: int, scale: float, window: int, sinks: int,
+                ws, out, out8=None, out_scale=None, stream=None) -> None:
+    """Attention of one new token of each sequence (q [B][q_heads * D]) over its cache;
+    window 0: over all of it, else over the last `window` tokens and the first `sinks`.
+    out in q's type and / or out8, out_scale (e4m3 rows with a scale for each 128 columns).
+    ws: a byte tensor of attn_workspace bytes."""
+    _attn("apmoe_attn_decode", ctx, cache, batch, q, q_heads, scale, window, sinks, ws, out, out8, out_scale, stream)
+
+
+def attn_prefill(ctx: Context, cache: KvCache, batch: KvBatch, q, q_heads: int, scale: float, window: int, sinks: int,
+                 ws, out, out8=None, out_scale=None, stream=None) -> None:
+    """The same for the new tokens of prompts or of their chunks (q_offsets), each row at its
+    own position; their keys and values have been appended before."""
+    _attn("apmoe_attn_prefill", ctx, cache, batch, q, q_heads, scale, window, sinks, ws, out, out8, out_scale, stream)
 
 
 # --------------------------------------------------------------------------- page movement

@@ -22,7 +22,7 @@ SAFE_LIB = os.path.join(PKG, "libapmoe_safe.so")
 PROBE_SRC = "hbm_probe.hip"
 PROBE_LIB = os.path.join(PKG, "libhbmprobe.so")
 SOURCES = ["api.hip", "route.hip", "gemm.hip", "gemm_tile.hip", "elementwise.hip", "norm.hip", "gemm_fp8.hip", "gemm_fp8_tile.hip",
-           "layer_fp8.hip"]
+           "layer_fp8.hip", "kv_append.hip", "attn_decode.hip", "attn_prefill.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

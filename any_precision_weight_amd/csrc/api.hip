@@ -16,6 +16,7 @@
 #include <vector>
 
 #include "internal.h"
+#include "launch_attn.h"
 #include "layer_fp8.h"
 
 using apmoe::DevBlock;
@@ -1376,6 +1377,236 @@ apmoe_status apmoe_moe_forward_fp8(apmoe_ctx *ctx, const apmoe_fp8_experts *ex, 
     if (e == hipSuccess)
         e = apmoe::launch_combine(y, 1, tw, inv, T, kt, H, out, st);
     return e == hipSuccess ? ok() : hip_fail(e, "fp8 layer launch");
+}
+
+// ----------------------------------------------------------------------------
+// the paged key-value cache
+// ----------------------------------------------------------------------------
+
+namespace {
+
+constexpr int kMaxHeads = 1024;
+constexpr int64_t kMaxCached = (int64_t)1 << 30;  // tokens of a sequence
+
+bool type16(int d) { return d == APMOE_F16 || d == APMOE_BF16; }
+
+// Sizes of a cache and a batch; pointers are not looked at.
+apmoe_status kv_sizes(const apmoe_kv_cache *c, const apmoe_kv_batch *s)
+{
+    if (!c || !s)
+        return fail(APMOE_INVALID_ARG, "cache / batch is NULL");
+    if (!type16(c->dtype) && c->dtype != APMOE_E4M3)
+        return fail(APMOE_UNSUPPORTED, "cache dtype %d", c->dtype);
+    if (c->page != 32 && c->page != 64 && c->page != 128 && c->page != 256)
+        return fail(APMOE_INVALID_ARG, "page=%d (need 32, 64, 128 or 256)", c->page);
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
+        return fail(APMOE_INVALID_ARG, "head_dim=%d (need 64, 128 or 256)", c->head_dim);
+    if (c->kv_heads < 1 || c->kv_heads > kMaxHeads || c->n_pages < 1)
+        return fail(APMOE_INVALID_ARG, "kv_heads=%d n_pages=%d (need 1 <= kv_heads <= %d, n_pages >= 1)", c->kv_heads,
+                    c->n_pages, kMaxHeads);
+    if (s->B < 0 || s->B > 65536 || s->T < 0 || s->T >= 1 << 24 || s->max_len < 0)
+        return fail(APMOE_INVALID_ARG, "B=%d T=%d max_len=%d (need 0 <= B <= 65536, 0 <= T < 2^24, max_len >= 0)", s->B,
+                    s->T, s->max_len);
+    if (s->B == 0 && s->T != 0)
+        return fail(APMOE_INVALID_ARG, "T=%d rows of no sequences", s->T);
+    if (s->B > 0 && (s->max_pages < 1 || (int64_t)s->max_pages * c->page > kMaxCached))
+        return fail(APMOE_INVALID_ARG, "max_pages=%d of %d tokens (need 1 to 2^30 tokens)", s->max_pages, c->page);
+    return ok();
+}
+
+apmoe_status attn_heads(const apmoe_kv_cache *c, int32_t q_heads)
+{
+    if (q_heads < 1 || q_heads > kMaxHeads || q_heads % c->kv_heads != 0)
+        return fail(APMOE_INVALID_ARG, "q_heads=%d with kv_heads=%d (need a multiple of it, at most %d)", q_heads,
+                    c->kv_heads, kMaxHeads);
+    return ok();
+}
+
+apmoe_status kv_pointers(const apmoe_kv_cache *c, const apmoe_kv_batch *s)
+{
+    if (!c->k || !c->v || (c->dtype == APMOE_E4M3 && (!c->k_scale || !c->v_scale)) || !s->pages || !s->lens)
+        return fail(APMOE_INVALID_ARG, "the cache's k / v / k_scale / v_scale or the batch's pages / lens is NULL");
+    if (!aligned16(c->k) || !aligned16(c->v) || !aligned4(s->pages) || !aligned4(s->lens) || !aligned4(s->q_offsets) ||
+        (c->dtype == APMOE_E4M3 && (!aligned16(c->k_scale) || !aligned16(c->v_scale))))
+        return fail(APMOE_INVALID_ARG, "misaligned pointer (cache 16 bytes; pages, lens, q_offsets 4)");
+    if (!s->q_offsets && s->T != s->B)
+        return fail(APMOE_INVALID_ARG, "q_offsets is NULL with %d rows of %d sequences", s->T, s->B);
+    return ok();
+}
+
+// Rows of `width` columns of a matrix with this stride.
+apmoe_status kv_rows(const char *name, const void *p, int64_t stride, int64_t width)
+{
+    if (!p || !aligned16(p))
+        return fail(APMOE_INVALID_ARG, "%s NULL or not 16-byte aligned", name);
+    if (stride < width || stride % 8 != 0 || stride > (int64_t)1 << 40)
+        return fail(APMOE_INVALID_ARG, "%s: stride %lld (need a multiple of 8, %lld or more)", name, (long long)stride,
+                    (long long)width);
+    return ok();
+}
+
+apmoe::KvView kv_view(const apmoe_kv_cache *c)
+{
+    return apmoe::KvView{c->k, c->v, c->k_scale, c->v_scale, c->n_pages, __builtin_ctz(c->page), c->kv_heads, c->head_dim,
+                         c->dtype == APMOE_E4M3};
+}
+
+apmoe::AttnBatch kv_batch(const apmoe_kv_cache *c, const apmoe_kv_batch *s)
+{
+    const int room = s->max_pages * c->page;  // at most 2^30
+    return apmoe::AttnBatch{s->pages, s->lens, s->q_offsets, s->B, s->T, s->max_pages,
+                            s->max_len > 0 && s->max_len < room ? s->max_len : room};
+}
+
+struct WsLayoutAttn {
+    int slots;
+    size_t part_o, part_ml, total;
+};
+
+WsLayoutAttn ws_layout_attn(const apmoe_kv_cache *c, int B, int q_heads)
+{
+    WsLayoutAttn L;
+    L.slots = apmoe::decode_slots(B, c->kv_heads, q_heads);
+    L.part_o = 0;
+    L.part_ml = up256((size_t)L.slots * q_heads * c->head_dim * 4);
+    L.total = L.part_ml + up256((size_t)L.slots * q_heads * 8);
+    return L;
+}
+
+// What the two attentions check alike, and their parameters.
+apmoe_status attn_args(apmoe_ctx *ctx, const apmoe_kv_cache *cache, const apmoe_kv_batch *batch, const uint16_t *q,
+                       int64_t q_stride, int32_t dtype, int32_t q_heads, float scale, int32_t window, int32_t sinks,
+                       void *ws, size_t ws_bytes, uint16_t *out, uint8_t *out8, float *out_scale,
+                       apmoe::AttnParams *p)
+{
+    if (!ctx)
+        return fail(APMOE_INVALID_ARG, "ctx is NULL");
+    apmoe_status s = kv_sizes(cache, batch);
+    if (s == APMOE_OK)
+        s = attn_heads(cache, q_heads);
+    if (s != APMOE_OK)
+        return s;
+    if (!type16(dtype) || (cache->dtype != dtype && cache->dtype != APMOE_E4M3))
+        return fail(APMOE_UNSUPPORTED, "dtype %d with a cache of dtype %d", dtype, cache->dtype);
+    if (!(scale >= -3.4e38f && scale <= 3.4e38f) || window < 0 || window > 1 << 30 || sinks < 0)
+        return fail(APMOE_INVALID_ARG, "scale=%g window=%d sinks=%d", (double)scale, window, sinks);
+    if (!out8 != !out_scale)
+        return fail(APMOE_INVALID_ARG, "out8 and out_scale: one is NULL");
+    if (out8 && cache->head_dim % 128 != 0)
+        return fail(APMOE_UNSUPPORTED, "out8 with head_dim %d", cache->head_dim);
+    if (batch->T == 0)  // outputs of no rows have no address
+        return ok();
+    if (!out && !out8)
+        return fail(APMOE_INVALID_ARG, "out and out8 are NULL");
+    s = kv_pointers(cache, batch);
+    if (s == APMOE_OK)
+        s = kv_rows("q", q, q_stride, (int64_t)q_heads * cache->head_dim);
+    if (s != APMOE_OK)
+        return s;
+    if (!aligned16(out) || !aligned16(out8) || !aligned4(out_scale))
+        return fail(APMOE_INVALID_ARG, "misaligned output (16 bytes; out_scale 4)");
+    const WsLayoutAttn L = ws_layout_attn(cache, batch->B, q_heads);
+    if (!ws || ws_bytes < L.total || ((uintptr_t)ws & 255u))
+        return fail(APMOE_INVALID_ARG, "workspace NULL, unaligned or smaller than %zu bytes", L.total);
+    char *w = reinterpret_cast<char *>(ws);
+    *p = apmoe::AttnParams{kv_view(cache), kv_batch(cache, batch), q, q_stride, dtype, q_heads, scale, window, sinks,
+                           out, out8, out_scale, reinterpret_cast<float *>(w + L.part_o),
+                           reinterpret_cast<float *>(w + L.part_ml), L.slots};
+    return ok();
+}
+
+}  // namespace
+
+apmoe_status apmoe_kv_append(apmoe_ctx *ctx, const apmoe_kv_cache *cache, const apmoe_kv_batch *batch,
+                             const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                             const uint16_t *v, int64_t v_stride, int32_t dtype, int32_t q_heads, const float *rope,
+                             int32_t n_pos, int32_t rot, int32_t interleaved, uint16_t *q_out, void *stream)
+{
+    if (!ctx)
+        return fail(APMOE_INVALID_ARG, "ctx is NULL");
+    apmoe_status s = kv_sizes(cache, batch);
+    if (s != APMOE_OK)
+        return s;
+    if (!type16(dtype) || (cache->dtype != dtype && cache->dtype != APMOE_E4M3))
+        return fail(APMOE_UNSUPPORTED, "dtype %d with a cache of dtype %d", dtype, cache->dtype);
+    if (q_heads < 0 || q_heads > kMaxHeads)
+        return fail(APMOE_INVALID_ARG, "q_heads=%d", q_heads);
+    if (rot < 0 || rot > cache->head_dim || rot % 16 != 0 || (rot > 0 && n_pos < 1))
+        return fail(APMOE_INVALID_ARG, "rot=%d n_pos=%d (need rot%%16==0, 0 <= rot <= %d, n_pos >= 1)", rot, n_pos,
+                    cache->head_dim);
+    if (batch->T == 0)
+        return ok();
+    s = kv_pointers(cache, batch);
+    const int64_t kw = (int64_t)cache->kv_heads * cache->head_dim;
+    if (s == APMOE_OK && q_heads > 0)
+        s = kv_rows("q", q, q_stride, (int64_t)q_heads * cache->head_dim);
+    if (s == APMOE_OK)
+        s = kv_rows("k", k, k_stride, kw);
+    if (s == APMOE_OK)
+        s = kv_rows("v", v, v_stride, kw);
+    if (s != APMOE_OK)
+        return s;
+    if (q_heads > 0 && (!q_out || !aligned16(q_out) || q_out == q))
+        return fail(APMOE_INVALID_ARG, "q_out NULL, not 16-byte aligned or q itself");
+    if (rot > 0 && (!rope || !aligned16(rope)))
+        return fail(APMOE_INVALID_ARG, "rope NULL or not 16-byte aligned");
+    OnDevice dev(ctx);
+    if (dev.status() != APMOE_OK)
+        return dev.status();
+    const apmoe::AppendParams p{kv_view(cache), kv_batch(cache, batch), q, k, v, q_stride, k_stride, v_stride, dtype,
+                                q_heads, rot > 0 ? rope : nullptr, n_pos, rot, interleaved, q_out};
+    const hipError_t e = apmoe::launch_kv_append(p, reinterpret_cast<hipStream_t>(stream));
+    return e == hipSuccess ? ok() : hip_fail(e, "kv_append launch");
+}
+
+apmoe_status apmoe_attn_workspace(apmoe_ctx *ctx, const apmoe_kv_cache *cache, const apmoe_kv_batch *batch,
+                                  int32_t q_heads, size_t *bytes)
+{
+    if (!ctx || !bytes)
+        return fail(APMOE_INVALID_ARG, "ctx / bytes is NULL");
+    apmoe_status s = kv_sizes(cache, batch);
+    if (s == APMOE_OK)
+        s = attn_heads(cache, q_heads);
+    if (s != APMOE_OK)
+        return s;
+    *bytes = ws_layout_attn(cache, batch->B, q_heads).total;
+    return ok();
+}
+
+apmoe_status apmoe_attn_decode(apmoe_ctx *ctx, const apmoe_kv_cache *cache, const apmoe_kv_batch *batch,
+                               const uint16_t *q, int64_t q_stride, int32_t dtype, int32_t q_heads, float scale,
+                               int32_t window, int32_t sinks, void *ws, size_t ws_bytes, uint16_t *out, uint8_t *out8,
+                               float *out_scale, void *stream)
+{
+    apmoe::AttnParams p;
+    const apmoe_status s = attn_args(ctx, cache, batch, q, q_stride, dtype, q_heads, scale, window, sinks, ws, ws_bytes,
+                                     out, out8, out_scale, &p);
+    if (s != APMOE_OK || batch->T == 0)
+        return s;
+    if (batch->q_offsets)
+        return fail(APMOE_INVALID_ARG, "q_offsets with one row a sequence");
+    OnDevice dev(ctx);
+    if (dev.status() != APMOE_OK)
+        return dev.status();
+    const hipError_t e = apmoe::launch_attn_decode(p, reinterpret_cast<hipStream_t>(stream));
+    return e == hipSuccess ? ok() : hip_fail(e, "attn_decode launch");
+}
+
+apmoe_status apmoe_attn_prefill(apmoe_ctx *ctx, const apmoe_kv_cache *cache, const apmoe_kv_batch *batch,
+                                const uint16_t *q, int64_t q_stride, int32_t dtype, int32_t q_heads, float scale,
+                                int32_t window, int32_t sinks, void *ws, size_t ws_bytes, uint16_t *out, uint8_t *out8,
+                                float *out_scale, void *stream)
+{
+    apmoe::AttnParams p;
+    const apmoe_status s = attn_args(ctx, cache, batch, q, q_stride, dtype, q_heads, scale, window, sinks, ws, ws_bytes,
+                                     out, out8, out_scale, &p);
+    if (s != APMOE_OK || batch->T == 0)
+        return s;
+    OnDevice dev(ctx);
+    if (dev.status() != APMOE_OK)
+        return dev.status();
+    const hipError_t e = apmoe::launch_attn_prefill(p, reinterpret_cast<hipStream_t>(stream));
+    return e == hipSuccess ? ok() : hip_fail(e, "attn_prefill launch");
 }
 
 }  // extern "C"

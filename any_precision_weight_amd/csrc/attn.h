@@ -1,0 +1,132 @@
+// attn.h -- attention over a paged key-value cache: what its kernels share (not installed).
+//
+// A page holds `page` tokens of every key-value head; inside a page each head has page * D
+// elements of K and of V, in the order of the matrix instructions' operands:
+//
+//   K  16-token tiles [D / c][16][c], c = 16 bytes of elements: 64 lanes that read 16 bytes
+//      each, one after the other, get the operand of 32 columns (2-byte elements) or 64
+//      (e4m3) of a 16-row product, 1 KB in whole lines, without LDS or a lane exchange;
+//   V  32-token tiles [4][D][8]: entry (g, d) holds tokens 4g .. 4g+3 and 16+4g .. 16+4g+3 of
+//      column d.  Those are the tokens whose scores lane group g of two 16 x 16 products
+//      holds, so probabilities go into the second product from the registers they are in.
+//
+// Both products are computed transposed (keys x queries, then values x queries), so that a
+// lane keeps one query column through both: its running maximum and sum need no lane but
+// those with the same column.
+#pragma once
+
+#include "fp8.h"
+#include "launch_attn.h"
+
+namespace apmoe {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef float float2v __attribute__((ext_vector_type(2)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kTile = 32;  // tokens of a V tile
+
+__device__ inline float4v mfma16(int dt, const u32x4 &a, const u32x4 &b, const float4v &c)
+{
+    if (dt == APMOE_F16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c, 0,
+                                                      0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+}
+
+__device__ inline float16v mfma32(int dt, const u32x4 &a, const u32x4 &b, const float16v &c)
+{
+    if (dt == APMOE_F16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c, 0,
+                                                      0, 0);
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+}
+
+// Two fp32 values as two 16-bit ones, to nearest even, lo in the low half.
+template <int DT>
+__device__ inline uint32_t pack2(float lo, float hi)
+{
+    const float2v v = {lo, hi};
+    if constexpr (DT == APMOE_F16)
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, half2v));
+    else
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+
+template <int DT>
+__device__ inline float low16(uint32_t w)
+{
+    if constexpr (DT == APMOE_F16)
+        return (float)__builtin_bit_cast(half2v, w)[0];
+    else
+        return __builtin_bit_cast(float, w << 16);
+}
+
+template <int DT>
+__device__ inline float high16(uint32_t w)
+{
+    if constexpr (DT == APMOE_F16)
+        return (float)__builtin_bit_cast(half2v, w)[1];
+    else
+        return __builtin_bit_cast(float, w & 0xFFFF0000u);
+}
+
+// Eight e4m3 bytes as eight 16-bit values (exact: both types hold e4m3's).
+template <int DT>
+__device__ inline u32x4 from_e4m3x8(uint32_t lo, uint32_t hi)
+{
+    if constexpr (DT == APMOE_F16)
+        return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true))};
+    else
+        return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true))};
+}
+
+// Tokens of a sequence of `len` tokens that the cache can hold at all.
+__device__ inline int cached_tokens(const AttnBatch &S, int len) { return max(0, min(len, S.room)); }
+
+__device__ inline int wave_scan(int v)
+{
+    const int lane = threadIdx.x % kWave;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+        const int o = __shfl_up(v, d, kWave);
+        v += lane >= d ? o : 0;
+    }
+    return v;
+}
+
+// Items of the sequences one after the other, count(b) of sequence b: the sequence b and the
+// index `local` in it of item w, and the sequence's number of items n; false when there are
+// no more than w items.  Every wave computes the same answer; 64 sequences a step.
+template <class Count>
+__device__ inline bool find_item(int B, int w, const Count &count, int &b, int &local, int &n)
+{
+    const int lane = threadIdx.x % kWave;
+    int base = 0;
+    for (int b0 = 0; b0 < B; b0 += kWave) {
+        const int mine = b0 + lane < B ? count(b0 + lane) : 0;
+        const int incl = wave_scan(mine);
+        const int total = __builtin_amdgcn_readlane(incl, kWave - 1);
+        if (w - base < total) {
+            const int at = (int)__builtin_ctzll(__ballot(incl > w - base));
+            b = b0 + at;
+            n = __builtin_amdgcn_readlane(mine, at);
+            local = w - base - (__builtin_amdgcn_readlane(incl, at) - n);
+            return true;
+        }
+        base += total;
+    }
+    return false;
+}
+
+}  // namespace apmoe

@@ -1,0 +1,510 @@
+// attn_decode.hip -- attention of one new token of each sequence over the paged cache,
+// split over the cache's length and joined.
+//
+//   o = sum_j p_j v_j / sum_j p_j,  p_j = exp2(c q.k_j - m),  c = scale * log2(e), m the running
+//   maximum; parts (m, l, o) and (m', l', o') join as exp2(m - M) and exp2(m' - M) times each,
+//   M = max(m, m').
+//
+// Bound by the cache's bytes.  A wave takes one 32-token tile after the other: the scores of
+// 16 query heads of a key-value head from two 16-token products, the softmax in registers,
+// the second product on the probabilities where they are.  Keys and values go from memory
+// into registers (no LDS: the operands of the products are whole lines of the cache); the
+// next tile's keys are asked for when this one's are used, its values likewise.
+//
+// Probabilities are given to the second product as the sum of two 16-bit numbers: the
+// matrix units have room (16 columns are computed for a group of 1 to 16 heads), and the
+// output then has the error of its own rounding only.
+#include <algorithm>
+
+#include "attn.h"
+
+namespace apmoe {
+namespace {
+
+constexpr int kCols = 16;      // query heads of one workgroup
+constexpr int kPartTiles = 4;  // the shortest part of a split sequence, in tiles
+constexpr int kParts = 1024;   // workgroups that a call is split into, about
+
+// The tiles of one sequence that its query sees: [0, sink) and [first, end).
+struct Span {
+    int pos, end_tok, sink, first, tiles;
+};
+
+__device__ inline Span span_of(const AttnParams &P, int b)
+{
+    const int len = P.s.lens[b];
+    Span r;
+    r.pos = len - 1;
+    r.end_tok = cached_tokens(P.s, len);
+    const int end = (r.end_tok + kTile - 1) / kTile;
+    r.first = P.window ? max(0, len - P.window) / kTile : 0;
+    r.sink = P.window ? min(r.first, (int)(((int64_t)P.sinks + kTile - 1) / kTile)) : 0;
+    r.sink = min(r.sink, end);
+    r.tiles = r.sink + max(0, end - r.first);
+    return r;
+}
+
+// Tiles of a part: every workgroup and the join compute the same number, from the lengths.
+__device__ inline int part_tiles(const AttnParams &P)
+{
+    const int lane = threadIdx.x % kWave;
+    int64_t sum = 0;
+    for (int b = lane; b < P.s.B; b += kWave)
+        sum += span_of(P, b).tiles;
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1)
+        sum += __shfl_xor((long long)sum, d, kWave);
+    const int64_t extra = P.slots - P.s.B;  // sum / ct more parts than sequences at most
+    const int64_t ct = extra > 0 ? (sum + extra - 1) / extra : sum;
+    return (int)max((int64_t)kPartTiles, min(ct, (int64_t)1 << 30));
+}
+
+__device__ inline int parts_of(int tiles, int ct) { return max(1, (tiles + ct - 1) / ct); }
+
+// 8-bit rows: a group of 128 columns is D / 128-th of a head.
+__device__ inline void store_row(const AttnParams &P, size_t row, int d, const float (&v)[4], float scale)
+{
+    const size_t at = row * P.kv.D + d;
+    if (P.out8) {
+        const float inv = 1.0f / scale;
+        *reinterpret_cast<uint32_t *>(P.out8 + at) = to_e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+    }
+    if (P.out) {
+        const u32x2 w = P.dtype == APMOE_F16 ? u32x2{pack2<APMOE_F16>(v[0], v[1]), pack2<APMOE_F16>(v[2], v[3])}
+                                             : u32x2{pack2<APMOE_BF16>(v[0], v[1]), pack2<APMOE_BF16>(v[2], v[3])};
+        *reinterpret_cast<u32x2 *>(P.out + at) = w;
+    }
+}
+
+template <int QT, bool C8, int D>
+struct Tile {
+    static constexpr int kVT = C8 ? APMOE_BF16 : QT;  // type of the second product (attn.h)
+    static constexpr int KL = C8 ? D / 64 : D / 32;   // 1 KB requests of 16 tokens' keys
+    u32x4 k[2][KL];
+    u32x4 v16[C8 ? 1 : D / 16];
+    u32x2 v8[C8 ? D / 16 : 1];
+    float4v ks[2], vs[2];
+
+    __device__ inline void load_k(const KvView &kv, size_t tile, size_t scale, int lane)
+    {
+        const char *p = static_cast<const char *>(kv.k) + tile * (C8 ? 1 : 2) + lane * 16;
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+#pragma unroll
+            for (int s = 0; s < KL; ++s)
+                k[a][s] = *reinterpret_cast<const u32x4 *>(p + a * 16 * D * (C8 ? 1 : 2) + s * 1024);
+            if constexpr (C8)
+                ks[a] = *reinterpret_cast<const float4v *>(kv.ks + scale + 16 * a + 4 * (lane / 16));
+        }
+    }
+    __device__ inline void load_v(const KvView &kv, size_t tile, size_t scale, int lane)
+    {
+        const size_t at = ((size_t)(lane / 16) * D + lane % 16) * 8;
+        if constexpr (C8) {
+            const char *p = static_cast<const char *>(kv.v) + tile + at;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+                v8[i] = *reinterpret_cast<const u32x2 *>(p + i * 128);
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+                vs[a] = *reinterpret_cast<const float4v *>(kv.vs + scale + 16 * a + 4 * (lane / 16));
+        } else {
+            const char *p = static_cast<const char *>(kv.v) + (tile + at) * 2;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+                v16[i] = *reinterpret_cast<const u32x4 *>(p + i * 256);
+        }
+    }
+    __device__ inline u32x4 value(int i) const
+    {
+        if constexpr (C8)
+            return from_e4m3x8<kVT>(v8[i][0], v8[i][1]);
+        else
+            return v16[i];
+    }
+};
+
+// Grid: x the slots (a part of a sequence each), y key-value heads x groups of 16 query heads.
+template <int QT, bool C8, int D, int NW>
+__global__ void __launch_bounds__(NW *kWave) decode_kernel(const AttnParams P)
+{
+    using T = Tile<QT, C8, D>;
+    constexpr int DT = D / 16;
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int G = P.Hq / P.kv.Hkv, kvh = blockIdx.y % P.kv.Hkv, h0 = blockIdx.y / P.kv.Hkv * kCols;
+    const int ct = part_tiles(P);
+    int b, part, parts;
+    if (!find_item(P.s.B, blockIdx.x, [&](int i) { return parts_of(span_of(P, i).tiles, ct); }, b, part, parts))
+        return;
+    const Span sp = span_of(P, b);
+    const int t0 = part * ct, t1 = min(sp.tiles, t0 + ct);
+    const int col = lane % 16, g = lane / 16;
+    const bool live = h0 + col < G;
+    // the queries: operand column `col`, the same columns of the row as the keys' lanes have
+    u32x4 q[D / 32];
+    {
+        const uint16_t *row = P.q + (size_t)b * P.q_stride + ((size_t)kvh * G + (live ? h0 + col : 0)) * D;
+#pragma unroll
+        for (int s = 0; s < D / 32; ++s)
+            q[s] = *reinterpret_cast<const u32x4 *>(row + (C8 ? 64 * (s / 2) + 16 * g + 8 * (s % 2) : 32 * s + 8 * g));
+    }
+    const float c = P.scale * kLog2e;
+    const int shift = P.kv.page_shift, tshift = shift - 5;
+    const size_t head = (size_t)D << shift;
+    const int32_t *table = P.s.pages + (size_t)b * P.s.max_pages;
+
+    float m = -INFINITY, l = 0.0f;
+    float4v o[DT];
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+        o[i] = float4v{0.f, 0.f, 0.f, 0.f};
+
+    // A wave's tiles are t0 + wave, + NW, ...; lane i has the page of the i-th of 64.
+    auto token_tile = [&](int t) { return t < sp.sink ? t : sp.first + t - sp.sink; };
+    int ids = 0;
+    auto load_ids = [&](int t) {
+        const int mine = t + lane * NW;
+        ids = mine < t1 ? table[token_tile(mine) >> tshift] : -1;
+    };
+    T cur;
+    size_t tile = 0, scale = 0;
+    bool here = false;
+    auto locate = [&](int t, int i) {
+        const int id = __builtin_amdgcn_readlane(ids, i);
+        here = id >= 0 && id < P.kv.n_pages;
+        const int at = token_tile(t) & ((1 << tshift) - 1);
+        const size_t base = (size_t)(here ? id : 0) * P.kv.Hkv + kvh;
+        tile = base * head + (size_t)at * kTile * D;
+        scale = (base << shift) + at * kTile;
+    };
+    int t = t0 + wave, i = 0;
+    if (t < t1) {
+        load_ids(t);
+        locate(t, 0);
+        cur.load_k(P.kv, tile, scale, lane);
+        cur.load_v(P.kv, tile, scale, lane);
+    }
+    for (; t < t1; t += NW) {
+        const bool on_page = here;
+        const int next = t + NW;
+        float4v s[2];
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+            s[a] = float4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) {
+                if constexpr (C8) {
+                    const u32x4 &w = cur.k[a][j / 2];
+                    s[a] = mfma16(QT, from_e4m3x8<QT>(w[j % 2 * 2], w[j % 2 * 2 + 1]), q[j], s[a]);
+                } else {
+                    s[a] = mfma16(QT, cur.k[a][j], q[j], s[a]);
+                }
+            }
+            if constexpr (C8)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    s[a][j] *= cur.ks[a][j];
+        }
+        if (next < t1) {
+            if (++i == kWave) {
+                i = 0;
+                load_ids(next);
+            }
+            locate(next, i);
+            cur.load_k(P.kv, tile, scale, lane);
+        }
+        // tokens of the tile: 16 a + 4 g + j of lane group g
+        const int tok0 = token_tile(t) * kTile;
+        const int last = tok0 + kTile - 1;
+        const bool whole = on_page && last < sp.end_tok &&
+                           (!P.window || sp.pos - tok0 < P.window || last < P.sinks);
+        uint32_t seen = 0xFFu;
+        if (!whole) {
+            seen = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int tok = tok0 + 16 * (e / 4) + 4 * g + e % 4;
+                const bool in = on_page && tok < sp.end_tok &&
+                                (!P.window || sp.pos - tok < P.window || tok < P.sinks);
+                seen |= in ? 1u << e : 0u;
+            }
+        }
+        float x[8], top = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            x[e] = s[e / 4][e % 4] * c;
+            if (!whole && !(seen >> e & 1))
+                x[e] = -INFINITY;
+            top = fmaxf(top, x[e]);
+        }
+        top = fmaxf(top, __shfl_xor(top, 16, kWave));
+        top = fmaxf(top, __shfl_xor(top, 32, kWave));
+        if (__any(top > m)) {
+            const float to = fmaxf(m, top);
+            const float f = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+            m = to;
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    o[d][j] *= f;
+        }
+        const float base = m == -INFINITY ? 0.0f : m;
+        float p[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            p[e] = __builtin_amdgcn_exp2f(x[e] - base);
+            l += p[e];
+        }
+        if constexpr (C8)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                p[e] *= cur.vs[e / 4][e % 4];
+                if (!whole && !(seen >> e & 1))
+                    p[e] = 0.0f;  // whatever scale lies there
+            }
+        u32x4 hi, lo;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            hi[e] = pack2<T::kVT>(p[2 * e], p[2 * e + 1]);
+            lo[e] = pack2<T::kVT>(p[2 * e] - low16<T::kVT>(hi[e]), p[2 * e + 1] - high16<T::kVT>(hi[e]));
+        }
+        if (whole) {
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                const u32x4 v = cur.value(d);
+                o[d] = mfma16(T::kVT, v, hi, o[d]);
+                o[d] = mfma16(T::kVT, v, lo, o[d]);
+            }
+        } else {
+            // what lies in places that are not seen may be a NaN: no factor makes it vanish
+            u32x4 keep;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                keep[e] = (seen >> (2 * e) & 1 ? 0xFFFFu : 0u) | (seen >> (2 * e + 1) & 1 ? 0xFFFF0000u : 0u);
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                const u32x4 v = cur.value(d) & keep;
+                o[d] = mfma16(T::kVT, v, hi, o[d]);
+                o[d] = mfma16(T::kVT, v, lo, o[d]);
+            }
+        }
+        if (next < t1)
+            cur.load_v(P.kv, tile, scale, lane);
+    }
+    l += __shfl_xor(l, 16, kWave);
+    l += __shfl_xor(l, 32, kWave);
+
+    // Join the waves, half of them at a time into the other half.
+    __shared__ float ml[NW][2][kCols];
+    __shared__ float4v os[NW / 2][DT][kWave];
+    if (g == 0) {
+        ml[wave][0][col] = m;
+        ml[wave][1][col] = l;
+    }
+    __syncthreads();
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < NW; ++w)
+        M = fmaxf(M, ml[w][0][col]);
+    float L = 0.0f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        const float mw = ml[w][0][col];
+        L += mw == -INFINITY ? 0.0f : ml[w][1][col] * __builtin_amdgcn_exp2f(mw - M);
+    }
+    {
+        const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - M);
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                o[d][j] = m == -INFINITY ? 0.0f : o[d][j] * f;
+    }
+#pragma unroll
+    for (int half = NW / 2; half >= 1; half /= 2) {
+        if (wave >= half && wave < 2 * half)
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+                os[wave - half][d][lane] = o[d];
+        __syncthreads();
+        if (wave < half)
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    o[d][j] += os[wave][d][lane][j];
+        __syncthreads();
+    }
+    if (wave != 0)
+        return;
+    const size_t headcol = (size_t)kvh * G + h0 + col;
+    if (parts > 1) {
+        if (!live)
+            return;
+        const size_t at = (size_t)blockIdx.x * P.Hq + headcol;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+            *reinterpret_cast<float4v *>(P.part_o + at * D + 16 * d + 4 * g) = o[d];
+        if (g == 0) {
+            P.part_ml[2 * at] = M;
+            P.part_ml[2 * at + 1] = L;
+        }
+        return;
+    }
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;  // nothing seen: zeros
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            o[d][j] *= inv;
+    const size_t row = (size_t)b * P.Hq + headcol;
+    constexpr int kGroups = D < kBlk ? 1 : D / kBlk;
+    float scale8[kGroups] = {};
+    if (D >= kBlk && P.out8) {
+#pragma unroll
+        for (int n = 0; n < kGroups; ++n) {
+            uint32_t a = 0;
+#pragma unroll
+            for (int d = 0; d < DT / kGroups; ++d)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    a = max(a, mag(o[n * (DT / kGroups) + d][j]));
+            a = max(a, (uint32_t)__shfl_xor((int)a, 16, kWave));
+            a = max(a, (uint32_t)__shfl_xor((int)a, 32, kWave));
+            scale8[n] = scale_of(a);
+            if (live && g == 0)
+                P.out_scale[row * kGroups + n] = scale8[n];
+        }
+    }
+    if (!live)
+        return;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) {
+        const float v[4] = {o[d][0], o[d][1], o[d][2], o[d][3]};
+        store_row(P, row, 16 * d + 4 * g, v, scale8[d * kGroups / DT]);
+    }
+}
+
+// Joins the parts of split sequences: a workgroup has one query head of one sequence, its
+// first D / 4 threads the columns and the others the same columns of other parts.
+template <int D>
+__global__ void __launch_bounds__(256) join_kernel(const AttnParams P)
+{
+    constexpr int kLanes = D / 4, kRows = 256 / kLanes;
+    const int ct = part_tiles(P);
+    const int lane = threadIdx.x % kWave, b = blockIdx.x, h = blockIdx.y;
+    const int n = parts_of(span_of(P, b).tiles, ct);
+    if (n <= 1)
+        return;
+    int first = 0;
+    for (int i = lane; i < b; i += kWave)
+        first += parts_of(span_of(P, i).tiles, ct);
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1)
+        first += __shfl_xor(first, d, kWave);
+    const float *ml = P.part_ml + 2 * ((size_t)first * P.Hq + h);
+    const size_t step = 2 * (size_t)P.Hq;
+    float M = -INFINITY;
+    for (int i = lane; i < n; i += kWave)
+        M = fmaxf(M, ml[i * step]);
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1)
+        M = fmaxf(M, __shfl_xor(M, d, kWave));
+    const int c = threadIdx.x % kLanes, r = threadIdx.x / kLanes;
+    float L = 0.0f;
+    float4v o = {0.f, 0.f, 0.f, 0.f};
+    for (int i = r; i < n; i += kRows) {
+        const float m = ml[i * step], f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - M);
+        const float4v p =
+            *reinterpret_cast<const float4v *>(P.part_o + ((size_t)(first + i) * P.Hq + h) * D + 4 * c);
+        if (m != -INFINITY) {
+            L += f * ml[i * step + 1];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                o[j] += f * p[j];
+        }
+    }
+    __shared__ float4v os[kRows][kLanes];
+    __shared__ float ls[kRows];
+    __shared__ uint32_t top[kLanes];
+    os[r][c] = o;
+    if (c == 0)
+        ls[r] = L;
+    __syncthreads();
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (r == 0) {
+        L = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            L += ls[i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j] += os[i][c][j];
+        }
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+        uint32_t a = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j] *= inv;
+            a = max(a, mag(v[j]));
+        }
+        top[c] = a;
+    }
+    __syncthreads();
+    if (r != 0)
+        return;
+    const size_t row = (size_t)b * P.Hq + h;
+    float scale = 1.0f;
+    if (D >= kBlk && P.out8) {
+        uint32_t a = 0;
+        for (int i = 0; i < kBlk / 4; ++i)
+            a = max(a, top[c / (kBlk / 4) * (kBlk / 4) + i]);
+        scale = scale_of(a);
+        if (c % (kBlk / 4) == 0)
+            P.out_scale[row * (D / kBlk) + c / (kBlk / 4)] = scale;
+    }
+    store_row(P, row, 4 * c, v, scale);
+}
+
+template <int QT, bool C8, int D>
+hipError_t decode_launch(const AttnParams &P, hipStream_t s)
+{
+    constexpr int NW = 4;
+    const int G = P.Hq / P.kv.Hkv;
+    hipLaunchKernelGGL((decode_kernel<QT, C8, D, NW>), dim3(P.slots, P.kv.Hkv * ((G + kCols - 1) / kCols)),
+                       dim3(NW * kWave), 0, s, P);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || P.s.room <= kPartTiles * kTile)
+        return e;
+    hipLaunchKernelGGL((join_kernel<D>), dim3(P.s.B, P.Hq), dim3(256), 0, s, P);
+    return hipGetLastError();
+}
+
+template <int QT, bool C8>
+hipError_t decode_dim(const AttnParams &P, hipStream_t s)
+{
+    if (P.kv.D == 64)
+        return decode_launch<QT, C8, 64>(P, s);
+    if (P.kv.D == 128)
+        return decode_launch<QT, C8, 128>(P, s);
+    return decode_launch<QT, C8, 256>(P, s);
+}
+
+}  // namespace
+
+int decode_slots(int B, int Hkv, int Hq)
+{
+    const int rows = Hkv * ((Hq / Hkv + kCols - 1) / kCols);
+    return B + std::max(1, kParts / rows);
+}
+
+hipError_t launch_attn_decode(const AttnParams &P, hipStream_t s)
+{
+    if (P.dtype == APMOE_F16)
+        return P.kv.c8 ? decode_dim<APMOE_F16, true>(P, s) : decode_dim<APMOE_F16, false>(P, s);
+    return P.kv.c8 ? decode_dim<APMOE_BF16, true>(P, s) : decode_dim<APMOE_BF16, false>(P, s);
+}
+
+}  // namespace apmoe

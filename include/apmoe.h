@@ -68,7 +68,8 @@ typedef int32_t apmoe_status;
 
 #define APMOE_F16 0
 #define APMOE_F32 1
-#define APMOE_BF16 2 /* the 8-bit path's calls only */
+#define APMOE_BF16 2 /* the 8-bit path's and the key-value cache's calls only */
+#define APMOE_E4M3 3 /* type of a key-value cache only */
 
 #define APMOE_MIN_BITS 3
 #define APMOE_MAX_BITS 8
@@ -558,6 +559,145 @@ apmoe_status apmoe_moe_forward_fp8(apmoe_ctx *ctx, const apmoe_fp8_experts *ex, 
                                    const float *x_scale, const uint16_t *w_router, const float *bias, int32_t T,
                                    int32_t topk, int32_t n_shared, int32_t renormalize, void *ws, size_t ws_bytes,
                                    uint16_t *out, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * The paged key-value cache, and attention over it: the other half of a decoder layer
+ * (norm, projection by apmoe_gemm_fp8, these calls, projection, norm, MoE layer)
+ *
+ * The cache is a pool of pages of `page` tokens; sequence b's token at position p lies in
+ * page pages[b][p / page], at place p % page.  A page holds page * head_dim elements of K
+ * and of V for each key-value head.  Their order inside a head of a page is the order in
+ * which the matrix instructions take them:
+ *   K  [page / 16][D / c][16][c]: token t, column d at [t / 16][d / c][t % 16][d % c],
+ *      c = 16 bytes of elements (8 or 16);
+ *   V  [page / 32][4][D][8]: token t, column d at
+ *      [t / 32][t % 16 / 4][d][t % 32 / 16 * 4 + t % 4].
+ * Elements are of the queries' type (APMOE_F16, APMOE_BF16) or APMOE_E4M3, which has one
+ * fp32 scale for each token and head: s = max(max |row| / 448, 2^-126) and the elements are
+ * e4m3(row / s), rounded once (the quotient is fp64's), to nearest even.  A row with a NaN
+ * or an infinity stands for NaN.
+ * Like the other calls of the 8-bit path these make the context's device current for their
+ * own time only; they use no counters of the context, so calls on one context may run at
+ * the same time (the two attentions need a workspace each then).
+ * ------------------------------------------------------------------------ */
+
+/* A pool of pages; device memory, caller-owned (layer by layer: one pool each).
+ *   page: 32, 64, 128 or 256; head_dim: 64, 128 or 256; 1 <= kv_heads <= 1024;
+ *   1 <= n_pages.
+ *   k, v: [n_pages][kv_heads][page * head_dim], 16-byte aligned;
+ *   k_scale, v_scale: fp32 [n_pages][kv_heads][page], 16-byte aligned (APMOE_E4M3; else
+ *   not looked at). */
+typedef struct apmoe_kv_cache {
+    int32_t dtype;
+    int32_t n_pages;
+    int32_t page;
+    int32_t kv_heads;
+    int32_t head_dim;
+    void *k;
+    void *v;
+    float *k_scale;
+    float *v_scale;
+} apmoe_kv_cache;
+
+/* The sequences of one call.
+ *   pages     [B][max_pages], device: page numbers.  Entries past a sequence's last token
+ *             are not read.  A number outside 0 .. n_pages-1 is no page: its tokens are
+ *             neither stored nor seen (pages that a window has left behind may be given
+ *             away and their entries set to -1).
+ *   lens      [B], device: tokens of each sequence, those of this call included; 0 or less:
+ *             an empty one.
+ *   q_offsets [B + 1], device, q_offsets[0] = 0: the rows q_offsets[b] .. q_offsets[b+1]-1
+ *             are sequence b's last ones, in their order.  NULL: row b is sequence b's last
+ *             token, and T = B.
+ *   T         rows of the call's matrices.  Rows at or past q_offsets[B] are left as they
+ *             were.
+ *   max_len   no sequence has more tokens (0: max_pages * page); tokens at or past it are
+ *             neither stored nor seen.  A small bound saves a launch of apmoe_attn_decode.
+ * Limits: 0 <= B <= 65536, 0 <= T < 2^24, max_pages * page <= 2^30 and 1 <= max_pages
+ * (B > 0), 0 <= max_len. */
+typedef struct apmoe_kv_batch {
+    int32_t B;
+    int32_t T;
+    int32_t max_pages;
+    int32_t max_len;
+    const int32_t *pages;
+    const int32_t *lens;
+    const int32_t *q_offsets;
+} apmoe_kv_batch;
+
+/*
+ * Position rotation of the new tokens' queries and keys, and their keys and values into the
+ * cache.
+ *   q [T][q_heads * D], k and v [T][kv_heads * D] of dtype (APMOE_F16, APMOE_BF16), rows
+ *   *_stride elements apart (parts of one projection's rows, for instance);
+ *   rope fp32 [n_pos][rot]: row p holds the rot / 2 cosines, then the sines of position p;
+ *   a pair (x, y) of columns becomes (x c - y s, x s + y c): pair i is columns i and
+ *   i + rot / 2, or with interleaved != 0 columns 2i and 2i + 1, of each head; the columns
+ *   from rot on are taken as they are (rot = 0: all of them, rope is not read);
+ *   q_out [T][q_heads * D] of dtype, dense, not q.  q and q_out are NULL when q_heads = 0
+ *   (keys and values only).
+ * Rotations are fp64, each value rounded once.  A row whose position is negative, at or
+ * past n_pos (rot > 0) or max_len, or on no page is padding: nothing of it is written.
+ * Two rows must not have the same place in the cache (sequences that share a page may not
+ * both write to it): which of them is stored is not defined.
+ * Limits: rot % 16 == 0, 0 <= rot <= D; 0 <= q_heads <= 1024; strides multiples of 8, at
+ * least a row's length.  q_out, the inputs and the cache must not overlap.
+ * Errors (nothing enqueued): INVALID_ARG for NULL or misaligned pointers (16 bytes; pages,
+ * lens, q_offsets 4) or bad sizes; UNSUPPORTED for another dtype, or a cache of another
+ * type than dtype and APMOE_E4M3.
+ */
+apmoe_status apmoe_kv_append(apmoe_ctx *ctx, const apmoe_kv_cache *cache, const apmoe_kv_batch *batch,
+                             const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                             const uint16_t *v, int64_t v_stride, int32_t dtype, int32_t q_heads, const float *rope,
+                             int32_t n_pos, int32_t rot, int32_t interleaved, uint16_t *q_out, void *stream);
+
+/* Device workspace bytes of either attention for this batch or a smaller one (fewer
+ * sequences, rows or tokens) on this cache.  Host only; pointers are not looked at. */
+apmoe_status apmoe_attn_workspace(apmoe_ctx *ctx, const apmoe_kv_cache *cache, const apmoe_kv_batch *batch,
+                                  int32_t q_heads, size_t *bytes);
+
+/*
+ * Attention of one new token of each sequence (q_offsets NULL, T = B) over its cache:
+ *   out[b][h] = sum_j softmax_j(scale * q[b][h] . k[j][h']) v[j][h'],
+ *   h' = h / (q_heads / kv_heads),
+ * over the tokens j <= p = lens[b] - 1 of the cache that are seen: all of them with
+ * window = 0; otherwise those with p - j < window or j < sinks.  The keys and values of
+ * token p itself have been appended before.
+ *   q [T][q_heads * D] of dtype, rows q_stride elements apart; dtype as the cache's, or
+ *   either type with an APMOE_E4M3 cache;
+ *   out [T][q_heads * D] of dtype or NULL; out8 e4m3 [T][q_heads * D] and out_scale fp32
+ *   [T][q_heads * D / 128] (the rows that apmoe_gemm_fp8 takes), both NULL or both set, with
+ *   head_dim 128 or 256.  At least one of out, out8 (T > 0).
+ * Scores, statistics and sums are fp32; the probabilities (with an APMOE_E4M3 cache, times
+ * the values' scales) go into the second product as two 16-bit numbers, to 2^-16 of each.  A row that sees nothing, or nothing but scores of -infinity, is zeros.  What lies
+ * in the cache where a row sees nothing does not matter, NaN and infinities included.
+ * ws: caller-owned device memory of at least apmoe_attn_workspace bytes, 256-byte aligned;
+ * calls (or captured graphs) that may run at the same time need one each.  Long caches are
+ * split over workgroups and joined in a second launch, in an order that depends on the
+ * batch's lengths only: repeated calls give identical bits.
+ * Limits: 1 <= q_heads <= 1024, a multiple of kv_heads; scale finite; 0 <= window <= 2^30,
+ * 0 <= sinks; q_stride a multiple of 8, at least q_heads * D.  The call enqueues only kernel
+ * launches on `stream` and can be captured.  Errors as apmoe_kv_append (out_scale 4 bytes),
+ * UNSUPPORTED also for out8 with head_dim 64.
+ */
+apmoe_status apmoe_attn_decode(apmoe_ctx *ctx, const apmoe_kv_cache *cache, const apmoe_kv_batch *batch,
+                               const uint16_t *q, int64_t q_stride, int32_t dtype, int32_t q_heads, float scale,
+                               int32_t window, int32_t sinks, void *ws, size_t ws_bytes, uint16_t *out, uint8_t *out8,
+                               float *out_scale, void *stream);
+
+/*
+ * Attention of the new tokens of prompts, or of chunks of prompts, over the cache: the same
+ * for every row, p being the row's position, so a row sees the cached tokens, the rows
+ * before it and itself.  All rows' keys and values have been appended before.
+ * The probabilities go into the second product rounded to one 16-bit number of the cache's
+ * type (bf16 with an APMOE_E4M3 cache; with fp16 queries on such a cache as two): 2^-8 or
+ * 2^-11 of each.  Rows with a negative position (more rows than lens[b]) are zeros.
+ * Arguments, limits and errors as apmoe_attn_decode, with or without q_offsets.
+ */
+apmoe_status apmoe_attn_prefill(apmoe_ctx *ctx, const apmoe_kv_cache *cache, const apmoe_kv_batch *batch,
+                                const uint16_t *q, int64_t q_stride, int32_t dtype, int32_t q_heads, float scale,
+                                int32_t window, int32_t sinks, void *ws, size_t ws_bytes, uint16_t *out, uint8_t *out8,
+                                float *out_scale, void *stream);
 
 #ifdef __cplusplus
 }
