@@ -19,6 +19,8 @@ constexpr int kWaves = 4;
 constexpr int kRows = 32 * kWaves;  // rows of a workgroup
 constexpr int kStep = 64;           // cached tokens of a step
 constexpr uint32_t kGridX = 1u << 22;
+constexpr float kSlack = 8.0f;
+constexpr int kAhead = 4;  // operands read ahead of their product
 
 __device__ inline int new_tokens(const AttnBatch &S, int b)
 {
@@ -34,14 +36,17 @@ struct Prefill {
     static constexpr int kBytes = kStep * D * 2;  // of a step's keys, and of its values
     static constexpr int kScales = C8 ? 2 * kStep * 4 : 0;
     static constexpr int kLds = 2 * kBytes + kScales;
+    static constexpr int kBuffers = 2;
 };
 
 // One granule (16 bytes of LDS) of values: the non-finite ones become 0, and their signs go
 // into two operands: 1 where a value is +infinity or a NaN, 1 where -infinity or a NaN.
+// Whether there are any.
 template <int DT>
-__device__ inline void split_values(u32x4 &v, u32x4 &plus, u32x4 &minus)
+__device__ inline bool split_values(u32x4 &v, u32x4 &plus, u32x4 &minus)
 {
     constexpr uint32_t kInf = DT == APMOE_F16 ? 0x7C00u : 0x7F80u, kOne = DT == APMOE_F16 ? 0x3C00u : 0x3F80u;
+    bool any = false;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         uint32_t keep = 0, p = 0, n = 0;
@@ -49,6 +54,7 @@ __device__ inline void split_values(u32x4 &v, u32x4 &plus, u32x4 &minus)
         for (int h = 0; h < 2; ++h) {
             const uint32_t x = v[i] >> (16 * h) & 0xFFFFu, a = x & 0x7FFFu;
             const bool bad = a >= kInf, nan = a > kInf, neg = x >> 15;
+            any |= bad;
             keep |= bad ? 0u : x << (16 * h);
             p |= bad && (nan || !neg) ? kOne << (16 * h) : 0u;
             n |= bad && (nan || neg) ? kOne << (16 * h) : 0u;
@@ -57,35 +63,123 @@ __device__ inline void split_values(u32x4 &v, u32x4 &plus, u32x4 &minus)
         plus[i] = p;
         minus[i] = n;
     }
-}
-
-template <int DT>
-__device__ inline bool not_finite(const u32x4 &v)
-{
-    constexpr uint32_t kInf = DT == APMOE_F16 ? 0x7C00u : 0x7F80u;
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        bad |= (v[i] & kInf) == kInf || (v[i] >> 16 & kInf) == kInf;
-    return bad;
+    return any;
 }
 
 __device__ inline u32x4 lds16(const char *base, int at) { return *reinterpret_cast<const u32x4 *>(base + at); }
 
+// Copies between global memory and LDS of one step: the cache's bytes go there without
+// passing registers; an 8-bit cache's pass through them to become 16-bit operands.
 template <int QT, bool C8, int D>
-__global__ void __launch_bounds__(kWaves *kWave) prefill_kernel(const AttnParams P)
+struct Stage {
+    using C = Prefill<QT, C8, D>;
+    static constexpr int kThreads = kWaves * kWave;
+    static constexpr int kPieces = kTile * D / 16 / kThreads > 0 ? kTile * D / 16 / kThreads : 1;  // 16 e4m3 bytes each
+    const KvView &kv;
+    int tid, wave, kvh;
+    // a step's two V tiles of 32 tokens: their pages' bases and places
+    bool here[2];
+    size_t base[2], at[2];
+    u32x4 k8[C8 ? 2 * kPieces : 1], v8[C8 ? 2 * kPieces : 1];
+    float sc[2];
+
+    __device__ inline void locate(const int32_t *table, int step, int end_tok)
+    {
+        const int tshift = kv.page_shift - 5;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int tt = 2 * step + u;
+            const int id = tt * kTile < end_tok ? table[tt >> tshift] : -1;
+            here[u] = id >= 0 && id < kv.n_pages;
+            base[u] = (size_t)(here[u] ? id : 0) * kv.Hkv + kvh;
+            at[u] = (size_t)(tt & ((1 << tshift) - 1)) * kTile;
+        }
+    }
+    // Sends the requests of the located step; `to` is its buffer.
+    __device__ inline void fetch(char *to)
+    {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const size_t tile = (base[u] << kv.page_shift) * D + at[u] * D;
+            if constexpr (C8) {
+                const char *k = static_cast<const char *>(kv.k) + tile, *v = static_cast<const char *>(kv.v) + tile;
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) {
+                    const int piece = tid + i * kThreads;
+                    if (kTile * D / 16 >= kThreads || piece < kTile * D / 16) {
+                        k8[u * kPieces + i] = *reinterpret_cast<const u32x4 *>(k + piece * 16);
+                        v8[u * kPieces + i] = *reinterpret_cast<const u32x4 *>(v + piece * 16);
+                    }
+                }
+                if (tid < 2 * kTile)
+                    sc[u] = (tid < kTile ? kv.ks : kv.vs)[(base[u] << kv.page_shift) + at[u] + tid % kTile];
+            } else {
+                const char *k = static_cast<const char *>(kv.k) + tile * 2, *v = static_cast<const char *>(kv.v) + tile * 2;
+#pragma unroll
+                for (int i = 0; i < kTile * D / 8 / kThreads; ++i) {
+                    const int off = (i * kWaves + wave) * 1024;
+                    char *dst = to + u * (C::kBytes / 2) + off;
+                    __builtin_amdgcn_global_load_lds(
+                        (const __attribute__((address_space(1))) void *)(uintptr_t)(k + off + tid % kWave * 16),
+                        (__attribute__((address_space(3))) void *)dst, 16, 0, 0);
+                    __builtin_amdgcn_global_load_lds(
+                        (const __attribute__((address_space(1))) void *)(uintptr_t)(v + off + tid % kWave * 16),
+                        (__attribute__((address_space(3))) void *)(dst + C::kBytes), 16, 0, 0);
+                }
+            }
+        }
+    }
+    // Writes what fetch left in registers.
+    __device__ inline void put(char *to) const
+    {
+        if constexpr (C8) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) {
+                    const int piece = tid + i * kThreads;
+                    if (kTile * D / 16 < kThreads && piece >= kTile * D / 16)
+                        continue;
+                    // 16 columns of one token: chunks 2 c and 2 c + 1 of its row
+                    const int a = piece / D, ch = piece % D / 16, t = piece % 16;
+                    char *tk = to + u * (C::kBytes / 2) + a * 16 * D * 2 + (ch * 2 * 16 + t) * 16;
+                    const u32x4 &w = k8[u * kPieces + i], &x = v8[u * kPieces + i];
+                    *reinterpret_cast<u32x4 *>(tk) = from_e4m3x8<QT>(w[0], w[1]);
+                    *reinterpret_cast<u32x4 *>(tk + 256) = from_e4m3x8<QT>(w[2], w[3]);
+                    char *tv = to + C::kBytes + u * (C::kBytes / 2) + piece * 32;
+                    *reinterpret_cast<u32x4 *>(tv) = from_e4m3x8<C::kVT>(x[0], x[1]);
+                    *reinterpret_cast<u32x4 *>(tv + 16) = from_e4m3x8<C::kVT>(x[2], x[3]);
+                }
+                if (tid < 2 * kTile)
+                    reinterpret_cast<float *>(to + 2 * C::kBytes)[tid / kTile * kStep + u * kTile + tid % kTile] = sc[u];
+            }
+        }
+    }
+};
+
+// The larger of x here and in the lane with the other half of the same column.
+__device__ inline float both_halves_max(float x)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x), false,
+                                                    false);
+    const uint32_t lo = r[0], hi = r[1];  // a bit cast of a vector's element reads element 0
+    return fmaxf(__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi));
+}
+
+template <int QT, bool C8, int D>
+__global__ void __launch_bounds__(kWaves *kWave, D <= 128 ? 2 : 1) prefill_kernel(const AttnParams P)
 {
     using C = Prefill<QT, C8, D>;
     constexpr int VT = C::kVT, KS = D / 16, DB = D / 32;
-    __shared__ __attribute__((aligned(16))) char lds[C::kLds];
-    char *const k_lds = lds, *const v_lds = lds + C::kBytes;
-    float *const ks_lds = reinterpret_cast<float *>(lds + 2 * C::kBytes), *const vs_lds = ks_lds + kStep;
+    __shared__ __attribute__((aligned(16))) char lds[C::kBuffers * C::kLds];
 
     const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-    const int G = P.Hq / P.kv.Hkv, kvh = blockIdx.y;
-    const uint32_t block = blockIdx.z * kGridX + blockIdx.x;
+    // heads are neighbours in the grid: workgroups b with the same b % 8 run on one XCD, and
+    // with 8 heads each XCD's L2 then has one head's keys and values
+    const uint32_t block = blockIdx.y * kGridX + blockIdx.x;
+    const int G = P.Hq / P.kv.Hkv, kvh = (int)(block % (uint32_t)P.kv.Hkv);
     int b, rt, n_rt;
-    if (block > 0x7FFFFFFFu || !find_item(P.s.B, (int)block, [&](int i) {
+    if (!find_item(P.s.B, (int)(block / (uint32_t)P.kv.Hkv), [&](int i) {
             return (int)(((int64_t)new_tokens(P.s, i) * G + kRows - 1) / kRows);
         }, b, rt, n_rt))
         return;
@@ -111,188 +205,185 @@ __global__ void __launch_bounds__(kWaves *kWave) prefill_kernel(const AttnParams
     const int first = P.window ? max(0, lo - P.window + 1) / kStep : 0;
     const int sink = P.window ? min(min(first, end), (int)(((int64_t)P.sinks + kStep - 1) / kStep)) : 0;
     const int steps = sink + max(0, end - first);
+    auto step_of = [&](int st) { return st < sink ? st : first + st - sink; };
 
+    // a negative scale is the queries' sign, and 0 a number too small to matter: c > 0 keeps
+    // the order of the scores, so the maximum is that of the unscaled ones
     u32x4 q[KS];
     {
         const uint16_t *row = P.q + (size_t)(live ? token : 0) * P.q_stride + (size_t)qh * D + 8 * h;
+        const uint32_t sign = P.scale < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
         for (int s = 0; s < KS; ++s)
-            q[s] = *reinterpret_cast<const u32x4 *>(row + 16 * s);
+            q[s] = *reinterpret_cast<const u32x4 *>(row + 16 * s) ^ sign;
     }
-    const float c = P.scale * kLog2e;
-    const int shift = P.kv.page_shift, tshift = shift - 5;
+    const float c = fmaxf(__builtin_fabsf(P.scale) * kLog2e, 0x1p-126f);
     const int32_t *table = P.s.pages + (size_t)b * P.s.max_pages;
 
     float m = -INFINITY, l = 0.0f;
     float16v o[DB] = {};
 
+    Stage<QT, C8, D> stage{P.kv, tid, wave, kvh};
+    if (steps > 0) {
+        stage.locate(table, step_of(0), end_tok);
+        stage.fetch(lds);
+        stage.put(lds);
+    }
     for (int st = 0; st < steps; ++st) {
-        const int step = st < sink ? st : first + st - sink;
-        bool here[2];
-        size_t base[2], at[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int tt = 2 * step + u;
-            const int id = tt * kTile < end_tok ? table[tt >> tshift] : -1;
-            here[u] = id >= 0 && id < P.kv.n_pages;
-            base[u] = (size_t)(here[u] ? id : 0) * P.kv.Hkv + kvh;
-            at[u] = (size_t)(tt & ((1 << tshift) - 1)) * kTile;
-        }
-        __syncthreads();  // the last step's operands have been read
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const size_t tile = (base[u] << shift) * D + at[u] * D;
-            constexpr int kHalf = C::kBytes / 2;
-            if constexpr (C8) {
-                const char *k = static_cast<const char *>(P.kv.k) + tile;
-                const char *v = static_cast<const char *>(P.kv.v) + tile;
-                for (int i = tid; i < kTile * D / 16; i += kWaves * kWave) {
-                    // 16 columns of one token: chunks 2 c and 2 c + 1
-                    const u32x4 w = *reinterpret_cast<const u32x4 *>(k + i * 16);
-                    const int a = i / D, ch = i % D / 16, t = i % 16;
-                    char *to = k_lds + u * kHalf + a * 16 * D * 2 + (ch * 2 * 16 + t) * 16;
-                    *reinterpret_cast<u32x4 *>(to) = from_e4m3x8<QT>(w[0], w[1]);
-                    *reinterpret_cast<u32x4 *>(to + 256) = from_e4m3x8<QT>(w[2], w[3]);
-                    const u32x4 x = *reinterpret_cast<const u32x4 *>(v + i * 16);
-                    char *tv = v_lds + u * kHalf + i * 32;
-                    *reinterpret_cast<u32x4 *>(tv) = from_e4m3x8<VT>(x[0], x[1]);
-                    *reinterpret_cast<u32x4 *>(tv + 16) = from_e4m3x8<VT>(x[2], x[3]);
-                }
-                if (tid < kTile) {
-                    const size_t sc = (base[u] << shift) + at[u] + tid;
-                    ks_lds[u * kTile + tid] = P.kv.ks[sc];
-                    vs_lds[u * kTile + tid] = P.kv.vs[sc];
-                }
-            } else {
-                const char *k = static_cast<const char *>(P.kv.k) + tile * 2;
-                const char *v = static_cast<const char *>(P.kv.v) + tile * 2;
-                for (int i = tid; i < kTile * D / 8; i += kWaves * kWave) {
-                    *reinterpret_cast<u32x4 *>(k_lds + u * kHalf + i * 16) = *reinterpret_cast<const u32x4 *>(k + i * 16);
-                    *reinterpret_cast<u32x4 *>(v_lds + u * kHalf + i * 16) = *reinterpret_cast<const u32x4 *>(v + i * 16);
-                }
-            }
-        }
+        const char *const k_lds = lds + st % C::kBuffers * C::kLds, *const v_lds = k_lds + C::kBytes;
+        const float *const ks_lds = reinterpret_cast<const float *>(k_lds + 2 * C::kBytes), *const vs_lds = ks_lds + kStep;
+        char *const next = lds + (st + 1) % C::kBuffers * C::kLds;
+        const bool here = stage.here[0] && stage.here[1];
+        const bool half_here[2] = {stage.here[0], stage.here[1]};
+        // this step's copies have landed, everyone's, and the other buffer has been read
+        __builtin_amdgcn_s_waitcnt(wait_vm<0>());
         __syncthreads();
-        const int tok0 = step * kStep, last = tok0 + kStep - 1;
-        if (tok0 > wave_hi)
-            continue;
-        const bool whole = here[0] && here[1] && last <= wave_lo && last < end_tok &&
-                           (!P.window || wave_hi - tok0 < P.window || last < P.sinks);
-        float16v s[2];
-        const int key_row = ((col >> 3) & 1) * 16 * D * 2 + ((col >> 4) * 8 + (col & 7)) * 16;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            s[u] = float16v{};
-#pragma unroll
-            for (int j = 0; j < KS; ++j)
-                s[u] = mfma32(QT, lds16(k_lds, u * (C::kBytes / 2) + key_row + (2 * j + h) * 256), q[j], s[u]);
+        if (st + 1 < steps) {
+            stage.locate(table, step_of(st + 1), end_tok);
+            stage.fetch(next);
         }
-        // score 16 u + 8 t + 4 a + b: token 32 u + 16 a + 8 t + 4 h + b
-        auto token_at = [&](int i) { return i / 16 * 32 + i % 8 / 4 * 16 + i % 16 / 8 * 8 + 4 * h + i % 4; };
-        uint32_t seen = 0xFFFFFFFFu;
-        if (!whole) {
-            seen = 0;
+        const int tok0 = step_of(st) * kStep, last = tok0 + kStep - 1;
+        if (tok0 <= wave_hi) {
+            const bool whole = here && last <= wave_lo && last < end_tok &&
+                               (!P.window || wave_hi - tok0 < P.window || last < P.sinks);
+            float16v s[2] = {};
+            const int key_row = ((col >> 3) & 1) * 16 * D * 2 + ((col >> 4) * 8 + (col & 7)) * 16 + h * 256;
+            auto key = [&](int n) { return lds16(k_lds, n % 2 * (C::kBytes / 2) + key_row + n / 2 * 512); };
+            {
+                u32x4 ring[kAhead];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const int tok = tok0 + token_at(i);
-                const bool in = here[i / 16] && tok < end_tok && tok <= pos &&
-                                (!P.window || pos - tok < P.window || tok < P.sinks);
-                seen |= in ? 1u << i : 0u;
-            }
-        }
-        float top = -INFINITY;
+                for (int n = 0; n < kAhead; ++n)
+                    ring[n] = key(n);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            float x = s[i / 16][i % 16] * c;
-            if constexpr (C8)
-                x *= ks_lds[token_at(i)];
-            if (!whole && !(seen >> i & 1))
-                x = -INFINITY;
-            s[i / 16][i % 16] = x;
-            top = fmaxf(top, x);
-        }
-        top = fmaxf(top, __shfl_xor(top, 32, kWave));
-        if (__any(top > m)) {
-            const float to = fmaxf(m, top);
-            const float f = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - to);
-            m = to;
-            l *= f;
-#pragma unroll
-            for (int d = 0; d < DB; ++d)
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    o[d][j] *= f;
-        }
-        const float zero = m == -INFINITY ? 0.0f : m;
-        u32x4 p[4], p2[C::kTwo ? 4 : 1];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float y[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int n = 2 * i + e;
-                y[e] = __builtin_amdgcn_exp2f(s[n / 16][n % 16] - zero);
-                l += y[e];
-                if constexpr (C8) {
-                    y[e] *= vs_lds[token_at(n)];
-                    if (!whole && !(seen >> n & 1))
-                        y[e] = 0.0f;  // whatever scale lies there
+                for (int n = 0; n < 2 * KS; ++n) {
+                    s[n % 2] = mfma32(QT, ring[n % kAhead], q[n / 2], s[n % 2]);
+                    if (n + kAhead < 2 * KS)
+                        ring[n % kAhead] = key(n + kAhead);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
-            const uint32_t w = pack2<VT>(y[0], y[1]);
-            p[i / 4][i % 4] = w;
-            if constexpr (C::kTwo)
-                p2[i / 4][i % 4] = pack2<VT>(y[0] - low16<VT>(w), y[1] - high16<VT>(w));
-        }
-        const int value_at = (h * D + col) * 16;
-        bool bad = false;
-        if (!whole) {
+            // score 16 u + 8 t + 4 a + b: token 32 u + 16 a + 8 t + 4 h + b
+            auto token_at = [&](int i) { return i / 16 * 32 + i % 8 / 4 * 16 + i % 16 / 8 * 8 + 4 * h + i % 4; };
+            if constexpr (C8)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+                for (int i = 0; i < 32; ++i)
+                    s[i / 16][i % 16] *= ks_lds[token_at(i)];
+            uint32_t seen = 0xFFFFFFFFu;
+            if (!whole) {
+                seen = 0;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const int tok = tok0 + token_at(i);
+                    const bool in = half_here[i / 16] && tok < end_tok && tok <= pos &&
+                                    (!P.window || pos - tok < P.window || tok < P.sinks);
+                    seen |= in ? 1u << i : 0u;
+                    s[i / 16][i % 16] = in ? s[i / 16][i % 16] : -INFINITY;
+                }
+            }
+            float top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                top = fmaxf(top, s[i / 16][i % 16]);
+            top = both_halves_max(top) * c;
+            // The sums are taken to a new maximum only when it is 2^8 times the old one's:
+            // probabilities up to 2^8 are as exact, and the sums have room.
+            if (__any(top > m + kSlack)) {
+                const float to = fmaxf(m, top);
+                const float f = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+                m = to;
+                l *= f;
 #pragma unroll
                 for (int d = 0; d < DB; ++d)
-                    bad |= not_finite<VT>(lds16(v_lds, value_at + (2 * j * D + 32 * d) * 16));
-            bad = __any(bad);
-        }
-        if (!bad) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < 16; ++j)
+                        o[d][j] *= f;
+            }
+            const float zero = m == -INFINITY ? 0.0f : -m;
+            u32x4 p[4], p2[C::kTwo ? 4 : 1];
 #pragma unroll
-                for (int d = 0; d < DB; ++d) {
-                    const u32x4 v = lds16(v_lds, value_at + (2 * j * D + 32 * d) * 16);
-                    o[d] = mfma32(VT, v, p[j], o[d]);
-                    if constexpr (C::kTwo)
-                        o[d] = mfma32(VT, v, p2[j], o[d]);
+            for (int i = 0; i < 16; ++i) {
+                float y[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int n = 2 * i + e;
+                    y[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n / 16][n % 16], c, zero));
+                    l += y[e];
+                    if constexpr (C8)
+                        y[e] *= vs_lds[token_at(n)];
                 }
-        } else {
-            // A value that is not finite reaches the rows that see it and no others: the
-            // product takes 0 for it, and counts of such values that a row sees say
-            // which of its sums become infinite.
-            u32x4 ones[4];
+                if constexpr (C8)
+                    if (!whole) {  // whatever scale lies there
+                        y[0] = seen >> (2 * i) & 1 ? y[0] : 0.0f;
+                        y[1] = seen >> (2 * i + 1) & 1 ? y[1] : 0.0f;
+                    }
+                const uint32_t w = pack2<VT>(y[0], y[1]);
+                p[i / 4][i % 4] = w;
+                if constexpr (C::kTwo)
+                    p2[i / 4][i % 4] = pack2<VT>(y[0] - low16<VT>(w), y[1] - high16<VT>(w));
+            }
+            const int value_at = (h * D + col) * 16;
+            auto value = [&](int n) { return lds16(v_lds, value_at + (n / DB * 2 * D + n % DB * 32) * 16); };
+            __builtin_amdgcn_sched_barrier(0);
+            if (whole) {
+                u32x4 ring[kAhead];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                ones[i / 4][i % 4] = (seen >> (2 * i) & 1 ? (VT == APMOE_F16 ? 0x3C00u : 0x3F80u) : 0u) |
-                                     (seen >> (2 * i + 1) & 1 ? (VT == APMOE_F16 ? 0x3C000000u : 0x3F800000u) : 0u);
+                for (int n = 0; n < kAhead; ++n)
+                    ring[n] = value(n);
 #pragma unroll
-            for (int d = 0; d < DB; ++d) {
-                float16v plus = {}, minus = {};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    u32x4 v = lds16(v_lds, value_at + (2 * j * D + 32 * d) * 16), a, z;
-                    split_values<VT>(v, a, z);
-                    o[d] = mfma32(VT, v, p[j], o[d]);
+                for (int n = 0; n < 4 * DB; ++n) {
+                    o[n % DB] = mfma32(VT, ring[n % kAhead], p[n / DB], o[n % DB]);
                     if constexpr (C::kTwo)
-                        o[d] = mfma32(VT, v, p2[j], o[d]);
-                    plus = mfma32(VT, a, ones[j], plus);
-                    minus = mfma32(VT, z, ones[j], minus);
+                        o[n % DB] = mfma32(VT, ring[n % kAhead], p2[n / DB], o[n % DB]);
+                    if (n + kAhead < 4 * DB)
+                        ring[n % kAhead] = value(n + kAhead);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
+            } else {
+                // A value that is not finite reaches the rows that see it and no others: the
+                // product takes 0 for it, and counts of such values that a row sees say
+                // which of its sums become infinite.
+                bool bad = false;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    o[d][j] += plus[j] > 0.0f ? INFINITY : 0.0f;
-                    o[d][j] += minus[j] > 0.0f ? -INFINITY : 0.0f;
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int d = 0; d < DB; ++d) {
+                        u32x4 v = lds16(v_lds, value_at + (2 * j * D + 32 * d) * 16), plus, minus;
+                        bad |= split_values<VT>(v, plus, minus);
+                        o[d] = mfma32(VT, v, p[j], o[d]);
+                        if constexpr (C::kTwo)
+                            o[d] = mfma32(VT, v, p2[j], o[d]);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                if (__any(bad)) {
+                    asm volatile("" ::: "memory");  // the operands are read anew
+                    constexpr uint32_t kOne = VT == APMOE_F16 ? 0x3C00u : 0x3F80u;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        u32x4 ones;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            ones[i] = (seen >> (8 * j + 2 * i) & 1 ? kOne : 0u) |
+                                      (seen >> (8 * j + 2 * i + 1) & 1 ? kOne << 16 : 0u);
+#pragma unroll
+                        for (int d = 0; d < DB; ++d) {
+                            u32x4 v = lds16(v_lds, value_at + (2 * j * D + 32 * d) * 16), plus, minus;
+                            split_values<VT>(v, plus, minus);
+                            const float16v a = mfma32(VT, plus, ones, float16v{});
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                o[d][i] += a[i] > 0.0f ? INFINITY : 0.0f;
+                            const float16v z = mfma32(VT, minus, ones, float16v{});
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                o[d][i] += z[i] > 0.0f ? -INFINITY : 0.0f;
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                    }
                 }
             }
         }
+        if (st + 1 < steps)
+            stage.put(next);
     }
     l += __shfl_xor(l, 32, kWave);
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // nothing seen: zeros
@@ -343,9 +434,9 @@ hipError_t prefill_launch(const AttnParams &P, hipStream_t s)
     const int G = P.Hq / P.kv.Hkv;
     // each sequence's last tile may be smaller
     const int64_t all = (int64_t)P.s.T * G, most = all / kRows + P.s.B;
-    const uint32_t tiles = (uint32_t)(most < all ? most : all);
+    const int64_t blocks = (most < all ? most : all) * P.kv.Hkv;  // below 2^35 / kRows
     hipLaunchKernelGGL((prefill_kernel<QT, C8, D>),
-                       dim3(tiles < kGridX ? tiles : kGridX, P.kv.Hkv, (tiles + kGridX - 1) / kGridX),
+                       dim3((uint32_t)(blocks < kGridX ? blocks : kGridX), (uint32_t)((blocks + kGridX - 1) / kGridX)),
                        dim3(kWaves * kWave), 0, s, P);
     return hipGetLastError();
 }
