@@ -36,17 +36,14 @@ struct Prefill {
     static constexpr int kBytes = kStep * D * 2;  // of a step's keys, and of its values
     static constexpr int kScales = C8 ? 2 * kStep * 4 : 0;
     static constexpr int kLds = 2 * kBytes + kScales;
-    static constexpr int kBuffers = 2;
 };
 
 // One granule (16 bytes of LDS) of values: the non-finite ones become 0, and their signs go
 // into two operands: 1 where a value is +infinity or a NaN, 1 where -infinity or a NaN.
-// Whether there are any.
 template <int DT>
-__device__ inline bool split_values(u32x4 &v, u32x4 &plus, u32x4 &minus)
+__device__ inline void split_values(u32x4 &v, u32x4 &plus, u32x4 &minus)
 {
     constexpr uint32_t kInf = DT == APMOE_F16 ? 0x7C00u : 0x7F80u, kOne = DT == APMOE_F16 ? 0x3C00u : 0x3F80u;
-    bool any = false;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         uint32_t keep = 0, p = 0, n = 0;
@@ -54,7 +51,6 @@ __device__ inline bool split_values(u32x4 &v, u32x4 &plus, u32x4 &minus)
         for (int h = 0; h < 2; ++h) {
             const uint32_t x = v[i] >> (16 * h) & 0xFFFFu, a = x & 0x7FFFu;
             const bool bad = a >= kInf, nan = a > kInf, neg = x >> 15;
-            any |= bad;
             keep |= bad ? 0u : x << (16 * h);
             p |= bad && (nan || !neg) ? kOne << (16 * h) : 0u;
             n |= bad && (nan || neg) ? kOne << (16 * h) : 0u;
@@ -63,7 +59,17 @@ __device__ inline bool split_values(u32x4 &v, u32x4 &plus, u32x4 &minus)
         plus[i] = p;
         minus[i] = n;
     }
-    return any;
+}
+
+template <int DT>
+__device__ inline bool not_finite(const u32x4 &v)
+{
+    constexpr uint32_t kInf = DT == APMOE_F16 ? 0x7C00u : 0x7F80u;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        bad |= (v[i] & kInf) == kInf || (v[i] >> 16 & kInf) == kInf;
+    return bad;
 }
 
 __device__ inline u32x4 lds16(const char *base, int at) { return *reinterpret_cast<const u32x4 *>(base + at); }
@@ -77,22 +83,32 @@ struct Stage {
     static constexpr int kPieces = kTile * D / 16 / kThreads > 0 ? kTile * D / 16 / kThreads : 1;  // 16 e4m3 bytes each
     const KvView &kv;
     int tid, wave, kvh;
+    int ids[2];
     // a step's two V tiles of 32 tokens: their pages' bases and places
     bool here[2];
     size_t base[2], at[2];
     u32x4 k8[C8 ? 2 * kPieces : 1], v8[C8 ? 2 * kPieces : 1];
     float sc[2];
 
-    __device__ inline void locate(const int32_t *table, int step, int end_tok)
+    // Lane i gets the pages of the i-th of 64 steps from st on.
+    template <class StepOf>
+    __device__ inline void load_ids(const int32_t *table, int st, int steps, const StepOf &step_of, int end_tok)
     {
-        const int tshift = kv.page_shift - 5;
+        const int mine = st + tid % kWave;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const int tt = 2 * step + u;
-            const int id = tt * kTile < end_tok ? table[tt >> tshift] : -1;
+            const int tt = 2 * step_of(mine) + u;
+            ids[u] = mine < steps && tt * kTile < end_tok ? table[tt >> (kv.page_shift - 5)] : -1;
+        }
+    }
+    __device__ inline void locate(int st, int step)
+    {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int id = __builtin_amdgcn_readlane(ids[u], st % kWave);
             here[u] = id >= 0 && id < kv.n_pages;
             base[u] = (size_t)(here[u] ? id : 0) * kv.Hkv + kvh;
-            at[u] = (size_t)(tt & ((1 << tshift) - 1)) * kTile;
+            at[u] = (size_t)((2 * step + u) & ((1 << (kv.page_shift - 5)) - 1)) * kTile;
         }
     }
     // Sends the requests of the located step; `to` is its buffer.
@@ -171,7 +187,7 @@ __global__ void __launch_bounds__(kWaves *kWave, D <= 128 ? 2 : 1) prefill_kerne
 {
     using C = Prefill<QT, C8, D>;
     constexpr int VT = C::kVT, KS = D / 16, DB = D / 32;
-    __shared__ __attribute__((aligned(16))) char lds[C::kBuffers * C::kLds];
+    __shared__ __attribute__((aligned(16))) char lds[2 * C::kLds];
 
     const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     // heads are neighbours in the grid: workgroups b with the same b % 8 run on one XCD, and
@@ -225,165 +241,206 @@ __global__ void __launch_bounds__(kWaves *kWave, D <= 128 ? 2 : 1) prefill_kerne
 
     Stage<QT, C8, D> stage{P.kv, tid, wave, kvh};
     if (steps > 0) {
-        stage.locate(table, step_of(0), end_tok);
+        stage.load_ids(table, 0, steps, step_of, end_tok);
+        stage.locate(0, step_of(0));
         stage.fetch(lds);
         stage.put(lds);
     }
-    for (int st = 0; st < steps; ++st) {
-        const char *const k_lds = lds + st % C::kBuffers * C::kLds, *const v_lds = k_lds + C::kBytes;
-        const float *const ks_lds = reinterpret_cast<const float *>(k_lds + 2 * C::kBytes), *const vs_lds = ks_lds + kStep;
-        char *const next = lds + (st + 1) % C::kBuffers * C::kLds;
-        const bool here = stage.here[0] && stage.here[1];
-        const bool half_here[2] = {stage.here[0], stage.here[1]};
+    const int key_at = ((col >> 3) & 1) * 16 * D * 2 + ((col >> 4) * 8 + (col & 7)) * 16 + h * 256;
+    const int value_at = (h * D + col) * 16;
+    // score 16 u + 8 t + 4 a + b: token 32 u + 16 a + 8 t + 4 h + b
+    auto token_at = [&](int i) { return i / 16 * 32 + i % 8 / 4 * 16 + i % 16 / 8 * 8 + 4 * h + i % 4; };
+    const char *k_lds = nullptr, *v_lds = nullptr;
+    bool here[2];
+    int tok0 = 0;
+
+    // Step st's operands are in LDS after this, and the next ones on their way.
+    auto open = [&](int st) {
+        k_lds = lds + st % 2 * C::kLds;
+        v_lds = k_lds + C::kBytes;
+        tok0 = step_of(st) * kStep;
+        here[0] = stage.here[0];
+        here[1] = stage.here[1];
         // this step's copies have landed, everyone's, and the other buffer has been read
         __builtin_amdgcn_s_waitcnt(wait_vm<0>());
         __syncthreads();
         if (st + 1 < steps) {
-            stage.locate(table, step_of(st + 1), end_tok);
-            stage.fetch(next);
+            if ((st + 1) % kWave == 0)
+                stage.load_ids(table, st + 1, steps, step_of, end_tok);
+            stage.locate(st + 1, step_of(st + 1));
+            stage.fetch(lds + (st + 1) % 2 * C::kLds);
         }
-        const int tok0 = step_of(st) * kStep, last = tok0 + kStep - 1;
-        if (tok0 <= wave_hi) {
-            const bool whole = here && last <= wave_lo && last < end_tok &&
-                               (!P.window || wave_hi - tok0 < P.window || last < P.sinks);
-            float16v s[2] = {};
-            const int key_row = ((col >> 3) & 1) * 16 * D * 2 + ((col >> 4) * 8 + (col & 7)) * 16 + h * 256;
-            auto key = [&](int n) { return lds16(k_lds, n % 2 * (C::kBytes / 2) + key_row + n / 2 * 512); };
-            {
-                u32x4 ring[kAhead];
+    };
+    // whether rows at positions lo .. hi all see the whole step
+    auto whole_for = [&](int lo, int hi) {
+        const int last = tok0 + kStep - 1;
+        return here[0] && here[1] && last <= lo && last < end_tok &&
+               (!P.window || hi - tok0 < P.window || last < P.sinks);
+    };
+    auto body = [&](auto slow_) {
+        constexpr bool kSlow = decltype(slow_)::value;
+        float16v s[2] = {};
+        {
+            auto key = [&](int n) { return lds16(k_lds, n % 2 * (C::kBytes / 2) + key_at + n / 2 * 512); };
+            u32x4 ring[kAhead];
 #pragma unroll
-                for (int n = 0; n < kAhead; ++n)
-                    ring[n] = key(n);
+            for (int n = 0; n < kAhead; ++n)
+                ring[n] = key(n);
 #pragma unroll
-                for (int n = 0; n < 2 * KS; ++n) {
-                    s[n % 2] = mfma32(QT, ring[n % kAhead], q[n / 2], s[n % 2]);
-                    if (n + kAhead < 2 * KS)
-                        ring[n % kAhead] = key(n + kAhead);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
+            for (int n = 0; n < 2 * KS; ++n) {
+                s[n % 2] = mfma32(QT, ring[n % kAhead], q[n / 2], s[n % 2]);
+                if (n + kAhead < 2 * KS)
+                    ring[n % kAhead] = key(n + kAhead);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            // score 16 u + 8 t + 4 a + b: token 32 u + 16 a + 8 t + 4 h + b
-            auto token_at = [&](int i) { return i / 16 * 32 + i % 8 / 4 * 16 + i % 16 / 8 * 8 + 4 * h + i % 4; };
-            if constexpr (C8)
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    s[i / 16][i % 16] *= ks_lds[token_at(i)];
-            uint32_t seen = 0xFFFFFFFFu;
-            if (!whole) {
-                seen = 0;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const int tok = tok0 + token_at(i);
-                    const bool in = half_here[i / 16] && tok < end_tok && tok <= pos &&
-                                    (!P.window || pos - tok < P.window || tok < P.sinks);
-                    seen |= in ? 1u << i : 0u;
-                    s[i / 16][i % 16] = in ? s[i / 16][i % 16] : -INFINITY;
-                }
-            }
-            float top = -INFINITY;
+        }
+        const float *const ks_lds = reinterpret_cast<const float *>(k_lds + 2 * C::kBytes), *const vs_lds = ks_lds + kStep;
+        if constexpr (C8)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-                top = fmaxf(top, s[i / 16][i % 16]);
-            top = both_halves_max(top) * c;
-            // The sums are taken to a new maximum only when it is 2^8 times the old one's:
-            // probabilities up to 2^8 are as exact, and the sums have room.
-            if (__any(top > m + kSlack)) {
-                const float to = fmaxf(m, top);
-                const float f = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - to);
-                m = to;
-                l *= f;
+                s[i / 16][i % 16] *= ks_lds[token_at(i)];
+        const bool whole = whole_for(wave_lo, wave_hi);
+        uint32_t seen = 0xFFFFFFFFu;
+        if (!whole) {
+            seen = 0;
 #pragma unroll
-                for (int d = 0; d < DB; ++d)
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        o[d][j] *= f;
-            }
-            const float zero = m == -INFINITY ? 0.0f : -m;
-            u32x4 p[4], p2[C::kTwo ? 4 : 1];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float y[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int n = 2 * i + e;
-                    y[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n / 16][n % 16], c, zero));
-                    l += y[e];
-                    if constexpr (C8)
-                        y[e] *= vs_lds[token_at(n)];
-                }
-                if constexpr (C8)
-                    if (!whole) {  // whatever scale lies there
-                        y[0] = seen >> (2 * i) & 1 ? y[0] : 0.0f;
-                        y[1] = seen >> (2 * i + 1) & 1 ? y[1] : 0.0f;
-                    }
-                const uint32_t w = pack2<VT>(y[0], y[1]);
-                p[i / 4][i % 4] = w;
-                if constexpr (C::kTwo)
-                    p2[i / 4][i % 4] = pack2<VT>(y[0] - low16<VT>(w), y[1] - high16<VT>(w));
-            }
-            const int value_at = (h * D + col) * 16;
-            auto value = [&](int n) { return lds16(v_lds, value_at + (n / DB * 2 * D + n % DB * 32) * 16); };
-            __builtin_amdgcn_sched_barrier(0);
-            if (whole) {
-                u32x4 ring[kAhead];
-#pragma unroll
-                for (int n = 0; n < kAhead; ++n)
-                    ring[n] = value(n);
-#pragma unroll
-                for (int n = 0; n < 4 * DB; ++n) {
-                    o[n % DB] = mfma32(VT, ring[n % kAhead], p[n / DB], o[n % DB]);
-                    if constexpr (C::kTwo)
-                        o[n % DB] = mfma32(VT, ring[n % kAhead], p2[n / DB], o[n % DB]);
-                    if (n + kAhead < 4 * DB)
-                        ring[n % kAhead] = value(n + kAhead);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-            } else {
-                // A value that is not finite reaches the rows that see it and no others: the
-                // product takes 0 for it, and counts of such values that a row sees say
-                // which of its sums become infinite.
-                bool bad = false;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int d = 0; d < DB; ++d) {
-                        u32x4 v = lds16(v_lds, value_at + (2 * j * D + 32 * d) * 16), plus, minus;
-                        bad |= split_values<VT>(v, plus, minus);
-                        o[d] = mfma32(VT, v, p[j], o[d]);
-                        if constexpr (C::kTwo)
-                            o[d] = mfma32(VT, v, p2[j], o[d]);
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
-                if (__any(bad)) {
-                    asm volatile("" ::: "memory");  // the operands are read anew
-                    constexpr uint32_t kOne = VT == APMOE_F16 ? 0x3C00u : 0x3F80u;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        u32x4 ones;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            ones[i] = (seen >> (8 * j + 2 * i) & 1 ? kOne : 0u) |
-                                      (seen >> (8 * j + 2 * i + 1) & 1 ? kOne << 16 : 0u);
-#pragma unroll
-                        for (int d = 0; d < DB; ++d) {
-                            u32x4 v = lds16(v_lds, value_at + (2 * j * D + 32 * d) * 16), plus, minus;
-                            split_values<VT>(v, plus, minus);
-                            const float16v a = mfma32(VT, plus, ones, float16v{});
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                o[d][i] += a[i] > 0.0f ? INFINITY : 0.0f;
-                            const float16v z = mfma32(VT, minus, ones, float16v{});
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                o[d][i] += z[i] > 0.0f ? -INFINITY : 0.0f;
-                            __builtin_amdgcn_sched_barrier(0);
-                        }
-                    }
-                }
+            for (int i = 0; i < 32; ++i) {
+                const int tok = tok0 + token_at(i);
+                const bool in = here[i / 16] && tok < end_tok && tok <= pos &&
+                                (!P.window || pos - tok < P.window || tok < P.sinks);
+                seen |= in ? 1u << i : 0u;
+                s[i / 16][i % 16] = in ? s[i / 16][i % 16] : -INFINITY;
             }
         }
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            top = fmaxf(top, s[i / 16][i % 16]);
+        top = both_halves_max(top) * c;
+        // The sums are taken to a new maximum only when it is 2^8 times the old one's:
+        // probabilities up to 2^8 are as exact, and the sums have room.
+        if (__any(top > m + kSlack)) {
+            const float to = fmaxf(m, top);
+            const float f = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+            m = to;
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    o[d][j] *= f;
+        }
+        const float zero = m == -INFINITY ? 0.0f : -m;
+        // Word i of the probabilities: scores 2 i and 2 i + 1; four words are an operand.
+        uint32_t p[2][4], p2[2][4];
+        auto word = [&](int i) {
+            float y[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int n = 2 * i + e;
+                y[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n / 16][n % 16], c, zero));
+                l += y[e];
+                if constexpr (C8) {
+                    y[e] *= vs_lds[token_at(n)];
+                    if (!(seen >> n & 1))
+                        y[e] = 0.0f;  // whatever scale lies there
+                }
+            }
+            const uint32_t w = pack2<VT>(y[0], y[1]);
+            p[i / 4 % 2][i % 4] = w;
+            if constexpr (C::kTwo)
+                p2[i / 4 % 2][i % 4] = pack2<VT>(y[0] - low16<VT>(w), y[1] - high16<VT>(w));
+        };
+        auto operand = [](const uint32_t(&w)[4]) { return u32x4{w[0], w[1], w[2], w[3]}; };
+        auto value = [&](int n) { return lds16(v_lds, value_at + (n / DB * 2 * D + n % DB * 32) * 16); };
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            word(i);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (!kSlow) {
+            u32x4 ring[kAhead];
+#pragma unroll
+            for (int n = 0; n < kAhead; ++n)
+                ring[n] = value(n);
+#pragma unroll
+            for (int n = 0; n < 4 * DB; ++n) {
+                const int j = n / DB, d = n % DB;
+                o[d] = mfma32(VT, ring[n % kAhead], operand(p[j % 2]), o[d]);
+                if constexpr (C::kTwo)
+                    o[d] = mfma32(VT, ring[n % kAhead], operand(p2[j % 2]), o[d]);
+                if (n + kAhead < 4 * DB)
+                    ring[n % kAhead] = value(n + kAhead);
+                // the next operand's words in the products' time
+                if (j < 3)
+#pragma unroll
+                    for (int i = 4 * d / DB; i < 4 * (d + 1) / DB; ++i)
+                        word(4 * (j + 1) + i);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        } else {
+            // A value that is not finite reaches the rows that see it and no others: the
+            // product takes 0 for it, and counts of such values that a row sees say which
+            // of its sums become infinite.
+            constexpr uint32_t kOne = VT == APMOE_F16 ? 0x3C00u : 0x3F80u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                u32x4 ones;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    ones[i] = (seen >> (8 * j + 2 * i) & 1 ? kOne : 0u) |
+                              (seen >> (8 * j + 2 * i + 1) & 1 ? kOne << 16 : 0u);
+#pragma unroll
+                for (int d = 0; d < DB; ++d) {
+                    u32x4 v = value(j * DB + d), plus, minus;
+                    split_values<VT>(v, plus, minus);
+                    o[d] = mfma32(VT, v, operand(p[j % 2]), o[d]);
+                    if constexpr (C::kTwo)
+                        o[d] = mfma32(VT, v, operand(p2[j % 2]), o[d]);
+                    const float16v a = mfma32(VT, plus, ones, float16v{});
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        o[d][i] += a[i] > 0.0f ? INFINITY : 0.0f;
+                    const float16v z = mfma32(VT, minus, ones, float16v{});
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        o[d][i] += z[i] > 0.0f ? -INFINITY : 0.0f;
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                if (j < 3)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        word(4 * (j + 1) + i);
+            }
+        }
+    };
+    auto close = [&](int st) {
         if (st + 1 < steps)
-            stage.put(next);
+            stage.put(lds + (st + 1) % 2 * C::kLds);
+    };
+
+    int st = 0;
+    for (; st < steps; ++st) {
+        open(st);
+        // Where not every row sees the whole step its values must be finite for the plain
+        // product: NaN and infinities times 0 are NaN.
+        if (!whole_for(lo, hi)) {
+            bool bad = false;
+            for (int i = tid; i < C::kBytes / 16; i += kWaves * kWave)
+                bad |= not_finite<VT>(lds16(v_lds, i * 16));
+            if (__syncthreads_or(bad))
+                break;
+        }
+        if (tok0 <= wave_hi)
+            body(std::false_type{});
+        close(st);
+    }
+    for (bool opened = true; st < steps; ++st) {
+        if (!opened)
+            open(st);
+        opened = false;
+        if (tok0 <= wave_hi)
+            body(std::true_type{});
+        close(st);
     }
     l += __shfl_xor(l, 32, kWave);
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // nothing seen: zeros
