@@ -1459,18 +1459,26 @@ apmoe::AttnBatch kv_batch(const apmoe_kv_cache *c, const apmoe_kv_batch *s)
 }
 
 struct WsLayoutAttn {
-    int slots;
     size_t part_o, part_ml, total;
 };
 
-WsLayoutAttn ws_layout_attn(const apmoe_kv_cache *c, int B, int q_heads)
+// `rows` parts of rows.
+WsLayoutAttn ws_layout_attn(size_t rows, int head_dim)
 {
     WsLayoutAttn L;
-    L.slots = apmoe::decode_slots(B, c->kv_heads, q_heads);
     L.part_o = 0;
-    L.part_ml = up256((size_t)L.slots * q_heads * c->head_dim * 4);
-    L.total = L.part_ml + up256((size_t)L.slots * q_heads * 8);
+    L.part_ml = up256(rows * head_dim * 4);
+    L.total = L.part_ml + up256(rows * 8);
     return L;
+}
+
+// Parts of rows that a call of either kind may need: a prefill call of fewer rows may be split
+// into more parts, up to a bound.
+size_t attn_part_rows(const apmoe_kv_cache *c, int B, int q_heads)
+{
+    const size_t decode = (size_t)apmoe::decode_slots(B, c->kv_heads, q_heads) * q_heads;
+    const size_t prefill = (size_t)apmoe::kPartBlocks * apmoe::kPartRows;
+    return decode > prefill ? decode : prefill;
 }
 
 // What the two attentions check alike, and their parameters.
@@ -1505,13 +1513,16 @@ apmoe_status attn_args(apmoe_ctx *ctx, const apmoe_kv_cache *cache, const apmoe_
         return s;
     if (!aligned16(out) || !aligned16(out8) || !aligned4(out_scale))
         return fail(APMOE_INVALID_ARG, "misaligned output (16 bytes; out_scale 4)");
-    const WsLayoutAttn L = ws_layout_attn(cache, batch->B, q_heads);
+    const WsLayoutAttn L = ws_layout_attn(attn_part_rows(cache, batch->B, q_heads), cache->head_dim);
     if (!ws || ws_bytes < L.total || ((uintptr_t)ws & 255u))
         return fail(APMOE_INVALID_ARG, "workspace NULL, unaligned or smaller than %zu bytes", L.total);
     char *w = reinterpret_cast<char *>(ws);
     *p = apmoe::AttnParams{kv_view(cache), kv_batch(cache, batch), q, q_stride, dtype, q_heads, scale, window, sinks,
                            out, out8, out_scale, reinterpret_cast<float *>(w + L.part_o),
-                           reinterpret_cast<float *>(w + L.part_ml), L.slots};
+                           reinterpret_cast<float *>(w + L.part_ml),
+                           apmoe::decode_slots(batch->B, cache->kv_heads, q_heads), 0, 1};
+    p->tiles = apmoe::prefill_tiles(batch->B, batch->T, q_heads / cache->kv_heads);
+    p->parts = apmoe::prefill_parts(p->tiles, cache->kv_heads, p->s.room);
     return ok();
 }
 
@@ -1569,7 +1580,7 @@ apmoe_status apmoe_attn_workspace(apmoe_ctx *ctx, const apmoe_kv_cache *cache, c
         s = attn_heads(cache, q_heads);
     if (s != APMOE_OK)
         return s;
-    *bytes = ws_layout_attn(cache, batch->B, q_heads).total;
+    *bytes = ws_layout_attn(attn_part_rows(cache, batch->B, q_heads), cache->head_dim).total;
     return ok();
 }
 

@@ -10,6 +10,8 @@
 // Rows of a key operand: row 16 t + 8 a + 4 h + b of a 32-token product is token 16 a + 8 t +
 // 4 h + b.  Lane half h then has, of scores 8t .. 8t+7, the tokens of granule g = 2 t + h of
 // V (attn.h), and the probabilities need not move.
+#include <algorithm>
+
 #include "attn.h"
 
 namespace apmoe {
@@ -17,10 +19,18 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kRows = 32 * kWaves;  // rows of a workgroup
+static_assert(kRows == kPartRows, "rows of a part");
 constexpr int kStep = 64;           // cached tokens of a step
 constexpr uint32_t kGridX = 1u << 22;
 constexpr float kSlack = 8.0f;
-constexpr int kAhead = 4;  // operands read ahead of their product
+// Calls of few row tiles are split over the steps: up to kSplitBlocks workgroups (of 256 CUs
+// that hold two) into parts of kPartSteps steps or more.  512 new tokens behind 32256, 32 heads
+// over 8: 796 -> 301 us, 4 of each of 16 sequences of 2700 to 8000 252 -> 93, 64 behind 4000
+// 93 -> 29; of 4 steps 316, 96 and 33, of 16 287, 93 and 37.  Not with more workgroups: 1000
+// behind 1000, 256 of them, 44.5 us and split in two 51.
+constexpr int kPartSteps = 8;
+constexpr int kSplitBlocks = 192;
+constexpr int kMaxParts = 64;
 
 __device__ inline int new_tokens(const AttnBatch &S, int b)
 {
@@ -34,8 +44,8 @@ struct Prefill {
     // bf16 numbers keep what fp16 would
     static constexpr bool kTwo = C8 && QT == APMOE_F16;
     static constexpr int kBytes = kStep * D * 2;  // of a step's keys, and of its values
-    static constexpr int kScales = C8 ? 2 * kStep * 4 : 0;
-    static constexpr int kLds = 2 * kBytes + kScales;
+    static constexpr int kAhead = D == 64 || C8 ? 3 : 4;  // operands read ahead of their product (registers)
+    static constexpr int kBuffer = kBytes + (C8 ? kStep * 4 : 0);  // with their scales
 };
 
 // One granule (16 bytes of LDS) of values: the non-finite ones become 0, and their signs go
@@ -74,101 +84,103 @@ __device__ inline bool not_finite(const u32x4 &v)
 
 __device__ inline u32x4 lds16(const char *base, int at) { return *reinterpret_cast<const u32x4 *>(base + at); }
 
-// Copies between global memory and LDS of one step: the cache's bytes go there without
-// passing registers; an 8-bit cache's pass through them to become 16-bit operands.
+// Copies between global memory and LDS: the cache's bytes go there without passing
+// registers; an 8-bit cache's pass through them to become 16-bit operands.
 template <int QT, bool C8, int D>
 struct Stage {
     using C = Prefill<QT, C8, D>;
     static constexpr int kThreads = kWaves * kWave;
-    static constexpr int kPieces = kTile * D / 16 / kThreads > 0 ? kTile * D / 16 / kThreads : 1;  // 16 e4m3 bytes each
+    static constexpr int kTileBytes = kTile * D * (C8 ? 1 : 2);  // of 32 tokens' keys in the cache
+    static constexpr int kPieces = (kTileBytes / 16 + kThreads - 1) / kThreads;
+    static constexpr bool kAll = kTileBytes / 16 % kThreads == 0;
     const KvView &kv;
     int tid, wave, kvh;
-    int ids[2];
-    // a step's two V tiles of 32 tokens: their pages' bases and places
-    bool here[2];
-    size_t base[2], at[2];
-    u32x4 k8[C8 ? 2 * kPieces : 1], v8[C8 ? 2 * kPieces : 1];
-    float sc[2];
+    // Lane i has the places of the two tiles of 32 tokens of step base + i, in tokens of all
+    // heads; bit i of on[u]: tile u is on a page.
+    int base;
+    uint32_t lo[2], hi[2];
+    uint64_t on[2];
+    u32x4 held[C8 ? 2 * kPieces : 1];  // what fetch asked for last, of keys or of values
+    float held_scale;
 
-    // Lane i gets the pages of the i-th of 64 steps from st on.
-    template <class StepOf>
-    __device__ inline void load_ids(const int32_t *table, int st, int steps, const StepOf &step_of, int end_tok)
+    // The steps from st on; `step` is the lane's own.
+    __device__ inline void load_places(const int32_t *table, int st, int step, bool in, int end_tok)
     {
-        const int mine = st + tid % kWave;
+        base = st;
+        bool ok[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const int tt = 2 * step_of(mine) + u;
-            ids[u] = mine < steps && tt * kTile < end_tok ? table[tt >> (kv.page_shift - 5)] : -1;
+            const int tt = 2 * step + u, tshift = kv.page_shift - 5;
+            const int id = in && tt * kTile < end_tok ? table[tt >> tshift] : -1;
+            ok[u] = id >= 0 && id < kv.n_pages;
+            const size_t page = (size_t)(ok[u] ? id : 0) * kv.Hkv + kvh;
+            const size_t at = (page << kv.page_shift) + (size_t)(tt & ((1 << tshift) - 1)) * kTile;
+            lo[u] = (uint32_t)at;
+            hi[u] = (uint32_t)(at >> 32);
         }
+        on[0] = __ballot(ok[0]);
+        on[1] = __ballot(ok[1]);
     }
-    __device__ inline void locate(int st, int step)
+    __device__ inline bool here(int st, int u) const { return on[u] >> (st - base) & 1; }
+    __device__ inline bool here(int st) const { return (on[0] & on[1]) >> (st - base) & 1; }
+    __device__ inline bool knows(int st) const { return st - base < kWave; }
+    __device__ inline size_t place(int st, int u) const
     {
+        return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)hi[u], st - base) << 32 |
+               (uint32_t)__builtin_amdgcn_readlane((int)lo[u], st - base);
+    }
+    // Sends the requests for the keys (or values) at these places to buffer `to`.
+    template <bool V>
+    __device__ inline void fetch(const size_t (&at)[2], char *to)
+    {
+        const char *const src = static_cast<const char *>(V ? kv.v : kv.k);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const int id = __builtin_amdgcn_readlane(ids[u], st % kWave);
-            here[u] = id >= 0 && id < kv.n_pages;
-            base[u] = (size_t)(here[u] ? id : 0) * kv.Hkv + kvh;
-            at[u] = (size_t)((2 * step + u) & ((1 << (kv.page_shift - 5)) - 1)) * kTile;
-        }
-    }
-    // Sends the requests of the located step; `to` is its buffer.
-    __device__ inline void fetch(char *to)
-    {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const size_t tile = (base[u] << kv.page_shift) * D + at[u] * D;
+            const char *const p = src + at[u] * (D * (C8 ? 1 : 2));
             if constexpr (C8) {
-                const char *k = static_cast<const char *>(kv.k) + tile, *v = static_cast<const char *>(kv.v) + tile;
 #pragma unroll
-                for (int i = 0; i < kPieces; ++i) {
-                    const int piece = tid + i * kThreads;
-                    if (kTile * D / 16 >= kThreads || piece < kTile * D / 16) {
-                        k8[u * kPieces + i] = *reinterpret_cast<const u32x4 *>(k + piece * 16);
-                        v8[u * kPieces + i] = *reinterpret_cast<const u32x4 *>(v + piece * 16);
-                    }
-                }
-                if (tid < 2 * kTile)
-                    sc[u] = (tid < kTile ? kv.ks : kv.vs)[(base[u] << kv.page_shift) + at[u] + tid % kTile];
+                for (int i = 0; i < kPieces; ++i)
+                    if (kAll || tid + i * kThreads < kTileBytes / 16)
+                        held[u * kPieces + i] = *reinterpret_cast<const u32x4 *>(p + (tid + i * kThreads) * 16);
+                if (tid / kTile == u)
+                    held_scale = (V ? kv.vs : kv.ks)[at[u] + tid % kTile];
             } else {
-                const char *k = static_cast<const char *>(kv.k) + tile * 2, *v = static_cast<const char *>(kv.v) + tile * 2;
+                constexpr int kMine = kTileBytes / kWaves;  // bytes of a wave
+                const __amdgpu_buffer_rsrc_t r = make_rsrc(p, kTileBytes);
+                char *const dst = to + u * (C::kBytes / 2) + wave * kMine;
 #pragma unroll
-                for (int i = 0; i < kTile * D / 8 / kThreads; ++i) {
-                    const int off = (i * kWaves + wave) * 1024;
-                    char *dst = to + u * (C::kBytes / 2) + off;
-                    __builtin_amdgcn_global_load_lds(
-                        (const __attribute__((address_space(1))) void *)(uintptr_t)(k + off + tid % kWave * 16),
-                        (__attribute__((address_space(3))) void *)dst, 16, 0, 0);
-                    __builtin_amdgcn_global_load_lds(
-                        (const __attribute__((address_space(1))) void *)(uintptr_t)(v + off + tid % kWave * 16),
-                        (__attribute__((address_space(3))) void *)(dst + C::kBytes), 16, 0, 0);
-                }
+                for (int i = 0; i < kMine / 1024; ++i)
+                    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)(dst + i * 1024),
+                                                             16, wave * kMine + tid % kWave * 16, i * 1024, 0, 0);
             }
         }
     }
     // Writes what fetch left in registers.
+    template <bool V>
     __device__ inline void put(char *to) const
     {
         if constexpr (C8) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int i = 0; i < kPieces; ++i) {
                     const int piece = tid + i * kThreads;
-                    if (kTile * D / 16 < kThreads && piece >= kTile * D / 16)
+                    if (!kAll && piece >= kTileBytes / 16)
                         continue;
-                    // 16 columns of one token: chunks 2 c and 2 c + 1 of its row
-                    const int a = piece / D, ch = piece % D / 16, t = piece % 16;
-                    char *tk = to + u * (C::kBytes / 2) + a * 16 * D * 2 + (ch * 2 * 16 + t) * 16;
-                    const u32x4 &w = k8[u * kPieces + i], &x = v8[u * kPieces + i];
-                    *reinterpret_cast<u32x4 *>(tk) = from_e4m3x8<QT>(w[0], w[1]);
-                    *reinterpret_cast<u32x4 *>(tk + 256) = from_e4m3x8<QT>(w[2], w[3]);
-                    char *tv = to + C::kBytes + u * (C::kBytes / 2) + piece * 32;
-                    *reinterpret_cast<u32x4 *>(tv) = from_e4m3x8<C::kVT>(x[0], x[1]);
-                    *reinterpret_cast<u32x4 *>(tv + 16) = from_e4m3x8<C::kVT>(x[2], x[3]);
+                    const u32x4 &w = held[u * kPieces + i];
+                    char *t = to + u * (C::kBytes / 2);
+                    if constexpr (V) {
+                        *reinterpret_cast<u32x4 *>(t + piece * 32) = from_e4m3x8<C::kVT>(w[0], w[1]);
+                        *reinterpret_cast<u32x4 *>(t + piece * 32 + 16) = from_e4m3x8<C::kVT>(w[2], w[3]);
+                    } else {
+                        // 16 columns of one token: chunks 2 c and 2 c + 1 of its row
+                        t += piece / D * 16 * D * 2 + (piece % D / 16 * 2 * 16 + piece % 16) * 16;
+                        *reinterpret_cast<u32x4 *>(t) = from_e4m3x8<QT>(w[0], w[1]);
+                        *reinterpret_cast<u32x4 *>(t + 256) = from_e4m3x8<QT>(w[2], w[3]);
+                    }
                 }
-                if (tid < 2 * kTile)
-                    reinterpret_cast<float *>(to + 2 * C::kBytes)[tid / kTile * kStep + u * kTile + tid % kTile] = sc[u];
-            }
+            if (tid < kStep)
+                reinterpret_cast<float *>(to + C::kBytes)[tid] = held_scale;
         }
     }
 };
@@ -182,46 +194,93 @@ __device__ inline float both_halves_max(float x)
     return fmaxf(__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi));
 }
 
+// Rows of a workgroup and the steps that they see.  Row i is query head (row0 + i) % G of new
+// token q0 + (row0 + i) / G of sequence b; rows past the last one stand for it.
+struct RowTile {
+    int b, len, nq, row_of_b, end_tok, q0, row0, last_row, lo, hi;
+    int first, sink, steps;  // [0, sink) and [first, first + steps - sink)
+    int parts, per;          // parts of `per` steps
+    int G;
+
+    __device__ inline int token(int i) const { return q0 + (int)((uint32_t)(row0 + i) / (uint32_t)G); }
+    __device__ inline int pos(int i) const { return len - nq + token(min(i, last_row)); }
+    __device__ inline int step(int st) const { return st < sink ? st : first + st - sink; }
+};
+
+__device__ inline bool row_tile(const AttnParams &P, uint32_t tile, RowTile &t)
+{
+    const int G = P.Hq / P.kv.Hkv;
+    int rt, n_rt;
+    if (!find_item(P.s.B, (int)tile, [&](int i) {
+            return (int)(((int64_t)new_tokens(P.s, i) * G + kRows - 1) / kRows);
+        }, t.b, rt, n_rt))
+        return false;
+    rt = n_rt - 1 - rt;  // the rows with the most to see first
+    t.G = G;
+    t.nq = new_tokens(P.s, t.b);
+    t.row_of_b = P.s.q_offsets ? P.s.q_offsets[t.b] : t.b;
+    t.len = P.s.lens[t.b];
+    t.end_tok = cached_tokens(P.s, t.len);
+    const int64_t r0 = (int64_t)rt * kRows;
+    t.q0 = (int)(r0 / G);
+    t.row0 = (int)(r0 - (int64_t)t.q0 * G);
+    t.last_row = (int)min((int64_t)kRows, (int64_t)t.nq * G - r0) - 1;
+    t.lo = t.pos(0);
+    t.hi = t.pos(kRows - 1);
+    const int end = (max(0, min(t.end_tok, t.hi + 1)) + kStep - 1) / kStep;
+    t.first = P.window ? max(0, t.lo - P.window + 1) / kStep : 0;
+    t.sink = P.window ? min(min(t.first, end), (int)(((int64_t)P.sinks + kStep - 1) / kStep)) : 0;
+    t.steps = t.sink + max(0, end - t.first);
+    const int most = min(P.parts, max(1, t.steps / kPartSteps));
+    t.per = (t.steps + most - 1) / most;
+    t.parts = t.steps > 0 ? (t.steps + t.per - 1) / t.per : 1;
+    return true;
+}
+
+// 4 columns from d on of a row, with the scale of their group of 128.
+template <int QT>
+__device__ inline void store_columns(const AttnParams &P, size_t row, int d, const float (&v)[4], float scale)
+{
+    const size_t at = row * P.kv.D + d;
+    if (P.out8) {
+        const float r = 1.0f / scale;
+        *reinterpret_cast<uint32_t *>(P.out8 + at) = to_e4m3x4(v[0] * r, v[1] * r, v[2] * r, v[3] * r);
+    }
+    if (P.out)
+        *reinterpret_cast<u32x2 *>(P.out + at) = u32x2{pack2<QT>(v[0], v[1]), pack2<QT>(v[2], v[3])};
+}
+
 template <int QT, bool C8, int D>
-__global__ void __launch_bounds__(kWaves *kWave, D <= 128 ? 2 : 1) prefill_kernel(const AttnParams P)
+__global__ void __launch_bounds__(kWaves *kWave, D == 64 && !C8 ? 3 : D <= 128 ? 2 : 1) prefill_kernel(const AttnParams P)
 {
     using C = Prefill<QT, C8, D>;
     constexpr int VT = C::kVT, KS = D / 16, DB = D / 32;
-    __shared__ __attribute__((aligned(16))) char lds[2 * C::kLds];
+    __shared__ __attribute__((aligned(16))) char lds[4 * C::kBuffer];
+    auto k_buf = [&](int st) { return lds + st % 2 * C::kBuffer; };
+    auto v_buf = [&](int st) { return lds + (2 + st % 2) * C::kBuffer; };
 
     const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     // heads are neighbours in the grid: workgroups b with the same b % 8 run on one XCD, and
     // with 8 heads each XCD's L2 then has one head's keys and values
-    const uint32_t block = blockIdx.y * kGridX + blockIdx.x;
-    const int G = P.Hq / P.kv.Hkv, kvh = (int)(block % (uint32_t)P.kv.Hkv);
-    int b, rt, n_rt;
-    if (!find_item(P.s.B, (int)(block / (uint32_t)P.kv.Hkv), [&](int i) {
-            return (int)(((int64_t)new_tokens(P.s, i) * G + kRows - 1) / kRows);
-        }, b, rt, n_rt))
+    const uint32_t block = blockIdx.y * kGridX + blockIdx.x, item = block / (uint32_t)P.kv.Hkv;
+    const int kvh = (int)(block - item * (uint32_t)P.kv.Hkv), part = (int)(item % (uint32_t)P.parts);
+    RowTile t;
+    if (!row_tile(P, item / (uint32_t)P.parts, t) || part >= t.parts)
         return;
-    rt = n_rt - 1 - rt;  // the rows with the most to see first
-    const int nq = new_tokens(P.s, b), row_of_b = P.s.q_offsets ? P.s.q_offsets[b] : b;
-    const int len = P.s.lens[b], end_tok = cached_tokens(P.s, len);
-    const int64_t rows = (int64_t)nq * G;
-    const int64_t r0 = (int64_t)rt * kRows;
+    const int end_tok = t.end_tok;
 
     // this lane's row (as a column of the products), and the positions of its wave's
     const int col = lane % 32, h = lane / 32;
-    const int64_t r = min(r0 + wave * 32 + col, rows - 1);
-    const int qi = (int)(r / G), qh = kvh * G + (int)(r % G);
-    const int64_t token = (int64_t)row_of_b + qi;
-    const bool live = r0 + wave * 32 + col < rows && token >= 0 && token < P.s.T;
-    const int pos = len - nq + qi;
-    auto pos_of = [&](int64_t row) { return len - nq + (int)(min(row, rows - 1) / G); };
-    const int wave_lo = pos_of(r0 + wave * 32), wave_hi = pos_of(r0 + wave * 32 + 31);
-    const int lo = pos_of(r0), hi = pos_of(r0 + kRows - 1);
+    const int mine = wave * 32 + col, last = min(mine, t.last_row), qi = t.token(last);
+    const int qh = kvh * t.G + t.row0 + last - (qi - t.q0) * t.G;
+    const int64_t token = (int64_t)t.row_of_b + qi;
+    const int pos = t.len - t.nq + qi;
+    const bool live = mine <= t.last_row && token >= 0 && token < P.s.T;
+    const int wave_lo = t.pos(wave * 32), wave_hi = t.pos(wave * 32 + 31);
 
-    // steps that a row of the workgroup sees: [0, sink) and [first, end)
-    const int end = (max(0, min(end_tok, hi + 1)) + kStep - 1) / kStep;
-    const int first = P.window ? max(0, lo - P.window + 1) / kStep : 0;
-    const int sink = P.window ? min(min(first, end), (int)(((int64_t)P.sinks + kStep - 1) / kStep)) : 0;
-    const int steps = sink + max(0, end - first);
-    auto step_of = [&](int st) { return st < sink ? st : first + st - sink; };
+    // the part's steps, counted from its first one
+    const int st0 = part * t.per, steps = min(t.steps - st0, t.per);
+    auto step_of = [&](int st) { return t.step(st0 + st); };
 
     // a negative scale is the queries' sign, and 0 a number too small to matter: c > 0 keeps
     // the order of the scores, so the maximum is that of the unscaled ones
@@ -234,91 +293,103 @@ __global__ void __launch_bounds__(kWaves *kWave, D <= 128 ? 2 : 1) prefill_kerne
             q[s] = *reinterpret_cast<const u32x4 *>(row + 16 * s) ^ sign;
     }
     const float c = fmaxf(__builtin_fabsf(P.scale) * kLog2e, 0x1p-126f);
-    const int32_t *table = P.s.pages + (size_t)b * P.s.max_pages;
+    const int32_t *table = P.s.pages + (size_t)t.b * P.s.max_pages;
 
-    float m = -INFINITY, l = 0.0f;
-    float16v o[DB] = {};
-
-    Stage<QT, C8, D> stage{P.kv, tid, wave, kvh};
-    if (steps > 0) {
-        stage.load_ids(table, 0, steps, step_of, end_tok);
-        stage.locate(0, step_of(0));
-        stage.fetch(lds);
-        stage.put(lds);
-    }
+    float m, l, top;
+    float16v o[DB], sa[2], sb[2];
     const int key_at = ((col >> 3) & 1) * 16 * D * 2 + ((col >> 4) * 8 + (col & 7)) * 16 + h * 256;
     const int value_at = (h * D + col) * 16;
     // score 16 u + 8 t + 4 a + b: token 32 u + 16 a + 8 t + 4 h + b
     auto token_at = [&](int i) { return i / 16 * 32 + i % 8 / 4 * 16 + i % 16 / 8 * 8 + 4 * h + i % 4; };
-    const char *k_lds = nullptr, *v_lds = nullptr;
-    bool here[2];
-    int tok0 = 0;
+    auto key = [&](const char *k, int n) { return lds16(k, n % 2 * (C::kBytes / 2) + key_at + n / 2 * 512); };
 
-    // Step st's operands are in LDS after this, and the next ones on their way.
-    auto open = [&](int st) {
-        k_lds = lds + st % 2 * C::kLds;
-        v_lds = k_lds + C::kBytes;
-        tok0 = step_of(st) * kStep;
-        here[0] = stage.here[0];
-        here[1] = stage.here[1];
-        // this step's copies have landed, everyone's, and the other buffer has been read
+    Stage<QT, C8, D> stage{P.kv, tid, wave, kvh};
+    auto load_places = [&](int st) __attribute__((always_inline)) {
+        stage.load_places(table, st, step_of(st + lane), st + lane < steps, end_tok);
+    };
+    auto turn = [] {  // copies have landed, everyone's, and what they replace next has been read
         __builtin_amdgcn_s_waitcnt(wait_vm<0>());
         __syncthreads();
-        if (st + 1 < steps) {
-            if ((st + 1) % kWave == 0)
-                stage.load_ids(table, st + 1, steps, step_of, end_tok);
-            stage.locate(st + 1, step_of(st + 1));
-            stage.fetch(lds + (st + 1) % 2 * C::kLds);
+    };
+    // Scores of a step whose keys are in LDS; `between(n)` runs in the time of product n.
+    auto scores = [&](float16v(&s)[2], const char *k, const auto &between) __attribute__((always_inline)) {
+        u32x4 ring[C::kAhead];
+#pragma unroll
+        for (int n = 0; n < C::kAhead; ++n)
+            ring[n] = key(k, n);
+#pragma unroll
+        for (int n = 0; n < 2 * KS; ++n) {
+            s[n % 2] = mfma32(QT, ring[n % C::kAhead], q[n / 2], n < 2 ? float16v{} : s[n % 2]);
+            if (n + C::kAhead < 2 * KS)
+                ring[n % C::kAhead] = key(k, n + C::kAhead);
+            between(n);
+            __builtin_amdgcn_sched_barrier(0);
         }
     };
-    // whether rows at positions lo .. hi all see the whole step
-    auto whole_for = [&](int lo, int hi) {
-        const int last = tok0 + kStep - 1;
-        return here[0] && here[1] && last <= lo && last < end_tok &&
-               (!P.window || hi - tok0 < P.window || last < P.sinks);
+    // An 8-bit cache's scales of scores 4 g .. 4 g + 3.
+    auto scales = [&](const char *buffer, int g) {
+        return *reinterpret_cast<const float4v *>(buffer + C::kBytes + token_at(4 * g) * 4);
     };
-    auto body = [&](auto slow_) {
-        constexpr bool kSlow = decltype(slow_)::value;
-        float16v s[2] = {};
-        {
-            auto key = [&](int n) { return lds16(k_lds, n % 2 * (C::kBytes / 2) + key_at + n / 2 * 512); };
-            u32x4 ring[kAhead];
-#pragma unroll
-            for (int n = 0; n < kAhead; ++n)
-                ring[n] = key(n);
-#pragma unroll
-            for (int n = 0; n < 2 * KS; ++n) {
-                s[n % 2] = mfma32(QT, ring[n % kAhead], q[n / 2], s[n % 2]);
-                if (n + kAhead < 2 * KS)
-                    ring[n % kAhead] = key(n + kAhead);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        }
-        const float *const ks_lds = reinterpret_cast<const float *>(k_lds + 2 * C::kBytes), *const vs_lds = ks_lds + kStep;
-        if constexpr (C8)
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                s[i / 16][i % 16] *= ks_lds[token_at(i)];
-        const bool whole = whole_for(wave_lo, wave_hi);
-        uint32_t seen = 0xFFFFFFFFu;
-        if (!whole) {
-            seen = 0;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const int tok = tok0 + token_at(i);
-                const bool in = here[i / 16] && tok < end_tok && tok <= pos &&
-                                (!P.window || pos - tok < P.window || tok < P.sinks);
-                seen |= in ? 1u << i : 0u;
-                s[i / 16][i % 16] = in ? s[i / 16][i % 16] : -INFINITY;
-            }
-        }
-        float top = -INFINITY;
+    auto top_of = [](const float16v(&s)[2]) __attribute__((always_inline)) {
+        float t = -INFINITY;
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-            top = fmaxf(top, s[i / 16][i % 16]);
+            t = fmaxf(t, s[i / 16][i % 16]);
+        return t;
+    };
+
+    // Steps that every row of the wave (or of the workgroup) sees whole, if their pages are
+    // there: those below `to`, from `from` on or below `sinks`.
+    struct Whole {
+        int to, from, sinks;
+        __device__ inline bool operator()(int st) const { return (st < to) & ((st >= from) | (st < sinks)); }
+    };
+    auto whole_of = [&](int least, int most) {
+        Whole w;
+        const int gap = t.sink - t.first, past = max(0, min(least + 1, end_tok)) / kStep;
+        w.to = past + gap;  // behind the sinks step = st - gap
+        w.from = P.window ? max(t.sink, (max(0, most - P.window + 1) + kStep - 1) / kStep + gap) : 0;
+        w.sinks = P.window ? min(min(P.sinks / kStep, t.sink), past) : 0;
+        if (w.to < t.sink)  // rows that end among the sinks
+            w.to = w.sinks;
+        w.to -= st0;
+        w.from -= st0;
+        w.sinks -= st0;
+        return w;
+    };
+    const Whole whole_wave = whole_of(wave_lo, wave_hi), whole_all = whole_of(t.lo, t.hi);
+    // What the rows see of step st.  Score i is of the token tok0 + token_at(i) = tok0 + 4 h + a
+    // number known here: seen if that number is below `below` and above `above` (the window)
+    // or below `sink_below`.
+    struct Sight {
+        int below[2], above, sink_below;
+    };
+    auto sight_of = [&](int st) __attribute__((always_inline)) {
+        Sight g;
+        const int at = step_of(st) * kStep + 4 * h;
+        const bool here0 = stage.here(st, 0), here1 = stage.here(st, 1);
+        const int past = min(pos + 1, end_tok) - at;
+        g.below[0] = here0 ? past : -1;
+        g.below[1] = here1 ? past : -1;
+        g.above = P.window ? pos - P.window - at : -kStep;
+        g.sink_below = P.sinks - at;
+        return g;
+    };
+    auto sees = [&](const Sight &g, int i) __attribute__((always_inline)) {
+        const int n = token_at(i) - 4 * h;
+        return (n < g.below[i / 16]) & ((n > g.above) | (n < g.sink_below));
+    };
+    auto mask = [&](const Sight &g, float16v(&s)[2]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            s[i / 16][i % 16] = sees(g, i) ? s[i / 16][i % 16] : -INFINITY;
+        top = top_of(s);
+    };
+    // The sums are taken to a new maximum only when it is 2^8 times the old one's:
+    // probabilities up to 2^8 are as exact, and the sums have room.
+    float zero;
+    auto rescale = [&]() __attribute__((always_inline)) {
         top = both_halves_max(top) * c;
-        // The sums are taken to a new maximum only when it is 2^8 times the old one's:
-        // probabilities up to 2^8 are as exact, and the sums have room.
         if (__any(top > m + kSlack)) {
             const float to = fmaxf(m, top);
             const float f = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - to);
@@ -330,72 +401,237 @@ __global__ void __launch_bounds__(kWaves *kWave, D <= 128 ? 2 : 1) prefill_kerne
                 for (int j = 0; j < 16; ++j)
                     o[d][j] *= f;
         }
-        const float zero = m == -INFINITY ? 0.0f : -m;
-        // Word i of the probabilities: scores 2 i and 2 i + 1; four words are an operand.
-        uint32_t p[2][4], p2[2][4];
-        auto word = [&](int i) {
-            float y[2];
+        zero = m == -INFINITY ? 0.0f : -m;
+    };
+    // Word i of the probabilities: scores 2 i and 2 i + 1; four words are an operand.  vq: an
+    // 8-bit cache's scales, those of the words after the next ones asked for here.
+    uint32_t p[16], p2[C::kTwo ? 16 : 1];
+    float4v vq[2];
+    auto word = [&](const float16v(&s)[2], const char *v, int i) __attribute__((always_inline)) {
+        float y[2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int n = 2 * i + e;
-                y[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n / 16][n % 16], c, zero));
-                l += y[e];
-                if constexpr (C8) {
-                    y[e] *= vs_lds[token_at(n)];
-                    if (!(seen >> n & 1))
-                        y[e] = 0.0f;  // whatever scale lies there
-                }
-            }
-            const uint32_t w = pack2<VT>(y[0], y[1]);
-            p[i / 4 % 2][i % 4] = w;
+        for (int e = 0; e < 2; ++e) {
+            const int n = 2 * i + e;
+            y[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n / 16][n % 16], c, zero));
+            l += y[e];
+            if constexpr (C8)  // 0 whatever the scale is, where nothing is seen
+                y[e] = y[e] == 0.0f ? 0.0f : y[e] * vq[n / 4 % 2][n % 4];
+        }
+        if constexpr (C8)
+            if (i % 2 == 1 && i < 13)
+                vq[i / 2 % 2] = scales(v, i / 2 + 2);
+        const uint32_t w = pack2<VT>(y[0], y[1]);
+        p[i] = w;
+        if constexpr (C::kTwo)
+            p2[i] = pack2<VT>(y[0] - low16<VT>(w), y[1] - high16<VT>(w));
+    };
+    auto first_scales = [&](const char *v) __attribute__((always_inline)) {
+        if constexpr (C8) {
+            vq[0] = scales(v, 0);
+            vq[1] = scales(v, 1);
+        }
+    };
+    auto operand = [](const auto &w, int j) __attribute__((always_inline)) {
+        return u32x4{w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]};
+    };
+    auto value = [&](const char *v, int n) { return lds16(v, value_at + (n / DB * 2 * D + n % DB * 32) * 16); };
+
+    // Step st: its values and the next one's keys are in LDS after open, the values behind them
+    // and the keys behind those on their way.  What passes registers is sent for and written
+    // one after the other: the values in the first half of the step, the keys in the second.
+    size_t at_k[2], at_v[2];  // of the keys and values sent for last
+    auto more_keys = [&](int st) __attribute__((always_inline)) {
+        if (st + 2 < steps) {
+            if (!stage.knows(st + 2))
+                load_places(st);
+            at_k[0] = stage.place(st + 2, 0);
+            at_k[1] = stage.place(st + 2, 1);
+            stage.template fetch<false>(at_k, k_buf(st));
+        }
+    };
+    auto open = [&](int st) __attribute__((always_inline)) {
+        turn();
+        at_v[0] = at_k[0];
+        at_v[1] = at_k[1];
+        if constexpr (!C8)
+            more_keys(st);
+        if (st + 1 < steps)
+            stage.template fetch<true>(at_v, v_buf(st + 1));
+    };
+    auto half = [&](int st) __attribute__((always_inline)) {
+        if constexpr (C8) {
+            if (st + 1 < steps)
+                stage.template put<true>(v_buf(st + 1));
+            more_keys(st);
+        }
+    };
+    auto close = [&](int st) __attribute__((always_inline)) {
+        if (st + 2 < steps)
+            stage.template put<false>(k_buf(st));
+    };
+    // One step: s has its scores, next gets those of the step behind it.
+    auto body = [&](int st, float16v(&s)[2], float16v(&next)[2]) __attribute__((always_inline)) {
+        const char *const v = v_buf(st), *const k = k_buf(st + 1);
+        if (!(whole_wave(st) && stage.here(st)))
+            mask(sight_of(st), s);
+        rescale();
+        first_scales(v);
+        // the first 12 words in the time of the next scores, the last 4 and the next maximum
+        // in that of the second product (the next scores of the last step are of keys that
+        // have been read before: nothing is done with them)
+        constexpr int kEarly = 12;
+        scores(next, k, [&](int n) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = n * kEarly / (2 * KS); i < (n + 1) * kEarly / (2 * KS); ++i)
+                word(s, v, i);
+        });
+        half(st);
+        __builtin_amdgcn_s_setprio(1);
+        u32x4 ring[C::kAhead];
+#pragma unroll
+        for (int n = 0; n < C::kAhead; ++n)
+            ring[n] = value(v, n);
+        float4v kq[2];
+        if constexpr (C8) {
+            kq[0] = scales(k, 0);
+            kq[1] = scales(k, 1);
+        }
+        top = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < 4 * DB; ++n) {
+            const int j = n / DB, d = n % DB;
+            o[d] = mfma32(VT, ring[n % C::kAhead], operand(p, j), o[d]);
             if constexpr (C::kTwo)
-                p2[i / 4 % 2][i % 4] = pack2<VT>(y[0] - low16<VT>(w), y[1] - high16<VT>(w));
-        };
-        auto operand = [](const uint32_t(&w)[4]) { return u32x4{w[0], w[1], w[2], w[3]}; };
-        auto value = [&](int n) { return lds16(v_lds, value_at + (n / DB * 2 * D + n % DB * 32) * 16); };
+                o[d] = mfma32(VT, ring[n % C::kAhead], operand(p2, j), o[d]);
+            if (n + C::kAhead < 4 * DB)
+                ring[n % C::kAhead] = value(v, n + C::kAhead);
+            if (j < 2)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            word(i);
-        __builtin_amdgcn_sched_barrier(0);
-        if constexpr (!kSlow) {
-            u32x4 ring[kAhead];
+                for (int i = n * (16 - kEarly) / (2 * DB); i < (n + 1) * (16 - kEarly) / (2 * DB); ++i)
+                    word(s, v, kEarly + i);
 #pragma unroll
-            for (int n = 0; n < kAhead; ++n)
-                ring[n] = value(n);
+            for (int g = n * 8 / (4 * DB); g < (n + 1) * 8 / (4 * DB); ++g) {
+                if constexpr (C8) {
 #pragma unroll
-            for (int n = 0; n < 4 * DB; ++n) {
-                const int j = n / DB, d = n % DB;
-                o[d] = mfma32(VT, ring[n % kAhead], operand(p[j % 2]), o[d]);
-                if constexpr (C::kTwo)
-                    o[d] = mfma32(VT, ring[n % kAhead], operand(p2[j % 2]), o[d]);
-                if (n + kAhead < 4 * DB)
-                    ring[n % kAhead] = value(n + kAhead);
-                // the next operand's words in the products' time
-                if (j < 3)
+                    for (int i = 0; i < 4; ++i)
+                        next[g / 4][4 * g % 16 + i] *= kq[g % 2][i];
+                    if (g < 6)
+                        kq[g % 2] = scales(k, g + 2);
+                }
 #pragma unroll
-                    for (int i = 4 * d / DB; i < 4 * (d + 1) / DB; ++i)
-                        word(4 * (j + 1) + i);
+                for (int i = 0; i < 4; ++i)
+                    top = fmaxf(top, next[g / 4][4 * g % 16 + i]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        __builtin_amdgcn_s_setprio(0);
+    };
+    // Where not every row sees the whole step its values must be finite for the plain
+    // product: NaN and infinities times 0 are NaN.
+    auto plain = [&](int st) __attribute__((always_inline)) {
+        if (whole_all(st) && stage.here(st))
+            return true;
+        bool bad = false;
+        for (int i = tid; i < C::kBytes / 16; i += kWaves * kWave)
+            bad |= not_finite<VT>(lds16(v_buf(st), i * 16));
+        return !__syncthreads_or(bad);
+    };
+
+    auto begin = [&]() __attribute__((always_inline)) {
+        m = -INFINITY;
+        l = 0.0f;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+            o[d] = float16v{};
+    };
+    auto all_scores = [&]() __attribute__((always_inline)) {
+        scores(sa, k_buf(0), [](int) {});
+        if constexpr (C8)
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+                const float4v f = scales(k_buf(0), g);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sa[g / 4][4 * g % 16 + i] *= f[i];
                 __builtin_amdgcn_sched_barrier(0);
             }
-        } else {
-            // A value that is not finite reaches the rows that see it and no others: the
-            // product takes 0 for it, and counts of such values that a row sees say which
-            // of its sums become infinite.
-            constexpr uint32_t kOne = VT == APMOE_F16 ? 0x3C00u : 0x3F80u;
+    };
+    begin();
+    int st = 0;
+    if (steps > 0) {
+        load_places(0);
+        at_k[0] = stage.place(0, 0);
+        at_k[1] = stage.place(0, 1);
+        stage.template fetch<false>(at_k, k_buf(0));
+        stage.template put<false>(k_buf(0));
+        stage.template fetch<true>(at_k, v_buf(0));
+        stage.template put<true>(v_buf(0));
+        if (steps > 1) {
+            at_k[0] = stage.place(1, 0);
+            at_k[1] = stage.place(1, 1);
+            stage.template fetch<false>(at_k, k_buf(1));
+            stage.template put<false>(k_buf(1));
+        }
+        turn();
+        all_scores();
+        top = top_of(sa);
+    }
+    // two steps a turn of the loop: the scores change places
+    while (st < steps) {
+        open(st);
+        if (!plain(st))
+            break;
+        body(st, sa, sb);
+        close(st);
+        if (++st == steps)
+            break;
+        open(st);
+        if (!plain(st))
+            break;
+        body(st, sb, sa);
+        close(st);
+        ++st;
+    }
+    if (st < steps) {
+        // All steps again, one after the other.  A value that is not finite reaches the rows
+        // that see it and no others: the product takes 0 for it, and counts of such values
+        // that a row sees say which of its sums become infinite.
+        constexpr uint32_t kOne = VT == APMOE_F16 ? 0x3C00u : 0x3F80u;
+        begin();
+        turn();
+        load_places(0);
+        for (st = 0; st < steps; ++st) {
+            if (!stage.knows(st))
+                load_places(st);
+            at_k[0] = stage.place(st, 0);
+            at_k[1] = stage.place(st, 1);
+            stage.template fetch<false>(at_k, k_buf(0));
+            stage.template put<false>(k_buf(0));
+            stage.template fetch<true>(at_k, v_buf(0));
+            stage.template put<true>(v_buf(0));
+            turn();
+            const char *const v = v_buf(0);
+            const Sight g = sight_of(st);
+            all_scores();
+            mask(g, sa);
+            rescale();
+            first_scales(v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                word(sa, v, i);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 u32x4 ones;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    ones[i] = (seen >> (8 * j + 2 * i) & 1 ? kOne : 0u) |
-                              (seen >> (8 * j + 2 * i + 1) & 1 ? kOne << 16 : 0u);
+                    ones[i] = (sees(g, 8 * j + 2 * i) ? kOne : 0u) | (sees(g, 8 * j + 2 * i + 1) ? kOne << 16 : 0u);
 #pragma unroll
                 for (int d = 0; d < DB; ++d) {
-                    u32x4 v = value(j * DB + d), plus, minus;
-                    split_values<VT>(v, plus, minus);
-                    o[d] = mfma32(VT, v, operand(p[j % 2]), o[d]);
+                    u32x4 x = value(v, j * DB + d), plus, minus;
+                    split_values<VT>(x, plus, minus);
+                    o[d] = mfma32(VT, x, operand(p, j), o[d]);
                     if constexpr (C::kTwo)
-                        o[d] = mfma32(VT, v, operand(p2[j % 2]), o[d]);
+                        o[d] = mfma32(VT, x, operand(p2, j), o[d]);
                     const float16v a = mfma32(VT, plus, ones, float16v{});
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
@@ -406,95 +642,124 @@ __global__ void __launch_bounds__(kWaves *kWave, D <= 128 ? 2 : 1) prefill_kerne
                         o[d][i] += z[i] > 0.0f ? -INFINITY : 0.0f;
                     __builtin_amdgcn_sched_barrier(0);
                 }
-                if (j < 3)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        word(4 * (j + 1) + i);
             }
+            turn();
         }
-    };
-    auto close = [&](int st) {
-        if (st + 1 < steps)
-            stage.put(lds + (st + 1) % 2 * C::kLds);
-    };
-
-    int st = 0;
-    for (; st < steps; ++st) {
-        open(st);
-        // Where not every row sees the whole step its values must be finite for the plain
-        // product: NaN and infinities times 0 are NaN.
-        if (!whole_for(lo, hi)) {
-            bool bad = false;
-            for (int i = tid; i < C::kBytes / 16; i += kWaves * kWave)
-                bad |= not_finite<VT>(lds16(v_lds, i * 16));
-            if (__syncthreads_or(bad))
-                break;
-        }
-        if (tok0 <= wave_hi)
-            body(std::false_type{});
-        close(st);
-    }
-    for (bool opened = true; st < steps; ++st) {
-        if (!opened)
-            open(st);
-        opened = false;
-        if (tok0 <= wave_hi)
-            body(std::true_type{});
-        close(st);
     }
     l += __shfl_xor(l, 32, kWave);
+    // columns 32 d + 8 j + 4 h .. + 3 of the row: o[d][4 j] .. + 3
+    if (t.parts > 1) {
+        const size_t slot = ((size_t)item * P.kv.Hkv + kvh) * kRows + mine;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<float4v *>(P.part_o + slot * D + 32 * d + 8 * j + 4 * h) =
+                    float4v{o[d][4 * j], o[d][4 * j + 1], o[d][4 * j + 2], o[d][4 * j + 3]};
+        if (h == 0) {
+            P.part_ml[2 * slot] = m;
+            P.part_ml[2 * slot + 1] = l;
+        }
+        return;
+    }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // nothing seen: zeros
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
         for (int j = 0; j < 16; ++j)
             o[d][j] *= inv;
-    // column 32 d + 8 (j / 4) + 4 h + j % 4 of the row
     const size_t row = (size_t)token * P.Hq + qh;
-    constexpr int kGroups = D < kBlk ? 1 : D / kBlk;
-    if (D >= kBlk && P.out8) {
+    constexpr int kGroups = D < kBlk ? 1 : D / kBlk, kBlocks = DB / kGroups;
 #pragma unroll
-        for (int n = 0; n < kGroups; ++n) {
+    for (int n = 0; n < kGroups; ++n) {
+        float scale = 1.0f;
+        if (D >= kBlk && P.out8) {
             uint32_t a = 0;
 #pragma unroll
-            for (int d = 0; d < DB / kGroups; ++d)
+            for (int d = 0; d < kBlocks; ++d)
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                    a = max(a, mag(o[n * (DB / kGroups) + d][j]));
+                    a = max(a, mag(o[n * kBlocks + d][j]));
             a = max(a, (uint32_t)__shfl_xor((int)a, 32, kWave));
-            const float sc = scale_of(a), r8 = 1.0f / sc;
+            scale = scale_of(a);
             if (live && h == 0)
-                P.out_scale[row * kGroups + n] = sc;
-            if (live)
-#pragma unroll
-                for (int d = 0; d < DB / kGroups; ++d)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float16v &x = o[n * (DB / kGroups) + d];
-                        *reinterpret_cast<uint32_t *>(P.out8 + row * D + 128 * n + 32 * d + 8 * j + 4 * h) = to_e4m3x4(
-                            x[4 * j] * r8, x[4 * j + 1] * r8, x[4 * j + 2] * r8, x[4 * j + 3] * r8);
-                    }
+                P.out_scale[row * kGroups + n] = scale;
         }
+        if (live)
+#pragma unroll
+            for (int d = n * kBlocks; d < (n + 1) * kBlocks; ++d)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float x[4] = {o[d][4 * j], o[d][4 * j + 1], o[d][4 * j + 2], o[d][4 * j + 3]};
+                    store_columns<QT>(P, row, 32 * d + 8 * j + 4 * h, x, scale);
+                }
     }
-    if (live && P.out)
+}
+
+// Joins the parts of the row tiles that are split: D / 4 threads a row, 256 a workgroup.
+template <int QT, int D>
+__global__ void __launch_bounds__(256) join_rows(const AttnParams P)
+{
+    constexpr int kLanes = D / 4, kGroupLanes = kBlk / 4;
+    RowTile t;
+    if (!row_tile(P, blockIdx.x, t) || t.parts <= 1)
+        return;
+    const int kvh = blockIdx.y, c = threadIdx.x % kLanes, i = blockIdx.z * (256 / kLanes) + threadIdx.x / kLanes;
+    if (i > t.last_row)
+        return;
+    const size_t slot0 = ((size_t)blockIdx.x * P.parts * P.kv.Hkv + kvh) * kRows + i;
+    const size_t step = (size_t)P.kv.Hkv * kRows;
+    float M = -INFINITY;
+    for (int n = 0; n < t.parts; ++n)
+        M = fmaxf(M, P.part_ml[2 * (slot0 + n * step)]);
+    float L = 0.0f, v[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int n = 0; n < t.parts; ++n) {
+        const size_t slot = slot0 + n * step;
+        const float m = P.part_ml[2 * slot];
+        const float4v o = *reinterpret_cast<const float4v *>(P.part_o + slot * D + 4 * c);
+        if (m == -INFINITY)  // the part saw nothing
+            continue;
+        const float f = __builtin_amdgcn_exp2f(m - M);
+        L += f * P.part_ml[2 * slot + 1];
 #pragma unroll
-        for (int d = 0; d < DB; ++d)
+        for (int j = 0; j < 4; ++j)
+            v[j] += f * o[j];
+    }
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    uint32_t a = 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<u32x2 *>(P.out + row * D + 32 * d + 8 * j + 4 * h) =
-                    u32x2{pack2<QT>(o[d][4 * j], o[d][4 * j + 1]), pack2<QT>(o[d][4 * j + 2], o[d][4 * j + 3])};
+    for (int j = 0; j < 4; ++j) {
+        v[j] *= inv;
+        a = max(a, mag(v[j]));
+    }
+    const int qi = t.token(i), qh = kvh * t.G + t.row0 + i - (qi - t.q0) * t.G;
+    const int64_t token = (int64_t)t.row_of_b + qi;
+    const bool live = token >= 0 && token < P.s.T;
+    const size_t row = (size_t)token * P.Hq + qh;
+    float scale = 1.0f;
+    if (D >= kBlk && P.out8) {
+#pragma unroll
+        for (int d = kGroupLanes / 2; d >= 1; d >>= 1)
+            a = max(a, (uint32_t)__shfl_xor((int)a, d, kWave));
+        scale = scale_of(a);
+        if (live && c % kGroupLanes == 0)
+            P.out_scale[row * (D / kBlk) + c / kGroupLanes] = scale;
+    }
+    if (live)
+        store_columns<QT>(P, row, 4 * c, v, scale);
 }
 
 template <int QT, bool C8, int D>
 hipError_t prefill_launch(const AttnParams &P, hipStream_t s)
 {
-    const int G = P.Hq / P.kv.Hkv;
-    // each sequence's last tile may be smaller
-    const int64_t all = (int64_t)P.s.T * G, most = all / kRows + P.s.B;
-    const int64_t blocks = (most < all ? most : all) * P.kv.Hkv;  // below 2^35 / kRows
+    const int64_t blocks = (int64_t)P.tiles * P.kv.Hkv * P.parts;  // below 2^36 / kRows
     hipLaunchKernelGGL((prefill_kernel<QT, C8, D>),
                        dim3((uint32_t)(blocks < kGridX ? blocks : kGridX), (uint32_t)((blocks + kGridX - 1) / kGridX)),
                        dim3(kWaves * kWave), 0, s, P);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || P.parts == 1)
+        return e;
+    hipLaunchKernelGGL((join_rows<QT, D>), dim3(P.tiles, P.kv.Hkv, kRows * D / 4 / 256), dim3(256), 0, s, P);
     return hipGetLastError();
 }
 
@@ -509,6 +774,21 @@ hipError_t prefill_dim(const AttnParams &P, hipStream_t s)
 }
 
 }  // namespace
+
+int prefill_tiles(int B, int T, int G)
+{
+    // each sequence's last tile may be smaller
+    const int64_t all = (int64_t)T * G, most = all / kRows + B;
+    return (int)(most < all ? most : all);
+}
+
+int prefill_parts(int tiles, int Hkv, int room)
+{
+    const int64_t blocks = (int64_t)tiles * Hkv;
+    if (blocks == 0 || blocks > kSplitBlocks || room < 2 * kPartSteps * kStep)
+        return 1;
+    return (int)std::min<int64_t>(kPartBlocks / blocks, kMaxParts);
+}
 
 hipError_t launch_attn_prefill(const AttnParams &P, hipStream_t s)
 {

@@ -46,15 +46,24 @@ struct AttnParams {
     uint16_t *out;      // NULL or out8 is
     uint8_t *out8;
     float *out_scale;
-    // decode: the parts of sequences that are split, [slots][Hq] of D sums, and of a maximum
-    // and a sum
+    // The parts of what is split: D sums a row, and a maximum and a sum.  decode: [slots][Hq];
+    // prefill: [tiles][parts][Hkv][kPartRows]
     float *part_o;
     float *part_ml;
     int slots;
+    int tiles, parts;
 };
+
+constexpr int kPartRows = 128;    // rows of a tile of prefill
+constexpr int kPartBlocks = 512;  // prefill splits no call into more workgroups than this
 
 // Slots of the parts of a decode call: one a sequence and as many again as fill the device.
 int decode_slots(int B, int Hkv, int Hq);
+
+// Row tiles of a prefill call with groups of G heads, an upper bound, and the parts that each
+// is split into.
+int prefill_tiles(int B, int T, int G);
+int prefill_parts(int tiles, int Hkv, int room);
 
 hipError_t launch_kv_append(const AppendParams &P, hipStream_t s);
 hipError_t launch_attn_decode(const AttnParams &P, hipStream_t s);
