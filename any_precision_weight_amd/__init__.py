@@ -410,10 +410,19 @@ def _arg(ctx: Context, t, name: str, n: int, types) -> int | None:
     return t.data_ptr()
 
 
+_raw_stream = None
+
+
 def _stream_of(ctx: Context, stream) -> int | None:
-    import torch
-    s = torch.cuda.current_stream(ctx.device) if stream is None else stream
-    return s.cuda_stream or None
+    global _raw_stream
+    if stream is not None:
+        return stream.cuda_stream or None
+    if _raw_stream is None:
+        import torch
+        # the handle alone, where torch has it: a Stream object costs as much as the rest of a small call
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
+    return _raw_stream(ctx.device) or None
 
 
 def _types(t, name: str):
@@ -585,21 +594,21 @@ class KvBatch:
 
 
 def _kv_on(ctx: Context, cache: KvCache, batch: KvBatch) -> None:
-    for name, o in (("cache", cache), ("batch", batch)):
-        if o.device != ctx.device:
-            raise ValueError(f"the {name} is on cuda:{o.device}, the context on cuda:{ctx.device}")
+    if cache.device != ctx.device or batch.device != ctx.device:
+        raise ValueError(f"the cache is on cuda:{cache.device}, the batch on cuda:{batch.device}, the context on "
+                         f"cuda:{ctx.device}")
 
 
 def _matrix(ctx: Context, t, name: str, T: int, width: int, types):
     """(pointer, stride) of a 2-dimensional tensor of at least T rows and `width` dense
     columns; rows may be apart."""
-    if t.dtype not in types or t.dim() != 2 or t.shape[0] < T or t.shape[1] != width or \
-            (width > 1 and t.stride(1) != 1):
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] < T or shape[1] != width or strides[1] != 1 or t.dtype not in types:
         raise ValueError(f"{name}: need [{T}][{width}] of {' / '.join(map(str, types))} with dense rows, got "
-                         f"{tuple(t.shape)} of {t.dtype}, strides {tuple(t.stride())}")
+                         f"{tuple(shape)} of {t.dtype}, strides {strides}")
     if t.get_device() != ctx.device:
         raise ValueError(f"{name} is on {t.device}, the context on cuda:{ctx.device}")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), width)
+    return t.data_ptr(), strides[0] if shape[0] > 1 else max(strides[0], width)
 
 
 def kv_append(ctx: Context, cache: KvCache, batch: KvBatch, q, k, v, q_heads: int, rope, rot: int, interleaved: bool,
@@ -609,19 +618,21 @@ def kv_append(ctx: Context, cache: KvCache, batch: KvBatch, q, k, v, q_heads: in
     q [T][q_heads * D], k, v [T][kv_heads * D], rows may be apart; q_out [T][q_heads * D].
     q and q_out None with q_heads 0."""
     _kv_on(ctx, cache, batch)
-    T, D, kw = batch.T, cache.head_dim, cache.kv_heads * cache.head_dim
+    T, D = batch.T, cache.head_dim
     dt, types = _types(k, "k")
-    qp = (None, 0) if q is None else _matrix(ctx, q, "q", T, q_heads * D, types)
-    kp, vp = _matrix(ctx, k, "k", T, kw, types), _matrix(ctx, v, "v", T, kw, types)
+    qp, qs = (None, 0) if q is None else _matrix(ctx, q, "q", T, q_heads * D, types)
+    kp, ks = _matrix(ctx, k, "k", T, cache.kv_heads * D, types)
+    vp, vs = _matrix(ctx, v, "v", T, cache.kv_heads * D, types)
     n_pos = 0
     if rope is not None:
         if rope.dim() != 2 or rope.shape[1] != rot:
             raise ValueError(f"rope: need [positions][{rot}], got {tuple(rope.shape)}")
         n_pos = rope.shape[0]
-    _check(ctx.L.apmoe_kv_append(ctx.handle, cache.ref, batch.ref, *qp, *kp, *vp, dt, q_heads,
-                                 _arg(ctx, rope, "rope", n_pos * rot, _f32), n_pos, rot, int(interleaved),
-                                 _arg(ctx, q_out, "q_out", T * q_heads * D, types), _stream_of(ctx, stream)),
-           "apmoe_kv_append", ctx.L)
+    st = ctx.L.apmoe_kv_append(ctx.handle, cache.ref, batch.ref, qp, qs, kp, ks, vp, vs, dt, q_heads,
+                               _arg(ctx, rope, "rope", n_pos * rot, _f32), n_pos, rot, 1 if interleaved else 0,
+                               _arg(ctx, q_out, "q_out", T * q_heads * D, types), _stream_of(ctx, stream))
+    if st:
+        _check(st, "apmoe_kv_append", ctx.L)
 
 
 def attn_workspace(ctx: Context, cache: KvCache, batch: KvBatch, q_heads: int) -> int:
@@ -631,18 +642,26 @@ def attn_workspace(ctx: Context, cache: KvCache, batch: KvBatch, q_heads: int) -
     return n.value
 
 
+_u8 = None
+
+
 def _attn(fn: str, ctx, cache, batch, q, q_heads, scale, window, sinks, ws, out, out8, out_scale, stream) -> None:
-    import torch
-    if not isinstance(ws, torch.Tensor):
+    global _u8
+    if _u8 is None:
+        import torch
+        _u8 = (torch.uint8,)
+    if not hasattr(ws, "data_ptr"):
         raise ValueError(f"ws: need a byte tensor, got {type(ws)}")
     _kv_on(ctx, cache, batch)
     dt, types = _types(q, "q")
     n = batch.T * q_heads * cache.head_dim
-    qp = _matrix(ctx, q, "q", batch.T, q_heads * cache.head_dim, types)
-    _check(getattr(ctx.L, fn)(ctx.handle, cache.ref, batch.ref, *qp, dt, q_heads, scale, window, sinks,
-                              _arg(ctx, ws, "ws", 0, (torch.uint8,)), ws.numel(), _arg(ctx, out, "out", n, types),
-                              _arg(ctx, out8, "out8", n, _e4m3_types),
-                              _arg(ctx, out_scale, "out_scale", n // 128, _f32), _stream_of(ctx, stream)), fn, ctx.L)
+    qp, qs = _matrix(ctx, q, "q", batch.T, q_heads * cache.head_dim, types)
+    st = getattr(ctx.L, fn)(ctx.handle, cache.ref, batch.ref, qp, qs, dt, q_heads, scale, window, sinks,
+                            _arg(ctx, ws, "ws", 0, _u8), ws.numel(), _arg(ctx, out, "out", n, types),
+                            _arg(ctx, out8, "out8", n, _e4m3_types), _arg(ctx, out_scale, "out_scale", n // 128, _f32),
+                            _stream_of(ctx, stream))
+    if st:
+        _check(st, fn, ctx.L)
 
 
 def attn_decode(ctx: Context, cache: KvCache, batch: KvBatch, q, q_heads: int, scale: float, window: int, sinks: int,

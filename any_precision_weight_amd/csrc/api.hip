@@ -1476,7 +1476,7 @@ WsLayoutAttn ws_layout_attn(size_t rows, int head_dim)
 // into more parts, up to a bound.
 size_t attn_part_rows(const apmoe_kv_cache *c, int B, int q_heads)
 {
-    const size_t decode = (size_t)apmoe::decode_slots(B, c->kv_heads, q_heads) * q_heads;
+    const size_t decode = (size_t)apmoe::decode_slots_most(B, c->kv_heads, q_heads) * q_heads;
     const size_t prefill = (size_t)apmoe::kPartBlocks * apmoe::kPartRows;
     return decode > prefill ? decode : prefill;
 }
@@ -1520,7 +1520,11 @@ apmoe_status attn_args(apmoe_ctx *ctx, const apmoe_kv_cache *cache, const apmoe_
     *p = apmoe::AttnParams{kv_view(cache), kv_batch(cache, batch), q, q_stride, dtype, q_heads, scale, window, sinks,
                            out, out8, out_scale, reinterpret_cast<float *>(w + L.part_o),
                            reinterpret_cast<float *>(w + L.part_ml),
-                           apmoe::decode_slots(batch->B, cache->kv_heads, q_heads), 0, 1};
+                           0, 0, 0, 0, 1};
+    const apmoe::DecodePlan d = apmoe::decode_plan(batch->B, cache->kv_heads, q_heads, p->s.room);
+    p->slots = d.slots;
+    p->part_tiles = d.part_tiles;
+    p->few = d.few;
     p->tiles = apmoe::prefill_tiles(batch->B, batch->T, q_heads / cache->kv_heads);
     p->parts = apmoe::prefill_parts(p->tiles, cache->kv_heads, p->s.room);
     return ok();

@@ -94,16 +94,20 @@ __device__ inline u32x4 from_e4m3x8(uint32_t lo, uint32_t hi)
 // Tokens of a sequence of `len` tokens that the cache can hold at all.
 __device__ inline int cached_tokens(const AttnBatch &S, int len) { return max(0, min(len, S.room)); }
 
+// Sum over the lanes up to and with this one: within rows of 16 lanes, then rows 0 and 2 into
+// the next one, then lane 31 into the upper half (lane exchanges without LDS).
 __device__ inline int wave_scan(int v)
 {
-    const int lane = threadIdx.x % kWave;
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-        const int o = __shfl_up(v, d, kWave);
-        v += lane >= d ? o : 0;
-    }
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);  // from 1, 2, 4, 8 lanes below
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row's last lane to the next row
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // lane 31 to the upper half
     return v;
 }
+
+__device__ inline int wave_sum(int v) { return __builtin_amdgcn_readlane(wave_scan(v), kWave - 1); }
 
 // Items of the sequences one after the other, count(b) of sequence b: the sequence b and the
 // index `local` in it of item w, and the sequence's number of items n; false when there are

@@ -21,9 +21,26 @@
 namespace apmoe {
 namespace {
 
-constexpr int kCols = 16;      // query heads of one workgroup
-constexpr int kPartTiles = 4;  // the shortest part of a split sequence, in tiles
-constexpr int kParts = 1024;   // workgroups that a call is split into, about
+constexpr int kCols = 16;  // query heads of one workgroup
+
+// How a call is split, by the workgroups that its sequences have without (a key-value head, 16
+// query heads and a sequence each).
+//
+// Fewer than kFew (a CU each): parts for 512, two a CU in one round, of 4 tiles and more, and
+// above 32 parts a row of 8.  131072 tokens of 48 heads over 8 104 us with 512, 114 with 768; one
+// sequence of 8192 13.2 us in parts of 8 tiles and 15.9 in parts of 4, of 2000 11.1 and 10.0.
+// Up to 1024: parts of 16 tiles and more for 2048, in several rounds, for even rounds of uneven
+// sequences (64 of 160 to 16000 tokens, 32 heads over 8: 176 us; with 1024 179, 512 196; 24 of 1500
+// to 30000 with a window of 4096, 16 heads: 63, 67 and 78).  More have their rounds anyway: 512
+// (200 of 870 to 2600, 8 bits: 146 us, with 1024 151, 2048 165).
+// Not at all, and so without the second launch, where no sequence is long: up to 768 tokens, or
+// 2048 with many workgroups (one of 601 8.4 us against 9.0, one of 1000 9.8 against 9.2; 32 of 512
+// to 1024 20 against 26, 128 of 167 to 500 30 against 37).  Then few have eight waves each (16 of
+// 133 to 400 8.0 us against 9.4 with four), many four (128 of 167 to 500 30 against 40).
+constexpr int kFew = 256, kMany = 1024;
+constexpr int kWholeFew = 768, kWholeMany = 2048;
+constexpr int kPartsOnce = 512, kPartsEven = 2048;
+constexpr int kTilesFew = 4, kTilesMany = 16;
 
 // The tiles of one sequence that its query sees: [0, sink) and [first, end).
 struct Span {
@@ -47,19 +64,21 @@ __device__ inline Span span_of(const AttnParams &P, int b)
 // Tiles of a part: every workgroup and the join compute the same number, from the lengths.
 __device__ inline int part_tiles(const AttnParams &P)
 {
+    if (P.slots == P.s.B)  // whole sequences
+        return 1 << 30;
     const int lane = threadIdx.x % kWave;
-    int64_t sum = 0;
+    int64_t mine = 0;
     for (int b = lane; b < P.s.B; b += kWave)
-        sum += span_of(P, b).tiles;
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1)
-        sum += __shfl_xor((long long)sum, d, kWave);
+        mine += span_of(P, b).tiles;
+    // below 2^35 a lane: in two parts
+    const int64_t sum = ((int64_t)wave_sum((int)(mine >> 20)) << 20) + wave_sum((int)(mine & 0xFFFFF));
     const int64_t extra = P.slots - P.s.B;  // sum / ct more parts than sequences at most
-    const int64_t ct = extra > 0 ? (sum + extra - 1) / extra : sum;
-    return (int)max((int64_t)kPartTiles, min(ct, (int64_t)1 << 30));
+    const int64_t ct = (sum + extra - 1) / extra;
+    // parts of less than 8 tiles only where they are few (kTilesFew)
+    return (int)max(max(ct, min((int64_t)8, 2 * ct)), (int64_t)P.part_tiles);
 }
 
-__device__ inline int parts_of(int tiles, int ct) { return max(1, (tiles + ct - 1) / ct); }
+__device__ inline int parts_of(int tiles, int ct) { return max(1, (int)(((uint32_t)tiles + ct - 1) / (uint32_t)ct)); }
 
 // 8-bit rows: a group of 128 columns is D / 128-th of a head.
 __device__ inline void store_row(const AttnParams &P, size_t row, int d, const float (&v)[4], float scale)
@@ -126,7 +145,7 @@ struct Tile {
 
 // Grid: x the slots (a part of a sequence each), y key-value heads x groups of 16 query heads.
 template <int QT, bool C8, int D, int NW>
-__global__ void __launch_bounds__(NW *kWave) decode_kernel(const AttnParams P)
+__global__ void __launch_bounds__(NW *kWave, D == 256 ? 1 : 2) decode_kernel(const AttnParams P)
 {
     using T = Tile<QT, C8, D>;
     constexpr int DT = D / 16;
@@ -401,9 +420,7 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams P)
     int first = 0;
     for (int i = lane; i < b; i += kWave)
         first += parts_of(span_of(P, i).tiles, ct);
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1)
-        first += __shfl_xor(first, d, kWave);
+    first = wave_sum(first);
     const float *ml = P.part_ml + 2 * ((size_t)first * P.Hq + h);
     const size_t step = 2 * (size_t)P.Hq;
     float M = -INFINITY;
@@ -468,15 +485,23 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams P)
     store_row(P, row, 4 * c, v, scale);
 }
 
-template <int QT, bool C8, int D>
-hipError_t decode_launch(const AttnParams &P, hipStream_t s)
+template <int QT, bool C8, int D, int NW>
+hipError_t decode_waves(const AttnParams &P, hipStream_t s)
 {
-    constexpr int NW = 4;
     const int G = P.Hq / P.kv.Hkv;
     hipLaunchKernelGGL((decode_kernel<QT, C8, D, NW>), dim3(P.slots, P.kv.Hkv * ((G + kCols - 1) / kCols)),
                        dim3(NW * kWave), 0, s, P);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || P.s.room <= kPartTiles * kTile)
+    return hipGetLastError();
+}
+
+template <int QT, bool C8, int D>
+hipError_t decode_launch(const AttnParams &P, hipStream_t s)
+{
+    if constexpr (D <= 128)  // 8 waves leave 256 registers each
+        if (P.slots == P.s.B && P.few)
+            return decode_waves<QT, C8, D, 8>(P, s);
+    const hipError_t e = decode_waves<QT, C8, D, 4>(P, s);
+    if (e != hipSuccess || P.slots == P.s.B)
         return e;
     hipLaunchKernelGGL((join_kernel<D>), dim3(P.s.B, P.Hq), dim3(256), 0, s, P);
     return hipGetLastError();
@@ -494,10 +519,22 @@ hipError_t decode_dim(const AttnParams &P, hipStream_t s)
 
 }  // namespace
 
-int decode_slots(int B, int Hkv, int Hq)
+// How a call is split.  Rows: workgroups that a sequence has anyway.
+DecodePlan decode_plan(int B, int Hkv, int Hq, int room)
+{
+    const int rows = Hkv * ((Hq / Hkv + kCols - 1) / kCols), all = B * rows;
+    DecodePlan p;
+    p.few = all < kFew;
+    p.part_tiles = p.few ? kTilesFew : kTilesMany;
+    const int whole = p.few ? kWholeFew : kWholeMany, parts = p.few || all >= kMany ? kPartsOnce : kPartsEven;
+    p.slots = room <= whole ? B : B + std::max(1, parts / rows);
+    return p;
+}
+
+int decode_slots_most(int B, int Hkv, int Hq)
 {
     const int rows = Hkv * ((Hq / Hkv + kCols - 1) / kCols);
-    return B + std::max(1, kParts / rows);
+    return B + std::max(1, kPartsEven / rows);
 }
 
 hipError_t launch_attn_decode(const AttnParams &P, hipStream_t s)

@@ -50,15 +50,20 @@ struct AttnParams {
     // prefill: [tiles][parts][Hkv][kPartRows]
     float *part_o;
     float *part_ml;
-    int slots;
+    int slots, part_tiles, few;
     int tiles, parts;
 };
 
 constexpr int kPartRows = 128;    // rows of a tile of prefill
 constexpr int kPartBlocks = 512;  // prefill splits no call into more workgroups than this
 
-// Slots of the parts of a decode call: one a sequence and as many again as fill the device.
-int decode_slots(int B, int Hkv, int Hq);
+// How a decode call is split: slots of parts (as many as sequences: not at all), the shortest
+// part in tiles of 32 tokens, and whether it has few workgroups.
+struct DecodePlan {
+    int slots, part_tiles, few;
+};
+DecodePlan decode_plan(int B, int Hkv, int Hq, int room);
+int decode_slots_most(int B, int Hkv, int Hq);  // for B sequences or fewer
 
 // Row tiles of a prefill call with groups of G heads, an upper bound, and the parts that each
 // is split into.
