@@ -242,6 +242,39 @@ def test_decode_in_parts(t, D, page, Hq, Hkv, lens, window, sinks, c8):
     assert torch.equal(a.view(torch.int16), b.view(torch.int16))
 
 
+@pytest.mark.parametrize("c8", [False, True])
+def test_decode_of_many_workgroups_in_parts(c8):
+    """256 to 1023 workgroups, and more: parts of 16 tiles for the long sequences only."""
+    rng = rng_of("many parts", c8)
+    lens = list(rng.integers(0, 200, 38)) + [3000, 1400]
+    bt = Batch(rng, lens, None, 8, 64, 64, "bf16", c8)
+    check(apw.attn_decode, bt, queries(rng, bt.T, 8, 64, "bf16", 2.0), 8)
+    lens = list(rng.integers(0, 40, 127)) + [5000, 2100, 600]
+    bt = Batch(rng, lens, None, 8, 64, 256, "f16", c8)
+    check(apw.attn_decode, bt, queries(rng, bt.T, 8, 64, "f16", 2.0), 8, window=4000, sinks=100)
+
+
+@pytest.mark.parametrize("fn", [apw.attn_decode, apw.attn_prefill])
+def test_a_long_tail_of_small_probabilities(fn):
+    """One token with 2^15 times the weight of each of 20000 others, which have a third of the
+    weight together: below fp16's normal numbers, and not to be lost."""
+    rng = rng_of("tail")
+    n, D = 20000, 64
+    bt = Batch(rng, [n], None if fn is apw.attn_decode else [2], 1, D, 256, "f16", False, filled=False)
+    idx = {x: ref.place(x, 256, D, 2) for x in "kv"}
+    keys, values = np.zeros((n, D)), 1.0 + ref.round16(rng.standard_normal((n, D)) * 0.1, "f16")
+    keys[n // 3, 0] = 15.0 * np.log(2.0)
+    keys, values = ref.round16(keys, "f16"), ref.round16(values, "f16")
+    values[n // 3] = -1.0
+    for x, rows in (("k", keys), ("v", values)):
+        for i in range(-(-n // 256)):
+            part = rows[i * 256:(i + 1) * 256]
+            bt.cache.data[x][bt.table[0, i], 0, idx[x][:len(part)].ravel()] = part.ravel()
+    q = torch.zeros((bt.T, D), dtype=torch.float16)
+    q[:, 0] = 1.0
+    check(fn, bt, q, 1, scale=1.0)
+
+
 def test_decode_of_more_sequences_than_a_wave():
     rng = rng_of("many")
     lens = list(rng.integers(0, 70, 200)) + [900]
@@ -299,6 +332,36 @@ def test_prefill_window(window, sinks):
     for c8 in (False, True):
         bt = Batch(rng, [300, 150, 33], [300, 20, 33], 2, 64, 32, "f16", c8)
         check(apw.attn_prefill, bt, queries(rng, bt.T, 2, 64, "f16", 2.0), 2, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("c8", [False, True])
+@pytest.mark.parametrize("t,D,page,Hq,Hkv,lens,news,window,sinks", [
+    ("f16", 128, 64, 8, 2, [3000], [4], 0, 0), ("bf16", 128, 32, 16, 1, [5000, 70, 0], [33, 70, 2], 0, 0),
+    ("bf16", 64, 64, 3, 3, [2048, 1999, 64], [1, 130, 64], 1500, 70), ("f16", 256, 256, 4, 2, [1700, 900], [7, 40], 0, 0),
+    ("bf16", 128, 128, 6, 1, [4100, 3], [60, 3], 2000, 600)])
+def test_prefill_in_parts(t, D, page, Hq, Hkv, lens, news, window, sinks, c8):
+    """Few rows behind long caches: split over the steps and joined."""
+    rng = rng_of("prefill parts", t, D, page, Hq, Hkv, lens, news, window, c8)
+    bt = Batch(rng, lens, news, Hkv, D, page, t, c8, pad=2)
+    q = queries(rng, bt.T, Hq, D, t, 2.0)
+    a = check(apw.attn_prefill, bt, q, Hq, window=window, sinks=sinks, out8=D >= 128)
+    b, _, _ = attend(apw.attn_prefill, bt, q, Hq, window=window, sinks=sinks)
+    assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+@pytest.mark.parametrize("c8", [False, True])
+def test_prefill_in_parts_with_missing_pages_and_bad_values(c8):
+    rng = rng_of("prefill parts, pages", c8)
+    bt = Batch(rng, [2000, 1500], [20, 9], 2, 64, 32, "bf16", c8)
+    bt.table[0, 10:40] = -1  # a part of nothing
+    bt.table[1, 5] = bt.cache.n_pages
+    for b, pos in ((0, 1985), (1, 1493)):
+        row = rng.standard_normal((2, 64))
+        row[1, 5] = np.nan
+        bt.cache.put("v", bt.table[b, pos // 32], pos % 32, row)
+    q = queries(rng, bt.T, 4, 64, "bf16")
+    check(apw.attn_prefill, bt, q, 4)
+    check(apw.attn_prefill, bt, q, 4, window=1200, sinks=40)
 
 
 def test_prefill_without_offsets_is_decode():
