@@ -2,14 +2,19 @@
 // split over the cache's length and joined.
 //
 //   o = sum_j p_j v_j / sum_j p_j,  p_j = exp2(c q.k_j - m),  c = scale * log2(e), m the running
-//   maximum; parts (m, l, o) and (m', l', o') join as exp2(m - M) and exp2(m' - M) times each,
+// maximum; parts (m, l, o) and (m', l', o') join as exp2(m - M) and exp2(m' - M) times each,
 //   M = max(m, m').
 //
-// Bound by the cache's bytes.  A wave takes one 32-token tile after the other: the scores of
-// 16 query heads of a key-value head from two 16-token products, the softmax in registers,
-// the second product on the probabilities where they are.  Keys and values go from memory
-// into registers (no LDS: the operands of the products are whole lines of the cache); the
-// next tile's keys are asked for when this one's are used, its values likewise.
+// Bound by the cache's bytes: 131072 tokens of 8 heads of 128 in fp16 88 us, 6.1 TB/s (4 us of
+// them the join); 64 sequences of 160 to 16000 157 us, 5.9; 200 of 870 to 2600 in 8 bits 133 us,
+// 5.0.  Short caches are a chain of loads (length, page, keys) and the waves' join: 100 tokens
+// 6.2 us, 601 8.4.
+//
+// A wave takes one 32-token tile after the other: the scores of 16 query heads of a key-value
+// head from two 16-token products, the softmax in registers, the second product on the
+// probabilities where they are.  Keys and values go from memory into registers (no LDS: the
+// operands of the products are whole lines of the cache); the next tile's keys are asked for
+// when this one's are used, its values likewise, so a wave always has 8 to 16 KB on the way.
 //
 // Probabilities are given to the second product as the sum of two 16-bit numbers: the
 // matrix units have room (16 columns are computed for a group of 1 to 16 heads), and the
@@ -419,14 +424,15 @@ __global__ void __launch_bounds__(NW *kWave, D == 256 ? 1 : 2) decode_kernel(con
     }
 }
 
-// Joins the parts of split sequences: a workgroup has one query head of one sequence, its
-// first D / 4 threads the columns and the others the same columns of other parts.
-template <int D>
+// Joins the parts of split sequences.  A row of D / 4 threads has the columns; RP rows, whole
+// waves, take every RP-th part of one query head of one sequence.
+template <int D, int RP>
 __global__ void __launch_bounds__(256) join_kernel(const AttnParams P)
 {
-    constexpr int kLanes = D / 4, kRows = 256 / kLanes;
+    constexpr int kLanes = D / 4, kRows = 256 / kLanes, kHeads = kRows / RP;
+    static_assert(RP * kLanes % kWave == 0, "a wave has one head");
     const int ct = part_tiles(P);
-    const int lane = threadIdx.x % kWave, b = blockIdx.x, h = blockIdx.y;
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, b = blockIdx.x;
     const int n = parts_of(span_of(P, b).tiles, ct);
     if (n <= 1)
         return;
@@ -434,68 +440,83 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams P)
     for (int i = lane; i < b; i += kWave)
         first += parts_of(span_of(P, i).tiles, ct);
     first = wave_sum(first);
-    const float *ml = P.part_ml + 2 * ((size_t)first * P.Hq + h);
-    const size_t step = 2 * (size_t)P.Hq;
+    const int c = threadIdx.x % kLanes, r = threadIdx.x / kLanes, rp = r % RP;
+    const int mine = blockIdx.y * kHeads + r / RP, h = min(mine, P.Hq - 1);
+    const float *const ml = P.part_ml + 2 * ((size_t)first * P.Hq + h);
+    const float *const po = P.part_o + ((size_t)first * P.Hq + h) * D + 4 * c;
+    const size_t step = P.Hq;
     float M = -INFINITY;
     for (int i = lane; i < n; i += kWave)
-        M = fmaxf(M, ml[i * step]);
+        M = fmaxf(M, ml[2 * i * step]);
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1)
         M = fmaxf(M, __shfl_xor(M, d, kWave));
-    const int c = threadIdx.x % kLanes, r = threadIdx.x / kLanes;
+    __shared__ float fs[4][kWave];
+    __shared__ float4v os[kRows][kLanes];
+    __shared__ uint32_t top[kHeads][kLanes];
     float L = 0.0f;
     float4v o = {0.f, 0.f, 0.f, 0.f};
-    for (int i = r; i < n; i += kRows) {
-        const float m = ml[i * step], f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - M);
-        const float4v p =
-            *reinterpret_cast<const float4v *>(P.part_o + ((size_t)(first + i) * P.Hq + h) * D + 4 * c);
-        if (m != -INFINITY) {
-            L += f * ml[i * step + 1];
+    for (int i0 = 0; i0 < n; i0 += kWave) {
+        const int i = i0 + lane, end = min(n - i0, kWave);
+        float f = 0.0f;
+        if (i < n) {
+            const float m = ml[2 * i * step];
+            f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - M);  // a part that saw nothing: zeros
+            L += m == -INFINITY ? 0.0f : f * ml[2 * i * step + 1];
+        }
+        // the wave's own: its lanes read what they wrote before and after, in order
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        fs[wave][lane] = f;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll 4
+        for (int j = rp; j < end; j += RP) {
+            const float4v p = *reinterpret_cast<const float4v *>(po + (size_t)(i0 + j) * step * D);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                o[j] += f * p[j];
+            for (int k = 0; k < 4; ++k)
+                o[k] += fs[wave][j] * p[k];
         }
     }
-    __shared__ float4v os[kRows][kLanes];
-    __shared__ float ls[kRows];
-    __shared__ uint32_t top[kLanes];
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1)
+        L += __shfl_xor(L, d, kWave);
     os[r][c] = o;
-    if (c == 0)
-        ls[r] = L;
     __syncthreads();
     float v[4] = {0.f, 0.f, 0.f, 0.f};
-    if (r == 0) {
-        L = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            L += ls[i];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                v[j] += os[i][c][j];
-        }
+    if (rp == 0) {
         const float inv = L == 0.0f ? 0.0f : 1.0f / L;
         uint32_t a = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[j] *= inv;
-            a = max(a, mag(v[j]));
+        for (int k = 0; k < 4; ++k) {
+#pragma unroll
+            for (int i = 0; i < RP; ++i)
+                v[k] += os[r + i][c][k];
+            v[k] *= inv;
+            a = max(a, mag(v[k]));
         }
-        top[c] = a;
+        top[r / RP][c] = a;
     }
     __syncthreads();
-    if (r != 0)
+    if (rp != 0 || mine >= P.Hq)
         return;
     const size_t row = (size_t)b * P.Hq + h;
     float scale = 1.0f;
     if (D >= kBlk && P.out8) {
         uint32_t a = 0;
         for (int i = 0; i < kBlk / 4; ++i)
-            a = max(a, top[c / (kBlk / 4) * (kBlk / 4) + i]);
+            a = max(a, top[r / RP][c / (kBlk / 4) * (kBlk / 4) + i]);
         scale = scale_of(a);
         if (c % (kBlk / 4) == 0)
             P.out_scale[row * (D / kBlk) + c / (kBlk / 4)] = scale;
     }
     store_row(P, row, 4 * c, v, scale);
+}
+
+template <int D, int RP>
+hipError_t join_launch(const AttnParams &P, hipStream_t s)
+{
+    constexpr int kHeads = 256 / (D / 4) / RP;
+    hipLaunchKernelGGL((join_kernel<D, RP>), dim3(P.s.B, (P.Hq + kHeads - 1) / kHeads), dim3(256), 0, s, P);
+    return hipGetLastError();
 }
 
 template <int QT, bool C8, int D, int NW, bool ONCE>
@@ -517,8 +538,8 @@ hipError_t decode_launch(const AttnParams &P, hipStream_t s)
     const hipError_t e = once ? decode_waves<QT, C8, D, 4, true>(P, s) : decode_waves<QT, C8, D, 4, false>(P, s);
     if (e != hipSuccess || P.slots == P.s.B)
         return e;
-    hipLaunchKernelGGL((join_kernel<D>), dim3(P.s.B, P.Hq), dim3(256), 0, s, P);
-    return hipGetLastError();
+    // few sequences have many parts
+    return P.few ? join_launch<D, 1024 / D>(P, s) : join_launch<D, 4>(P, s);
 }
 
 template <int QT, bool C8>

@@ -4,8 +4,23 @@
 // The formulas are attn_decode.hip's.  A row is a (new token, query head) pair; the heads of a
 // key-value head's group are neighbours, so a workgroup's 128 rows share their keys and
 // values whatever the group's size.  Four waves have 32 rows each and walk over 64 cached
-// tokens at a time, staged in LDS in the cache's own order: the operands of the 32 x 32
-// products are then 16-byte reads of neighbouring places.
+// tokens a step, staged in LDS in the cache's own order (two buffers each of keys and values,
+// sent for a step ahead): the operands of the 32 x 32 products are 16-byte reads of
+// neighbouring places, without bank conflicts.
+//
+// A step is the products of the next scores with this step's exponentials between them, then
+// the second products with the next maximum between them: a wave's vector instructions run in
+// its own matrix instructions' time (3.4 of them and one exponential beside each, where one of
+// two waves a SIMD has room for about 6), and two workgroups a CU cover each other's barriers.
+//
+// Bound by the matrix units at the clock that the power allows: 8192 tokens, 32 heads over 8 of
+// 128 in bf16 511 to 528 us, 1.04 to 1.08 PFLOP/s; 6000 tokens of each of three sequences behind
+// up to 14000, with a window, 3.1 to 3.3 ms, 1.04 to 1.09 (a large library product reaches 1.50
+// here).  The matrix units are busy for 59% of the SIMDs' cycles, at 1.6 GHz; before the
+// interleaving it was 47% at 2.0 GHz for 571 us.  Heads of 64 take 327 us for two prompts of 6000
+// (0.90), of 256 (one wave a SIMD) 528 us for two of 5000 of 16 heads (0.78); an 8-bit cache,
+// converted on its way into LDS, 680 us for the first (0.81).  64 rows a wave (half the reads
+// from LDS, one wave a SIMD) took 654 us for it.
 //
 // Rows of a key operand: row 16 t + 8 a + 4 h + b of a 32-token product is token 16 a + 8 t +
 // 4 h + b.  Lane half h then has, of scores 8t .. 8t+7, the tokens of granule g = 2 t + h of
@@ -486,6 +501,7 @@ __global__ void __launch_bounds__(kWaves *kWave, D == 64 && !C8 ? 3 : D <= 128 ?
                 word(s, v, i);
         });
         half(st);
+        // ahead of a wave that is at its scores: 529 us against 538 for 8192 tokens
         __builtin_amdgcn_s_setprio(1);
         u32x4 ring[C::kAhead];
 #pragma unroll
