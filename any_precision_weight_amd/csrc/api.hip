@@ -1496,7 +1496,7 @@ apmoe_status attn_args(apmoe_ctx *ctx, const apmoe_kv_cache *cache, const apmoe_
         return s;
     if (!type16(dtype) || (cache->dtype != dtype && cache->dtype != APMOE_E4M3))
         return fail(APMOE_UNSUPPORTED, "dtype %d with a cache of dtype %d", dtype, cache->dtype);
-    if (!(scale >= -3.4e38f && scale <= 3.4e38f) || window < 0 || window > 1 << 30 || sinks < 0)
+    if (!(scale >= -0x1p100f && scale <= 0x1p100f) || window < 0 || window > 1 << 30 || sinks < 0)
         return fail(APMOE_INVALID_ARG, "scale=%g window=%d sinks=%d", (double)scale, window, sinks);
     if (!out8 != !out_scale)
         return fail(APMOE_INVALID_ARG, "out8 and out_scale: one is NULL");

@@ -639,7 +639,7 @@ typedef struct apmoe_kv_batch {
  * Rotations are fp64, each value rounded once.  A row whose position is negative, at or
  * past n_pos (rot > 0) or max_len, or on no page is padding: nothing of it is written.
  * Two rows must not have the same place in the cache (sequences that share a page may not
- * both write to it): which of them is stored is not defined.
+ * both write to it): what is stored there is then a mixture of both.
  * Limits: rot % 16 == 0, 0 <= rot <= D; 0 <= q_heads <= 1024; strides multiples of 8, at
  * least a row's length.  q_out, the inputs and the cache must not overlap.
  * Errors (nothing enqueued): INVALID_ARG for NULL or misaligned pointers (16 bytes; pages,
@@ -669,13 +669,14 @@ apmoe_status apmoe_attn_workspace(apmoe_ctx *ctx, const apmoe_kv_cache *cache, c
  *   [T][q_heads * D / 128] (the rows that apmoe_gemm_fp8 takes), both NULL or both set, with
  *   head_dim 128 or 256.  At least one of out, out8 (T > 0).
  * Scores, statistics and sums are fp32; the probabilities (with an APMOE_E4M3 cache, times
- * the values' scales) go into the second product as two 16-bit numbers, to 2^-16 of each.  A row that sees nothing, or nothing but scores of -infinity, is zeros.  What lies
- * in the cache where a row sees nothing does not matter, NaN and infinities included.
+ * the values' scales) go into the second product as two 16-bit numbers, to 2^-16 of each.
+ * A row that sees nothing, or nothing but scores of -infinity, is zeros.  What lies in the
+ * cache where a row sees nothing does not matter, NaN and infinities included.
  * ws: caller-owned device memory of at least apmoe_attn_workspace bytes, 256-byte aligned;
  * calls (or captured graphs) that may run at the same time need one each.  Long caches are
  * split over workgroups and joined in a second launch, in an order that depends on the
- * batch's lengths only: repeated calls give identical bits.
- * Limits: 1 <= q_heads <= 1024, a multiple of kv_heads; scale finite; 0 <= window <= 2^30,
+ * batch's sizes and lengths only: repeated calls give identical bits.
+ * Limits: 1 <= q_heads <= 1024, a multiple of kv_heads; |scale| <= 2^100; 0 <= window <= 2^30,
  * 0 <= sinks; q_stride a multiple of 8, at least q_heads * D.  The call enqueues only kernel
  * launches on `stream` and can be captured.  Errors as apmoe_kv_append (out_scale 4 bytes),
  * UNSUPPORTED also for out8 with head_dim 64.

@@ -108,7 +108,7 @@ def test_append_refusals(kw, status):
 @pytest.mark.parametrize("kw,status", [
     (dict(ctx=None), 1), (dict(dt=apw.F32), 2), (dict(dt=apw.BF16), 2), (dict(dt=apw.E4M3), 2), (dict(heads=0), 1),
     (dict(heads=3), 1), (dict(heads=1026), 1), (dict(heads=-2), 1), (dict(scale=float("nan")), 1),
-    (dict(scale=float("inf")), 1), (dict(window=-1), 1), (dict(window=(1 << 30) + 1), 1), (dict(sinks=-1), 1),
+    (dict(scale=float("inf")), 1), (dict(scale=-1e31), 1), (dict(window=-1), 1), (dict(window=(1 << 30) + 1), 1), (dict(sinks=-1), 1),
     (dict(ws=None), 1), (dict(ws=A + 64), 1), (dict(ws_bytes=100), 1), (dict(q=None), 1), (dict(q=A + 8), 1),
     (dict(qs=508), 1), (dict(qs=504), 1), (dict(out=None), 1), (dict(out=A + 8), 1), (dict(out8=A), 1),
     (dict(out_scale=A), 1), (dict(out8=A + 8, out_scale=A), 1), (dict(out8=A, out_scale=A + 2), 1)])
