@@ -1521,7 +1521,9 @@ apmoe_status attn_args(apmoe_ctx *ctx, const apmoe_kv_cache *cache, const apmoe_
                            out, out8, out_scale, reinterpret_cast<float *>(w + L.part_o),
                            reinterpret_cast<float *>(w + L.part_ml),
                            0, 0, 0, 0, 1};
-    const apmoe::DecodePlan d = apmoe::decode_plan(batch->B, cache->kv_heads, q_heads, p->s.room);
+    const int64_t near = (int64_t)window + sinks;
+    const apmoe::DecodePlan d = apmoe::decode_plan(batch->B, cache->kv_heads, q_heads, cache->dtype == APMOE_E4M3,
+                                                   window && near < p->s.room ? near : p->s.room);
     p->slots = d.slots;
     p->part_tiles = d.part_tiles;
     p->few = d.few;

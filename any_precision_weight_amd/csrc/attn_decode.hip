@@ -6,8 +6,8 @@
 //   M = max(m, m').
 //
 // Bound by the cache's bytes: 131072 tokens of 8 heads of 128 in fp16 88 us, 6.1 TB/s (4 us of
-// them the join); 64 sequences of 160 to 16000 157 us, 5.9; 200 of 870 to 2600 in 8 bits 133 us,
-// 5.0.  Short caches are a chain of loads (length, page, keys) and the waves' join: 100 tokens
+// them the join); 64 sequences of 160 to 16000 157 us, 5.9; 200 of 870 to 2600 in 8 bits 123 to
+// 129 us, 5.2 to 5.4.  Short caches are a chain of loads (length, page, keys) and the waves' join: 100 tokens
 // 6.2 us, 601 8.4.
 //
 // A wave takes one 32-token tile after the other: the scores of 16 query heads of a key-value
@@ -32,18 +32,21 @@ constexpr int kCols = 16;  // query heads of one workgroup
 // query heads and a sequence each).
 //
 // Fewer than kFew (a CU each): parts for 512, two a CU in one round, of 4 tiles and more, and
-// above 32 parts a row of 8.  131072 tokens of 48 heads over 8 104 us with 512, 114 with 768; one
+// above 32 parts a row of 8.  131072 tokens of 48 heads over 8 88 us with 512, 97 with 768; one
 // sequence of 8192 13.2 us in parts of 8 tiles and 15.9 in parts of 4, of 2000 11.1 and 10.0.
-// Up to 1024: parts of 16 tiles and more for 2048, in several rounds, for even rounds of uneven
-// sequences (64 of 160 to 16000 tokens, 32 heads over 8: 176 us; with 1024 179, 512 196; 24 of 1500
-// to 30000 with a window of 4096, 16 heads: 63, 67 and 78).  More have their rounds anyway: 512
-// (200 of 870 to 2600, 8 bits: 146 us, with 1024 151, 2048 165).
-// Not at all, and so without the second launch, where no sequence is long: up to 768 tokens, or
+// More: parts of 16 tiles and more for 2048, in several rounds, for even rounds of uneven
+// sequences (64 of 160 to 16000 tokens, 32 heads over 8: 158 us; with 1024 162, 512 177; 200 of
+// 160 to 8000 292, with 1024 307, 512 334; 24 of 1500 to 30000 with a window of 4096, 16 heads:
+// 64, 68 and 79).
+// Not at all, and so without the second launch, where no query sees many tokens: up to 768, or
 // 2048 with many workgroups (one of 601 8.4 us against 9.0, one of 1000 9.8 against 9.2; 32 of 512
-// to 1024 20 against 26, 128 of 167 to 500 30 against 37).  Then few have eight waves each (16 of
-// 133 to 400 8.0 us against 9.4 with four), many four (128 of 167 to 500 30 against 40).
+// to 1024 20 against 26, 128 of 167 to 500 30 against 37), or 4096 of an 8-bit cache with kMany
+// (as many bytes; 200 of 870 to 2600 123 us against 150; 160 of 30 to 3000 70 against 79; with 16
+// bits 200 of 870 to 2600 take 210 against 223, but 128 of 133 to 4000 122 against 110).  Then few
+// have eight waves each (16 of 133 to 400 8.0 us against 9.4 with four), many four (128 of 167 to
+// 500 30 against 40).
 constexpr int kFew = 256, kMany = 1024;
-constexpr int kWholeFew = 768, kWholeMany = 2048;
+constexpr int kWholeFew = 768, kWholeMany = 2048, kWhole8 = 4096;
 constexpr int kPartsOnce = 512, kPartsEven = 2048;
 constexpr int kTilesFew = 4, kTilesMany = 16;
 
@@ -554,15 +557,16 @@ hipError_t decode_dim(const AttnParams &P, hipStream_t s)
 
 }  // namespace
 
-// How a call is split.  Rows: workgroups that a sequence has anyway.
-DecodePlan decode_plan(int B, int Hkv, int Hq, int room)
+// How a call is split.  Rows: workgroups that a sequence has anyway; seen: tokens that a query
+// sees at most.
+DecodePlan decode_plan(int B, int Hkv, int Hq, bool c8, int64_t seen)
 {
     const int rows = Hkv * ((Hq / Hkv + kCols - 1) / kCols), all = B * rows;
     DecodePlan p;
     p.few = all < kFew;
     p.part_tiles = p.few ? kTilesFew : kTilesMany;
-    const int whole = p.few ? kWholeFew : kWholeMany, parts = p.few || all >= kMany ? kPartsOnce : kPartsEven;
-    p.slots = room <= whole ? B : B + std::max(1, parts / rows);
+    const int whole = p.few ? kWholeFew : c8 && all >= kMany ? kWhole8 : kWholeMany;
+    p.slots = seen <= whole ? B : B + std::max(1, (p.few ? kPartsOnce : kPartsEven) / rows);
     return p;
 }
 

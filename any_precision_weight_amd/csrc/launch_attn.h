@@ -62,7 +62,7 @@ constexpr int kPartBlocks = 512;  // prefill splits no call into more workgroups
 struct DecodePlan {
     int slots, part_tiles, few;
 };
-DecodePlan decode_plan(int B, int Hkv, int Hq, int room);
+DecodePlan decode_plan(int B, int Hkv, int Hq, bool c8, int64_t seen);
 int decode_slots_most(int B, int Hkv, int Hq);  // for B sequences or fewer
 
 // Row tiles of a prefill call with groups of G heads, an upper bound, and the parts that each
