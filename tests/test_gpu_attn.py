@@ -254,6 +254,18 @@ def test_decode_of_many_workgroups_in_parts(c8):
     check(apw.attn_decode, bt, queries(rng, bt.T, 8, 64, "f16", 2.0), 8, window=4000, sinks=100)
 
 
+@pytest.mark.parametrize("c8", [False, True])
+def test_decode_of_long_sequences_whole(c8):
+    """Many workgroups with up to 4096 tokens in 8 bits, and windows that leave little of a long cache."""
+    rng = rng_of("whole", c8)
+    lens = list(rng.integers(0, 60, 127)) + [4090, 2500]
+    bt = Batch(rng, lens, None, 8, 64, 128, "bf16", c8)
+    check(apw.attn_decode, bt, queries(rng, bt.T, 8, 64, "bf16", 2.0), 8)
+    for window, sinks in ((700, 68), (700, 69), (1, 0), (0, 0), (3, (1 << 31) - 1)):
+        bt = Batch(rng, [5000, 767, 0, 769], None, 2, 128, 64, "f16", c8)
+        check(apw.attn_decode, bt, queries(rng, bt.T, 8, 128, "f16", 2.0), 8, window=window, sinks=sinks, out8=True)
+
+
 @pytest.mark.parametrize("fn", [apw.attn_decode, apw.attn_prefill])
 def test_a_long_tail_of_small_probabilities(fn):
     """One token with 2^15 times the weight of each of 20000 others, which have a third of the
