@@ -91,6 +91,15 @@ __device__ inline u32x4 from_e4m3x8(uint32_t lo, uint32_t hi)
                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true))};
 }
 
+// Factor of a part with maximum m and sum l where the largest maximum is M.  m = -infinity with
+// l = 0 is a part that saw nothing (or scores of -infinity only): 0.  The maximum passes a NaN
+// by, the sum does not: m = -infinity with any other l is a part whose scores were NaN, and
+// the factor is that NaN.
+__device__ inline float part_factor(float m, float l, float M)
+{
+    return m == -INFINITY ? l : __builtin_amdgcn_exp2f(m - M);
+}
+
 // Tokens of a sequence of `len` tokens that the cache can hold at all.
 __device__ inline int cached_tokens(const AttnBatch &S, int len) { return max(0, min(len, S.room)); }
 

@@ -351,16 +351,16 @@ __global__ void __launch_bounds__(NW *kWave, D == 256 ? 1 : 2) decode_kernel(con
     float L = 0.0f;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-        const float mw = ml[w][0][col];
-        L += mw == -INFINITY ? 0.0f : ml[w][1][col] * __builtin_amdgcn_exp2f(mw - M);
+        const float lw = ml[w][1][col];
+        L += lw * part_factor(ml[w][0][col], lw, M);
     }
     {
-        const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - M);
+        const float f = part_factor(m, l, M);
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                o[d][j] = m == -INFINITY ? 0.0f : o[d][j] * f;
+                o[d][j] = l == 0.0f ? 0.0f : o[d][j] * f;
     }
 #pragma unroll
     for (int half = NW / 2; half >= 1; half /= 2) {
@@ -463,9 +463,9 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams P)
         const int i = i0 + lane, end = min(n - i0, kWave);
         float f = 0.0f;
         if (i < n) {
-            const float m = ml[2 * i * step];
-            f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - M);  // a part that saw nothing: zeros
-            L += m == -INFINITY ? 0.0f : f * ml[2 * i * step + 1];
+            const float l = ml[2 * i * step + 1];
+            f = part_factor(ml[2 * i * step], l, M);
+            L += f * l;
         }
         // the wave's own: its lanes read what they wrote before and after, in order
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");

@@ -731,12 +731,11 @@ __global__ void __launch_bounds__(256) join_rows(const AttnParams P)
     float L = 0.0f, v[4] = {0.f, 0.f, 0.f, 0.f};
     for (int n = 0; n < t.parts; ++n) {
         const size_t slot = slot0 + n * step;
-        const float m = P.part_ml[2 * slot];
+        const float l = P.part_ml[2 * slot + 1], f = part_factor(P.part_ml[2 * slot], l, M);
         const float4v o = *reinterpret_cast<const float4v *>(P.part_o + slot * D + 4 * c);
-        if (m == -INFINITY)  // the part saw nothing
+        if (l == 0.0f)  // the part saw nothing
             continue;
-        const float f = __builtin_amdgcn_exp2f(m - M);
-        L += f * P.part_ml[2 * slot + 1];
+        L += f * l;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             v[j] += f * o[j];

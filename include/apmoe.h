@@ -670,8 +670,9 @@ apmoe_status apmoe_attn_workspace(apmoe_ctx *ctx, const apmoe_kv_cache *cache, c
  *   head_dim 128 or 256.  At least one of out, out8 (T > 0).
  * Scores, statistics and sums are fp32; the probabilities (with an APMOE_E4M3 cache, times
  * the values' scales) go into the second product as two 16-bit numbers, to 2^-16 of each.
- * A row that sees nothing, or nothing but scores of -infinity, is zeros.  What lies in the
- * cache where a row sees nothing does not matter, NaN and infinities included.
+ * A row that sees nothing, or nothing but scores of -infinity, is zeros; one that sees a
+ * score that is NaN is NaN.  What lies in the cache where a row sees nothing does not matter,
+ * NaN and infinities included.
  * ws: caller-owned device memory of at least apmoe_attn_workspace bytes, 256-byte aligned;
  * calls (or captured graphs) that may run at the same time need one each.  Long caches are
  * split over workgroups and joined in a second launch, in an order that depends on the
