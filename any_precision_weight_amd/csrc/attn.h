@@ -91,13 +91,28 @@ __device__ inline u32x4 from_e4m3x8(uint32_t lo, uint32_t hi)
                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true))};
 }
 
+// A value that all lanes have, in a scalar register.
+__device__ inline float uniform(float v)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, v)));
+}
+
+// exp2's argument is (s - m) c: c > 0 for scores s of queries whose signs are turned where the
+// scale is negative, so the maximum m is that of the scores as the products give them.  The
+// largest one's argument is 0 exactly, and no product of a score and c has to be a number.
+// A scale of 0 (or next to it) takes fp32's smallest number: arguments below 2^-20 for any
+// scores, and -infinity stays what it is.
+__device__ inline float score_factor(float scale) { return uniform(fmaxf(__builtin_fabsf(scale) * kLog2e, 0x1p-149f)); }
+
+__device__ inline uint32_t query_sign(float scale) { return scale < 0.0f ? 0x80008000u : 0u; }
+
 // Factor of a part with maximum m and sum l where the largest maximum is M.  m = -infinity with
 // l = 0 is a part that saw nothing (or scores of -infinity only): 0.  The maximum passes a NaN
 // by, the sum does not: m = -infinity with any other l is a part whose scores were NaN, and
 // the factor is that NaN.
-__device__ inline float part_factor(float m, float l, float M)
+__device__ inline float part_factor(float m, float l, float M, float c)
 {
-    return m == -INFINITY ? l : __builtin_amdgcn_exp2f(m - M);
+    return m == -INFINITY ? l : __builtin_amdgcn_exp2f((m - M) * c);
 }
 
 // Tokens of a sequence of `len` tokens that the cache can hold at all.

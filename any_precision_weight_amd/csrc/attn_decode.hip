@@ -1,9 +1,9 @@
 // attn_decode.hip -- attention of one new token of each sequence over the paged cache,
 // split over the cache's length and joined.
 //
-//   o = sum_j p_j v_j / sum_j p_j,  p_j = exp2(c q.k_j - m),  c = scale * log2(e), m the running
-// maximum; parts (m, l, o) and (m', l', o') join as exp2(m - M) and exp2(m' - M) times each,
-//   M = max(m, m').
+//   o = sum_j p_j v_j / sum_j p_j,  p_j = exp2(c (q.k_j - m)),  c = scale * log2(e), m the running
+// maximum of the scores; parts (m, l, o) and (m', l', o') join as exp2(c (m - M)) and
+// exp2(c (m' - M)) times each, M = max(m, m').
 //
 // Bound by the cache's bytes: 131072 tokens of 8 heads of 128 in fp16 88 us, 6.1 TB/s (4 us of
 // them the join); 64 sequences of 160 to 16000 157 us, 5.9; 200 of 870 to 2600 in 8 bits 123 to
@@ -186,9 +186,10 @@ __global__ void __launch_bounds__(NW *kWave, D == 256 ? 1 : 2) decode_kernel(con
         const uint16_t *row = P.q + (size_t)b * P.q_stride + ((size_t)kvh * G + (live ? h0 + col : 0)) * D;
 #pragma unroll
         for (int s = 0; s < D / 32; ++s)
-            q[s] = *reinterpret_cast<const u32x4 *>(row + (C8 ? 64 * (s / 2) + 16 * g + 8 * (s % 2) : 32 * s + 8 * g));
+            q[s] = *reinterpret_cast<const u32x4 *>(row + (C8 ? 64 * (s / 2) + 16 * g + 8 * (s % 2) : 32 * s + 8 * g)) ^
+                   query_sign(P.scale);
     }
-    const float c = P.scale * kLog2e;
+    const float c = score_factor(P.scale);
     const int shift = P.kv.page_shift, tshift = shift - 5;
     const size_t head = (size_t)D << shift;
     const int32_t *table = P.s.pages + (size_t)b * P.s.max_pages;
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(NW *kWave, D == 256 ? 1 : 2) decode_kernel(con
         float x[8], top = -INFINITY;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            x[e] = s[e / 4][e % 4] * c;
+            x[e] = s[e / 4][e % 4];
             if (!whole && !(seen >> e & 1))
                 x[e] = -INFINITY;
             top = fmaxf(top, x[e]);
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(NW *kWave, D == 256 ? 1 : 2) decode_kernel(con
         top = fmaxf(top, __shfl_xor(top, 32, kWave));
         if (__any(top > m)) {
             const float to = fmaxf(m, top);
-            const float f = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+            const float f = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m - to) * c);
             m = to;
             l *= f;
 #pragma unroll
@@ -294,7 +295,7 @@ __global__ void __launch_bounds__(NW *kWave, D == 256 ? 1 : 2) decode_kernel(con
         float p[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            p[e] = __builtin_amdgcn_exp2f(x[e] - base);
+            p[e] = __builtin_amdgcn_exp2f((x[e] - base) * c);
             l += p[e];
         }
         if constexpr (C8)
@@ -352,10 +353,10 @@ __global__ void __launch_bounds__(NW *kWave, D == 256 ? 1 : 2) decode_kernel(con
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
         const float lw = ml[w][1][col];
-        L += lw * part_factor(ml[w][0][col], lw, M);
+        L += lw * part_factor(ml[w][0][col], lw, M, c);
     }
     {
-        const float f = part_factor(m, l, M);
+        const float f = part_factor(m, l, M, c);
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -464,7 +465,7 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams P)
         float f = 0.0f;
         if (i < n) {
             const float l = ml[2 * i * step + 1];
-            f = part_factor(ml[2 * i * step], l, M);
+            f = part_factor(ml[2 * i * step], l, M, score_factor(P.scale));
             L += f * l;
         }
         // the wave's own: its lanes read what they wrote before and after, in order

@@ -38,6 +38,7 @@ static_assert(kRows == kPartRows, "rows of a part");
 constexpr int kStep = 64;           // cached tokens of a step
 constexpr uint32_t kGridX = 1u << 22;
 constexpr float kSlack = 8.0f;
+constexpr float kFar = 0x1p20f;
 // Calls of few row tiles are split over the steps: up to kSplitBlocks workgroups (of 256 CUs
 // that hold two) into parts of kPartSteps steps or more.  512 new tokens behind 32256, 32 heads
 // over 8: 796 -> 301 us, 4 of each of 16 sequences of 2700 to 8000 252 -> 93, 64 behind 4000
@@ -297,17 +298,14 @@ __global__ void __launch_bounds__(kWaves *kWave, D == 64 && !C8 ? 3 : D <= 128 ?
     const int st0 = part * t.per, steps = min(t.steps - st0, t.per);
     auto step_of = [&](int st) { return t.step(st0 + st); };
 
-    // a negative scale is the queries' sign, and 0 a number too small to matter: c > 0 keeps
-    // the order of the scores, so the maximum is that of the unscaled ones
     u32x4 q[KS];
     {
         const uint16_t *row = P.q + (size_t)(live ? token : 0) * P.q_stride + (size_t)qh * D + 8 * h;
-        const uint32_t sign = P.scale < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
         for (int s = 0; s < KS; ++s)
-            q[s] = *reinterpret_cast<const u32x4 *>(row + 16 * s) ^ sign;
+            q[s] = *reinterpret_cast<const u32x4 *>(row + 16 * s) ^ query_sign(P.scale);
     }
-    const float c = fmaxf(__builtin_fabsf(P.scale) * kLog2e, 0x1p-126f);
+    const float c = score_factor(P.scale), slack = uniform(kSlack / c);
     const int32_t *table = P.s.pages + (size_t)t.b * P.s.max_pages;
 
     float m, l, top;
@@ -400,15 +398,23 @@ __global__ void __launch_bounds__(kWaves *kWave, D == 64 && !C8 ? 3 : D <= 128 ?
             s[i / 16][i % 16] = sees(g, i) ? s[i / 16][i % 16] : -INFINITY;
         top = top_of(s);
     };
-    // The sums are taken to a new maximum only when it is 2^8 times the old one's:
-    // probabilities up to 2^8 are as exact, and the sums have room.
-    float zero;
-    auto rescale = [&]() __attribute__((always_inline)) {
-        top = both_halves_max(top) * c;
-        if (__any(top > m + kSlack)) {
+    // The sums are taken to a new maximum m only when a score passes `limit`, where its
+    // probability would be 2^8: up to there they are as exact, and the sums have room.  An
+    // exponent is then one operation, s c + zero with zero = -m c.  From |m c| = 2^20 on (far)
+    // the rounding of m c would be part of every exponent, up to any size: there m is taken
+    // from the scores before, and without slack.
+    float limit, zero;
+    bool far;
+    auto rescale = [&](float16v(&s)[2]) __attribute__((always_inline)) {
+        top = both_halves_max(top);
+        if (__any(top > limit)) {
             const float to = fmaxf(m, top);
-            const float f = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+            const float f = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m - to) * c);
             m = to;
+            const float mc = m == -INFINITY ? 0.0f : m * c;
+            far = __any(__builtin_fabsf(mc) >= kFar);
+            zero = far ? 0.0f : -mc;
+            limit = far || m == -INFINITY ? m : m + slack;
             l *= f;
 #pragma unroll
             for (int d = 0; d < DB; ++d)
@@ -416,7 +422,12 @@ __global__ void __launch_bounds__(kWaves *kWave, D == 64 && !C8 ? 3 : D <= 128 ?
                 for (int j = 0; j < 16; ++j)
                     o[d][j] *= f;
         }
-        zero = m == -INFINITY ? 0.0f : -m;
+        if (far) {
+            const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                s[i / 16][i % 16] -= base;
+        }
     };
     // Word i of the probabilities: scores 2 i and 2 i + 1; four words are an operand.  vq: an
     // 8-bit cache's scales, those of the words after the next ones asked for here.
@@ -489,7 +500,7 @@ __global__ void __launch_bounds__(kWaves *kWave, D == 64 && !C8 ? 3 : D <= 128 ?
         const char *const v = v_buf(st), *const k = k_buf(st + 1);
         if (!(whole_wave(st) && stage.here(st)))
             mask(sight_of(st), s);
-        rescale();
+        rescale(s);
         first_scales(v);
         // the first 12 words in the time of the next scores, the last 4 and the next maximum
         // in that of the second product (the next scores of the last step are of keys that
@@ -554,8 +565,9 @@ __global__ void __launch_bounds__(kWaves *kWave, D == 64 && !C8 ? 3 : D <= 128 ?
     };
 
     auto begin = [&]() __attribute__((always_inline)) {
-        m = -INFINITY;
-        l = 0.0f;
+        m = limit = -INFINITY;
+        l = zero = 0.0f;
+        far = false;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
             o[d] = float16v{};
@@ -630,7 +642,7 @@ __global__ void __launch_bounds__(kWaves *kWave, D == 64 && !C8 ? 3 : D <= 128 ?
             const Sight g = sight_of(st);
             all_scores();
             mask(g, sa);
-            rescale();
+            rescale(sa);
             first_scales(v);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
@@ -731,7 +743,7 @@ __global__ void __launch_bounds__(256) join_rows(const AttnParams P)
     float L = 0.0f, v[4] = {0.f, 0.f, 0.f, 0.f};
     for (int n = 0; n < t.parts; ++n) {
         const size_t slot = slot0 + n * step;
-        const float l = P.part_ml[2 * slot + 1], f = part_factor(P.part_ml[2 * slot], l, M);
+        const float l = P.part_ml[2 * slot + 1], f = part_factor(P.part_ml[2 * slot], l, M, score_factor(P.scale));
         const float4v o = *reinterpret_cast<const float4v *>(P.part_o + slot * D + 4 * c);
         if (l == 0.0f)  // the part saw nothing
             continue;

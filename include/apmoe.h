@@ -668,7 +668,8 @@ apmoe_status apmoe_attn_workspace(apmoe_ctx *ctx, const apmoe_kv_cache *cache, c
  *   out [T][q_heads * D] of dtype or NULL; out8 e4m3 [T][q_heads * D] and out_scale fp32
  *   [T][q_heads * D / 128] (the rows that apmoe_gemm_fp8 takes), both NULL or both set, with
  *   head_dim 128 or 256.  At least one of out, out8 (T > 0).
- * Scores, statistics and sums are fp32; the probabilities (with an APMOE_E4M3 cache, times
+ * Scores, statistics and sums are fp32: q.k has to stay within its range, scale times it need
+ * not; the probabilities (with an APMOE_E4M3 cache, times
  * the values' scales) go into the second product as two 16-bit numbers, to 2^-16 of each.
  * A row that sees nothing, or nothing but scores of -infinity, is zeros; one that sees a
  * score that is NaN is NaN.  What lies in the cache where a row sees nothing does not matter,

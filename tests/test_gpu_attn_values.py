@@ -1,4 +1,5 @@
-"""Attention over the paged cache at the ends of the types: scores that are NaN."""
+"""Attention over the paged cache at the ends of the types: scores that are NaN, scores at and
+past fp32's range."""
 import numpy as np
 import pytest
 import torch
@@ -86,3 +87,67 @@ def test_8_bit_rows_of_nan(fn):
         q[0, 128:] = float("nan")
         _, _, scale = attend(fn, bt, q, 2, out8=True)
         same(np.isnan(np64(scale)), np.array([[False, True], [False, False]]))
+
+
+# ------------------------------------------------------------------ large scores
+
+def fill_column(bt, rng, keys):
+    """Sequence b's key at position p is keys[b][p] in column 0 and zeros; values as always."""
+    for b, n in enumerate(bt.lens):
+        for p in range(int(n)):
+            row = np.zeros((bt.Hkv, bt.D))
+            row[:, 0] = keys[b][p]
+            pg, at = bt.table[b, p // bt.page], p % bt.page
+            bt.cache.put("k", pg, at, row)
+            bt.cache.put("v", pg, at, rng.standard_normal((bt.Hkv, bt.D)))
+
+
+def check_largest(fn, bt, q, Hq, scale):
+    """Rows against the mean of the values whose scores are the largest (the others' weights
+    are e^-200 and less of theirs), or of all values where the scores differ by less than
+    2^-18: equal weights are exact in any type, or off by 2^-18 each and in the sum.  So the
+    errors are those of the values' scales (an 8-bit cache: p_err of each), of fp32 sums, and
+    half a step."""
+    g = np64(attend(fn, bt, q, Hq, scale)[0]).reshape(bt.T, Hq, bt.D)
+    q = np64(q).reshape(bt.T, Hq, bt.D)
+    p_err = 2.0 ** -8 if bt.c8 and bt.t == "bf16" and fn is apw.attn_prefill else 2.0 ** -15
+    rows = [(bt.cache.rows("k", bt.table[b], int(n)), bt.cache.rows("v", bt.table[b], int(n)))
+            for b, n in enumerate(bt.lens)]
+    for row, b, pos in ref.tokens(bt.lens, bt.offsets, bt.T):
+        K, V = (x[:, :pos + 1] for x in rows[b])
+        for h in range(Hq):
+            s = K[h * bt.Hkv // Hq] @ q[row, h] * scale
+            off = s.max() - s
+            w = (off < 2.0 ** -18).astype(np.float64)
+            assert np.all((off > 200) | (w == 1))  # the case says what it says it does
+            v = V[h * bt.Hkv // Hq]
+            want, size = w @ v / w.sum(), w @ np.abs(v) / w.sum()
+            tol = (np.abs(want) + size * 2.0 ** -7) * ref.HALF_STEP[bt.t] + ref.SMALLEST[bt.t] + size * (
+                p_err + 2.0 ** -16 + (len(s) + 64) * 2.0 ** -23)
+            d = np.abs(g[row, h] - want)
+            assert np.all(d <= tol), (row, h, d.max(), g[row, h][:4], want[:4])
+
+
+@pytest.mark.parametrize("c8", [False, True])
+@pytest.mark.parametrize("t,top", [("f16", 60000.0), ("bf16", 2.0 ** 60)])
+@pytest.mark.parametrize("scale", [1.0, 1000.0, 2.0 ** 100, -1.0, -(2.0 ** 90), 0.0, 1e-42])
+@pytest.mark.parametrize("fn", BOTH)
+def test_the_largest_of_large_scores_has_the_weight(fn, scale, t, top, c8):
+    """Scores up to 2^32 (fp16) and 2^120 (bf16), whose product with the scale may pass fp32's
+    range: two largest ones, all of them the same, and all of them negative; rows of small
+    scores beside those of large ones; whole and in parts."""
+    rng = rng_of("large", scale, t, c8)
+    for lens, news in (([200, 45, 64], [70, 3, 64]), ([3000], [4])):
+        bt = Batch(rng, lens, None if fn is apw.attn_decode else news, 1, 64, 32, t, c8, filled=False)
+        q = torch.zeros((bt.T, 2 * 64), dtype=ref.TORCH[t])
+        q[:, 0], q[:, 64] = top, 1.0
+        mixed = [rng.choice([-top, 0.0, top / 2], n) for n in lens]
+        for x in mixed:
+            x[[3, -2]] = top
+            x[[0, 5]] = -1.5 * top if t == "bf16" else -65504.0
+        below = [np.full(n, -top) for n in lens]
+        for x in below:
+            x[[1, -1]] = -top / 2
+        for keys in (mixed, [np.full(n, -top) for n in lens], below):
+            fill_column(bt, rng, keys)
+            check_largest(fn, bt, q, 2, scale)
