@@ -106,6 +106,11 @@ __device__ inline float score_factor(float scale) { return uniform(fmaxf(__built
 
 __device__ inline uint32_t query_sign(float scale) { return scale < 0.0f ? 0x80008000u : 0u; }
 
+// Probabilities and their sum are 2^kTop times what they are by the formula: fp16 has numbers up
+// to 2^15 and none below 2^-25, so the largest probability goes there; bf16 has fp32's range.
+template <int DT>
+constexpr float kTop = DT == APMOE_F16 ? 15.0f : 0.0f;
+
 // Factor of a part with maximum m and sum l where the largest maximum is M.  m = -infinity with
 // l = 0 is a part that saw nothing (or scores of -infinity only): 0.  The maximum passes a NaN
 // by, the sum does not: m = -infinity with any other l is a part whose scores were NaN, and

@@ -18,7 +18,8 @@
 //
 // Probabilities are given to the second product as the sum of two 16-bit numbers: the
 // matrix units have room (16 columns are computed for a group of 1 to 16 heads), and the
-// output then has the error of its own rounding only.
+// output then has the error of its own rounding only.  In fp16 they are 2^15 times as large, so
+// what is left of one is 2^-40 of the largest.
 #include <algorithm>
 
 #include "attn.h"
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__(NW *kWave, D == 256 ? 1 : 2) decode_kernel(con
         float p[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            p[e] = __builtin_amdgcn_exp2f((x[e] - base) * c);
+            p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e] - base, c, kTop<T::kVT>));
             l += p[e];
         }
         if constexpr (C8)

@@ -59,6 +59,7 @@ struct Prefill {
     // fp16 queries on an 8-bit cache: probabilities times scales have bf16's range, and two
     // bf16 numbers keep what fp16 would
     static constexpr bool kTwo = C8 && QT == APMOE_F16;
+    static constexpr float kFirst = kTop<kVT> > 0.0f ? kTop<kVT> - kSlack : 0.0f;  // exponent of a maximum (attn.h)
     static constexpr int kBytes = kStep * D * 2;  // of a step's keys, and of its values
     static constexpr int kAhead = D == 64 || C8 ? 3 : 4;  // operands read ahead of their product (registers)
     static constexpr int kBuffer = kBytes + (C8 ? kStep * 4 : 0);  // with their scales
@@ -400,7 +401,7 @@ __global__ void __launch_bounds__(kWaves *kWave, D == 64 && !C8 ? 3 : D <= 128 ?
     };
     // The sums are taken to a new maximum m only when a score passes `limit`, where its
     // probability would be 2^8: up to there they are as exact, and the sums have room.  An
-    // exponent is then one operation, s c + zero with zero = -m c.  From |m c| = 2^20 on (far)
+    // exponent is then one operation, s c + zero with zero = kFirst - m c.  From |m c| = 2^20 on (far)
     // the rounding of m c would be part of every exponent, up to any size: there m is taken
     // from the scores before, and without slack.
     float limit, zero;
@@ -413,7 +414,7 @@ __global__ void __launch_bounds__(kWaves *kWave, D == 64 && !C8 ? 3 : D <= 128 ?
             m = to;
             const float mc = m == -INFINITY ? 0.0f : m * c;
             far = __any(__builtin_fabsf(mc) >= kFar);
-            zero = far ? 0.0f : -mc;
+            zero = far ? C::kFirst : C::kFirst - mc;
             limit = far || m == -INFINITY ? m : m + slack;
             l *= f;
 #pragma unroll
@@ -566,7 +567,8 @@ __global__ void __launch_bounds__(kWaves *kWave, D == 64 && !C8 ? 3 : D <= 128 ?
 
     auto begin = [&]() __attribute__((always_inline)) {
         m = limit = -INFINITY;
-        l = zero = 0.0f;
+        l = 0.0f;
+        zero = C::kFirst;
         far = false;
 #pragma unroll
         for (int d = 0; d < DB; ++d)

@@ -669,8 +669,9 @@ apmoe_status apmoe_attn_workspace(apmoe_ctx *ctx, const apmoe_kv_cache *cache, c
  *   [T][q_heads * D / 128] (the rows that apmoe_gemm_fp8 takes), both NULL or both set, with
  *   head_dim 128 or 256.  At least one of out, out8 (T > 0).
  * Scores, statistics and sums are fp32: q.k has to stay within its range, scale times it need
- * not; the probabilities (with an APMOE_E4M3 cache, times
- * the values' scales) go into the second product as two 16-bit numbers, to 2^-16 of each.
+ * not.  The probabilities (with an APMOE_E4M3 cache, times the values' scales) go into the
+ * second product as two 16-bit numbers of the cache's type (bf16 with an APMOE_E4M3 cache), to
+ * 2^-16 of each; in fp16 also to 2^-40 of the row's largest one.
  * A row that sees nothing, or nothing but scores of -infinity, is zeros; one that sees a
  * score that is NaN is NaN.  What lies in the cache where a row sees nothing does not matter,
  * NaN and infinities included.
@@ -693,8 +694,8 @@ apmoe_status apmoe_attn_decode(apmoe_ctx *ctx, const apmoe_kv_cache *cache, cons
  * for every row, p being the row's position, so a row sees the cached tokens, the rows
  * before it and itself.  All rows' keys and values have been appended before.
  * The probabilities go into the second product rounded to one 16-bit number of the cache's
- * type (bf16 with an APMOE_E4M3 cache; with fp16 queries on such a cache as two): 2^-8 or
- * 2^-11 of each.  Rows with a negative position (more rows than lens[b]) are zeros.
+ * type (bf16 with an APMOE_E4M3 cache; with fp16 queries on such a cache as two): 2^-8 (bf16)
+ * or 2^-11 of each; in fp16 also to 2^-32 of the row's largest one.  Rows with a negative position (more rows than lens[b]) are zeros.
  * Arguments, limits and errors as apmoe_attn_decode, with or without q_offsets.
  */
 apmoe_status apmoe_attn_prefill(apmoe_ctx *ctx, const apmoe_kv_cache *cache, const apmoe_kv_batch *batch,

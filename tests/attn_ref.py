@@ -120,7 +120,7 @@ def append(cache: Cache, table, lens, offsets, q, k, v, rope, rot, interleaved, 
         cache.put("v", p, pos % cache.page, v[row].astype(np.float64))
 
 
-def attention(cache: Cache, table, lens, offsets, q, scale, window, sinks, limit, p_err, out_t):
+def attention(cache: Cache, table, lens, offsets, q, scale, window, sinks, limit, p_err, out_t, floor=2.0 ** -24):
     """(out [T][Hq][D], bound of the error, rows that belong to a sequence), for q values
     [T][Hq][D].
 
@@ -130,7 +130,7 @@ def attention(cache: Cache, table, lens, offsets, q, scale, window, sinks, limit
     probabilities of at most d = 2 x that.  They are normalised by their own sum, so the
     output is off by 2 d sum p |v|; their rounding for the second product p_err, and its
     fp32 sum (also over parts and waves) (n + 64) 2^-23 of sum p |v|.  Probabilities below
-    fp16's normal range are off by 2^-24 of the largest.  Then half a step of the type."""
+    fp16's normal range are off by `floor` of the largest.  Then half a step of the type."""
     T, Hq, D = q.shape
     G = Hq // cache.heads
     out, bound = np.zeros((T, Hq, D)), np.zeros((T, Hq, D))
@@ -163,5 +163,5 @@ def attention(cache: Cache, table, lens, offsets, q, scale, window, sinks, limit
                 d = 2 * ((D + 4) * 2.0 ** -23 * mag.max() + 2.0 ** -21)
                 size = p @ np.abs(v) / L
                 bound[row, h] = (np.abs(o) + size * 2 * d) * HALF_STEP[out_t] + SMALLEST[out_t] + size * (
-                    2 * d + p_err + (m.sum() + 64) * 2.0 ** -23) + np.abs(v).sum(axis=0) * 2.0 ** -24 / L
+                    2 * d + p_err + (m.sum() + 64) * 2.0 ** -23) + np.abs(v).sum(axis=0) * floor / L
     return out, bound, live

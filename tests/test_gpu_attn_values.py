@@ -1,5 +1,5 @@
 """Attention over the paged cache at the ends of the types: scores that are NaN, scores at and
-past fp32's range."""
+past fp32's range, many small probabilities."""
 import numpy as np
 import pytest
 import torch
@@ -151,3 +151,44 @@ def test_the_largest_of_large_scores_has_the_weight(fn, scale, t, top, c8):
         for keys in (mixed, [np.full(n, -top) for n in lens], below):
             fill_column(bt, rng, keys)
             check_largest(fn, bt, q, 2, scale)
+
+
+# ------------------------------------------------------------------ small probabilities
+
+def first_token_case(n, t, gap, news, rng, D=64):
+    """One token a third of the way with exp(gap) times the weight of each of the others."""
+    bt = Batch(rng, [n], news, 1, D, 256, t, False, filled=False)
+    idx = {x: ref.place(x, 256, D, 2) for x in "kv"}
+    keys = np.zeros((n, D))
+    keys[n // 3, 0] = gap
+    values = 1.0 + rng.standard_normal((n, D)) * 0.1
+    values[n // 3] = 0.0
+    for x, rows in (("k", ref.round16(keys, t)), ("v", ref.round16(values, t))):
+        for i in range(-(-n // 256)):
+            part = rows[i * 256:(i + 1) * 256]
+            bt.cache.data[x][bt.table[0, i], 0, idx[x][:len(part)].ravel()] = part.ravel()
+    q = torch.zeros((bt.T, D), dtype=ref.TORCH[t])
+    q[:, 0] = 1.0
+    return bt, q
+
+
+@pytest.mark.parametrize("gap", [14.3, 16.25, 17.3, 18.0, 20.0])
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("n,fn,news", [(20000, apw.attn_decode, None), (20000, apw.attn_prefill, [2]), (700, apw.attn_decode, None),
+                                       (700, apw.attn_prefill, [700]), (131072, apw.attn_decode, None)])
+def test_many_small_probabilities_beside_a_large_one(n, fn, news, t, gap):
+    """Probabilities of 2^-20 to 2^-29 of the largest, whose token's value is zero: the output is theirs alone.
+
+    As the sum of two 16-bit numbers of probabilities up to 2^15 they are off by half of
+    fp16's smallest number, 2^-25 of 2^15; prefill's, up to 2^7 and one number, by 2^-32 of the
+    largest beside their rounding."""
+    rng = rng_of("small", n, t, gap)
+    bt, q = first_token_case(n, t, gap, news, rng)
+    decode = fn is apw.attn_decode
+    p_err = 2.0 ** -15 if decode else ref.HALF_STEP[t]
+    floor = 0.0 if t == "bf16" else 2.0 ** -40 if decode else 2.0 ** -32
+    got = np64(attend(fn, bt, q, 1, 1.0)[0]).reshape(bt.T, 1, 64)
+    want, bound, _ = ref.attention(bt.cache, bt.table, bt.lens, bt.offsets, np64(q).reshape(bt.T, 1, 64), 1.0, 0, 0, 1 << 30,
+                                   p_err, t, floor)
+    off = np.abs(got - want)
+    assert np.all(off <= bound), (off.max(), want.ravel()[-4:], got.ravel()[-4:], bound.ravel()[-4:])
