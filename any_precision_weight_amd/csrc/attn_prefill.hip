@@ -38,7 +38,7 @@ static_assert(kRows == kPartRows, "rows of a part");
 constexpr int kStep = 64;           // cached tokens of a step
 constexpr uint32_t kGridX = 1u << 22;
 constexpr float kSlack = 8.0f;
-constexpr float kFar = 0x1p20f;
+constexpr float kFar = 0x1p10f;
 // Calls of few row tiles are split over the steps: up to kSplitBlocks workgroups (of 256 CUs
 // that hold two) into parts of kPartSteps steps or more.  512 new tokens behind 32256, 32 heads
 // over 8: 796 -> 301 us, 4 of each of 16 sequences of 2700 to 8000 252 -> 93, 64 behind 4000
@@ -401,9 +401,10 @@ __global__ void __launch_bounds__(kWaves *kWave, D == 64 && !C8 ? 3 : D <= 128 ?
     };
     // The sums are taken to a new maximum m only when a score passes `limit`, where its
     // probability would be 2^8: up to there they are as exact, and the sums have room.  An
-    // exponent is then one operation, s c + zero with zero = kFirst - m c.  From |m c| = 2^20 on (far)
-    // the rounding of m c would be part of every exponent, up to any size: there m is taken
-    // from the scores before, and without slack.
+    // exponent is then one operation, s c + zero with zero = kFirst - m c.  The rounding of m c is
+    // part of it, and another one after each new maximum: 2^-15 at most below |m c| = 2^10, a
+    // 16th of what the probabilities are rounded by.  From there on (far; weights of e^710 and
+    // more) m is taken from the scores before, and without slack.
     float limit, zero;
     bool far;
     auto rescale = [&](float16v(&s)[2]) __attribute__((always_inline)) {

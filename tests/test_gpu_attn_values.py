@@ -192,3 +192,33 @@ def test_many_small_probabilities_beside_a_large_one(n, fn, news, t, gap):
                                    p_err, t, floor)
     off = np.abs(got - want)
     assert np.all(off <= bound), (off.max(), want.ravel()[-4:], got.ravel()[-4:], bound.ravel()[-4:])
+
+
+@pytest.mark.parametrize("top", [256.0, 704.0])
+@pytest.mark.parametrize("fn,lens,news", [(apw.attn_decode, [600, 90], None), (apw.attn_prefill, [600, 90], [600, 90]),
+                                          (apw.attn_decode, [4000], None), (apw.attn_prefill, [4000], [3])])
+def test_small_differences_of_large_scores(fn, lens, news, top):
+    """Scores of 2^16 and 2^19, exact as fp32 sums of two products, that rise by 20 along the
+    sequence: the differences count, so the maximum's own rounding must not.  Beside the
+    probabilities' rounding each may be off by 2^-13 (an exponent's rounding below 2^10)."""
+    rng = rng_of("differences", lens, top)
+    bt = Batch(rng, lens, news, 1, 64, 32, "f16", False, filled=False)
+    for b, n in enumerate(lens):
+        for p in range(n):
+            row = np.zeros((1, 64))
+            row[0, 0], row[0, 1] = top, np.rint(p * 160 / n) / 8
+            bt.cache.put("k", bt.table[b, p // 32], p % 32, row)
+            bt.cache.put("v", bt.table[b, p // 32], p % 32, rng.standard_normal((1, 64)) + p / n)
+    q = torch.zeros((bt.T, 64), dtype=torch.float16)
+    q[:, 0], q[:, 1] = top, 1.0
+    g = np64(attend(fn, bt, q, 1, 1.0)[0])
+    p_err = 2.0 ** -15 if fn is apw.attn_decode else 2.0 ** -11
+    for row, b, pos in ref.tokens(bt.lens, bt.offsets, bt.T):
+        K, V = (bt.cache.rows(x, bt.table[b], pos + 1)[0] for x in "kv")
+        s = K[:, 0] * top + K[:, 1]
+        assert np.all(s == s.astype(np.float32))
+        w = np.exp(s - s.max())
+        want, size = w @ V / w.sum(), w @ np.abs(V) / w.sum()
+        tol = (np.abs(want) + size * 2.0 ** -8) * 2.0 ** -11 + size * (p_err + 2.0 ** -13 + (pos + 65) * 2.0 ** -23)
+        d = np.abs(g[row] - want)
+        assert np.all(d <= tol), (row, (d / tol).max(), d.max())
