@@ -693,12 +693,12 @@ __global__ void __launch_bounds__(kWaves *kWave, D == 64 && !C8 ? 3 : D <= 128 ?
         }
         return;
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // nothing seen: zeros
+    const float inv = 1.0f / l;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-            o[d][j] *= inv;
+            o[d][j] = l == 0.0f ? 0.0f : o[d][j] * inv;  // nothing seen: zeros, whatever lies there
     const size_t row = (size_t)token * P.Hq + qh;
     constexpr int kGroups = D < kBlk ? 1 : D / kBlk, kBlocks = DB / kGroups;
 #pragma unroll

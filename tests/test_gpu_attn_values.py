@@ -222,3 +222,26 @@ def test_small_differences_of_large_scores(fn, lens, news, top):
         tol = (np.abs(want) + size * 2.0 ** -8) * 2.0 ** -11 + size * (p_err + 2.0 ** -13 + (pos + 65) * 2.0 ** -23)
         d = np.abs(g[row] - want)
         assert np.all(d <= tol), (row, (d / tol).max(), d.max())
+
+
+@pytest.mark.parametrize("fn,lens,news", [(apw.attn_decode, [300, 40], None), (apw.attn_prefill, [300, 40], [20, 40]),
+                                          (apw.attn_decode, [3000], None), (apw.attn_prefill, [3000], [3])])
+@pytest.mark.parametrize("value", [1.0, float("inf"), float("nan")])
+def test_nothing_but_scores_of_minus_infinity_is_zeros_whatever_the_values_are(fn, lens, news, value):
+    """Head 0's scores are all -infinity; head 1's query is turned, and sees +infinity only."""
+    rng = rng_of("minus values", value)
+    for t in ("f16", "bf16"):
+        bt = Batch(rng, lens, news, 1, 64, 32, t, False, filled=False)
+        for b, n in enumerate(lens):
+            for p in range(n):
+                row = np.zeros((1, 64))
+                row[0, 0] = -np.inf
+                bt.cache.put("k", bt.table[b, p // 32], p % 32, row)
+                row = rng.standard_normal((1, 64))
+                row[0, p % 64] = value
+                bt.cache.put("v", bt.table[b, p // 32], p % 32, row)
+        q = torch.zeros((bt.T, 128), dtype=ref.TORCH[t])
+        q[:, 0], q[:, 64] = 1.0, -1.0
+        g = np64(attend(fn, bt, q, 2)[0])
+        assert np.all(g[:, :64] == 0), np.argwhere(g[:, :64] != 0)[:4]
+        assert np.isnan(g[:, 64:]).all()
