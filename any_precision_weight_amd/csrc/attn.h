@@ -106,10 +106,12 @@ __device__ inline float score_factor(float scale) { return uniform(fmaxf(__built
 
 __device__ inline uint32_t query_sign(float scale) { return scale < 0.0f ? 0x80008000u : 0u; }
 
-// Probabilities and their sum are 2^kTop times what they are by the formula: fp16 has numbers up
-// to 2^15 and none below 2^-25, so the largest probability goes there; bf16 has fp32's range.
+// Probabilities and their sum are 2^kTop times what they are by the formula.  fp16 has numbers up
+// to 2^15 and none below 2^-25, so the largest probability goes there.  bf16 has fp32's range, and
+// its values too: with 2^-30 the sum over 2^30 tokens is at most 1, and no sum of probabilities
+// times values is larger than the largest value.
 template <int DT>
-constexpr float kTop = DT == APMOE_F16 ? 15.0f : 0.0f;
+constexpr float kTop = DT == APMOE_F16 ? 15.0f : -30.0f;
 
 // Factor of a part with maximum m and sum l where the largest maximum is M.  m = -infinity with
 // l = 0 is a part that saw nothing (or scores of -infinity only): 0.  The maximum passes a NaN

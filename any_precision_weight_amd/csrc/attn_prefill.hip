@@ -59,7 +59,7 @@ struct Prefill {
     // fp16 queries on an 8-bit cache: probabilities times scales have bf16's range, and two
     // bf16 numbers keep what fp16 would
     static constexpr bool kTwo = C8 && QT == APMOE_F16;
-    static constexpr float kFirst = kTop<kVT> > 0.0f ? kTop<kVT> - kSlack : 0.0f;  // exponent of a maximum (attn.h)
+    static constexpr float kFirst = kTop<kVT> - kSlack;  // exponent of a maximum (attn.h)
     static constexpr int kBytes = kStep * D * 2;  // of a step's keys, and of its values
     static constexpr int kAhead = D == 64 || C8 ? 3 : 4;  // operands read ahead of their product (registers)
     static constexpr int kBuffer = kBytes + (C8 ? kStep * 4 : 0);  // with their scales

@@ -1,5 +1,5 @@
 """Attention over the paged cache at the ends of the types: scores that are NaN, scores at and
-past fp32's range, many small probabilities."""
+past fp32's range, many small probabilities, large and small values."""
 import numpy as np
 import pytest
 import torch
@@ -245,3 +245,41 @@ def test_nothing_but_scores_of_minus_infinity_is_zeros_whatever_the_values_are(f
         g = np64(attend(fn, bt, q, 2)[0])
         assert np.all(g[:, :64] == 0), np.argwhere(g[:, :64] != 0)[:4]
         assert np.isnan(g[:, 64:]).all()
+
+
+# ------------------------------------------------------------------ large values
+
+@pytest.mark.parametrize("fn,lens,news", [(apw.attn_decode, [300, 40], None), (apw.attn_prefill, [300, 40], [200, 40]),
+                                          (apw.attn_decode, [3000], None), (apw.attn_prefill, [3000], [3])])
+@pytest.mark.parametrize("c8", [False, True])
+def test_the_largest_bf16_values(fn, lens, news, c8):
+    """Sums of many of them, in decode of 16-bit rows the largest there are: their mean is a number.
+    (Prefill's probabilities and those times an 8-bit row's scale are off by 2^-8 each, and so a mean of the
+    type's largest may come out as its infinity: half of it there.)"""
+    rng = rng_of("values", lens, c8)
+    top = 2.0 ** 126 if c8 else 2.0 ** 128 - 2.0 ** 120 if fn is apw.attn_decode else 2.0 ** 127
+    bt = Batch(rng, lens, news, 1, 128, 32, "bf16", c8, filled=False)
+    for b, n in enumerate(lens):
+        for p in range(n):
+            row = 0.3 * p / n * rng.standard_normal((1, 128))
+            bt.cache.put("k", bt.table[b, p // 32], p % 32, row)
+            row = np.full((1, 128), top)
+            row[0, 1], row[0, 2:] = -top, top * rng.choice([1.0, -1.0, 0.5], 126)
+            bt.cache.put("v", bt.table[b, p // 32], p % 32, row)
+    q = queries(rng, bt.T, 2, 128, "bf16", 3.0)
+    g = np64(check(fn, bt, q, 2)).reshape(bt.T, 2, 128)
+    assert np.all(np.abs(g[:, :, 0] - top) <= top * 2.0 ** -6)
+
+
+@pytest.mark.parametrize("fn,lens,news", [(apw.attn_decode, [300, 40], None), (apw.attn_prefill, [300, 40], [200, 40]),
+                                          (apw.attn_decode, [3000], None), (apw.attn_prefill, [3000], [3])])
+@pytest.mark.parametrize("c8", [False, True])
+def test_small_bf16_values(fn, lens, news, c8):
+    """2^-64 and less, with weights down to 2^-20: their products are numbers too."""
+    rng = rng_of("small values", lens, c8)
+    bt = Batch(rng, lens, news, 1, 128, 32, "bf16", c8, filled=False)
+    for b, n in enumerate(lens):
+        for p in range(n):
+            bt.cache.put("k", bt.table[b, p // 32], p % 32, 0.3 * rng.standard_normal((1, 128)))
+            bt.cache.put("v", bt.table[b, p // 32], p % 32, rng.standard_normal((1, 128)) * 2.0 ** -64)
+    check(fn, bt, queries(rng, bt.T, 2, 128, "bf16", 3.0), 2)
