@@ -542,6 +542,13 @@ def moe_forward_fp8(ctx: Context, experts: Fp8Experts, x, x8, x_scale, w_router,
 
 # --------------------------------------------------------------------------- paged key-value cache
 
+def _int32(**numbers) -> None:
+    """ctypes cuts a number to the C ABI's 32 bits, and another one would be taken."""
+    for name, n in numbers.items():
+        if not -0x80000000 <= n <= 0x7FFFFFFF:
+            raise ValueError(f"{name}={n} does not fit into 32 bits")
+
+
 class KvCache:
     """A pool of pages of the key-value cache: k and v of n_pages * kv_heads * page *
     head_dim elements (any shape that begins with n_pages), float16, bfloat16, or e4m3
@@ -555,6 +562,7 @@ class KvCache:
             raise ValueError(f"k: need float16, bfloat16 or e4m3, got {k.dtype}")
         if e4m3 and (k_scale is None or v_scale is None):
             raise ValueError("an e4m3 cache needs k_scale and v_scale")
+        _int32(n_pages=k.shape[0], page=page, kv_heads=kv_heads, head_dim=head_dim)
         self.n_pages, self.page, self.kv_heads, self.head_dim = k.shape[0], page, kv_heads, head_dim
         self.device = k.get_device()
         self.tensors = (k, v, k_scale, v_scale)
@@ -581,6 +589,7 @@ class KvBatch:
         _load_types()
         if pages.dim() != 2 or pages.shape[0] != lens.numel():
             raise ValueError(f"pages {tuple(pages.shape)} and lens {tuple(lens.shape)} are not [B][max_pages], [B]")
+        _int32(B=pages.shape[0], T=T, max_pages=pages.shape[1], max_len=max_len)
         self.B, self.T = pages.shape[0], T
         self.device = pages.get_device()
         self.tensors = (pages, lens, q_offsets)
@@ -628,6 +637,7 @@ def kv_append(ctx: Context, cache: KvCache, batch: KvBatch, q, k, v, q_heads: in
         if rope.dim() != 2 or rope.shape[1] != rot:
             raise ValueError(f"rope: need [positions][{rot}], got {tuple(rope.shape)}")
         n_pos = rope.shape[0]
+    _int32(q_heads=q_heads, n_pos=n_pos, rot=rot)
     st = ctx.L.apmoe_kv_append(ctx.handle, cache.ref, batch.ref, qp, qs, kp, ks, vp, vs, dt, q_heads,
                                _arg(ctx, rope, "rope", n_pos * rot, _f32), n_pos, rot, 1 if interleaved else 0,
                                _arg(ctx, q_out, "q_out", T * q_heads * D, types), _stream_of(ctx, stream))
@@ -636,6 +646,7 @@ def kv_append(ctx: Context, cache: KvCache, batch: KvBatch, q, k, v, q_heads: in
 
 
 def attn_workspace(ctx: Context, cache: KvCache, batch: KvBatch, q_heads: int) -> int:
+    _int32(q_heads=q_heads)
     n = ctypes.c_size_t()
     _check(ctx.L.apmoe_attn_workspace(ctx.handle, cache.ref, batch.ref, q_heads, ctypes.byref(n)),
            "apmoe_attn_workspace", ctx.L)
@@ -653,6 +664,7 @@ def _attn(fn: str, ctx, cache, batch, q, q_heads, scale, window, sinks, ws, out,
     if not hasattr(ws, "data_ptr"):
         raise ValueError(f"ws: need a byte tensor, got {type(ws)}")
     _kv_on(ctx, cache, batch)
+    _int32(q_heads=q_heads, window=window, sinks=sinks)
     dt, types = _types(q, "q")
     n = batch.T * q_heads * cache.head_dim
     qp, qs = _matrix(ctx, q, "q", batch.T, q_heads * cache.head_dim, types)
