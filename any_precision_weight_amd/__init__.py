@@ -542,10 +542,13 @@ def moe_forward_fp8(ctx: Context, experts: Fp8Experts, x, x8, x_scale, w_router,
 
 # --------------------------------------------------------------------------- paged key-value cache
 
+_MAX32 = 0x7FFFFFFF
+
+
 def _int32(**numbers) -> None:
     """ctypes cuts a number to the C ABI's 32 bits, and another one would be taken."""
     for name, n in numbers.items():
-        if not -0x80000000 <= n <= 0x7FFFFFFF:
+        if not -_MAX32 - 1 <= n <= _MAX32:
             raise ValueError(f"{name}={n} does not fit into 32 bits")
 
 
@@ -637,7 +640,8 @@ def kv_append(ctx: Context, cache: KvCache, batch: KvBatch, q, k, v, q_heads: in
         if rope.dim() != 2 or rope.shape[1] != rot:
             raise ValueError(f"rope: need [positions][{rot}], got {tuple(rope.shape)}")
         n_pos = rope.shape[0]
-    _int32(q_heads=q_heads, n_pos=n_pos, rot=rot)
+    if not (0 <= q_heads <= _MAX32 and 0 <= rot <= _MAX32 and n_pos <= _MAX32):
+        _int32(q_heads=q_heads, rot=rot, n_pos=n_pos)
     st = ctx.L.apmoe_kv_append(ctx.handle, cache.ref, batch.ref, qp, qs, kp, ks, vp, vs, dt, q_heads,
                                _arg(ctx, rope, "rope", n_pos * rot, _f32), n_pos, rot, 1 if interleaved else 0,
                                _arg(ctx, q_out, "q_out", T * q_heads * D, types), _stream_of(ctx, stream))
@@ -664,7 +668,8 @@ def _attn(fn: str, ctx, cache, batch, q, q_heads, scale, window, sinks, ws, out,
     if not hasattr(ws, "data_ptr"):
         raise ValueError(f"ws: need a byte tensor, got {type(ws)}")
     _kv_on(ctx, cache, batch)
-    _int32(q_heads=q_heads, window=window, sinks=sinks)
+    if not (0 <= window <= _MAX32 and 0 <= sinks <= _MAX32):
+        _int32(window=window, sinks=sinks)
     dt, types = _types(q, "q")
     n = batch.T * q_heads * cache.head_dim
     qp, qs = _matrix(ctx, q, "q", batch.T, q_heads * cache.head_dim, types)
