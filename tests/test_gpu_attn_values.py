@@ -283,3 +283,47 @@ def test_small_bf16_values(fn, lens, news, c8):
             bt.cache.put("k", bt.table[b, p // 32], p % 32, 0.3 * rng.standard_normal((1, 128)))
             bt.cache.put("v", bt.table[b, p // 32], p % 32, rng.standard_normal((1, 128)) * 2.0 ** -64)
     check(fn, bt, queries(rng, bt.T, 2, 128, "bf16", 3.0), 2)
+
+
+# ------------------------------------------------------------------ two walks over the same steps
+
+@pytest.mark.parametrize("c8", [False, True])
+@pytest.mark.parametrize("t,D,Hq,Hkv", [("f16", 64, 4, 2), ("bf16", 128, 8, 2), ("f16", 128, 6, 1), ("bf16", 256, 2, 2)])
+def test_prefill_step_by_step_gives_the_bits_of_the_pipeline(t, D, Hq, Hkv, c8):
+    """A value that is not finite where no row sees it (behind a sequence's end) makes a row
+    tile walk its steps one after the other, each staged, waited for and used by itself; with
+    zeros there the copies run two steps ahead of the products.  The operations are the same."""
+    rng = rng_of("walks", t, D, Hq, Hkv, c8)
+    lens, news = [1500, 333, 70, 41], [260, 333, 3, 41]
+    bt = Batch(rng, lens, news, Hkv, D, 64, t, c8)
+    q = queries(rng, bt.T, Hq, D, t, 2.0)
+    runs = []
+    for bad in (True, False):
+        if not bad:  # every page of the pool past the sequences' ends, and those of nobody
+            for x in "kv":
+                data, scale = bt.cache.data[x], bt.cache.scale[x]
+                if c8:
+                    data[data == 0x7F] = 0
+                    scale[np.isnan(scale)] = 0.0
+                else:
+                    data[np.isnan(data)] = 0.0
+        for window, sinks in ((0, 0), (300, 70)):
+            runs.append(check(apw.attn_prefill, bt, q, Hq, window=window, sinks=sinks))
+    for a, b in zip(runs[:2], runs[2:]):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+@pytest.mark.parametrize("c8", [False, True])
+def test_a_context_of_separate_launches_gives_the_same_bits(c8, monkeypatch):
+    monkeypatch.setenv("APMOE_UNFUSED", "1")
+    other = apw.Context(0)
+    monkeypatch.delenv("APMOE_UNFUSED")
+    rng = rng_of("separate", c8)
+    bt = Batch(rng, [1000, 77], [40, 77], 2, 128, 32, "bf16", c8)
+    q = queries(rng, bt.T, 8, 128, "bf16")
+    a, b = (attend(apw.attn_prefill, bt, q, 8, out8=True, c=c) for c in (ctx(), other))
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    bt.offsets, bt.T = None, 2
+    a, b = (attend(apw.attn_decode, bt, q[:2], 8, out8=True, c=c) for c in (ctx(), other))
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    other.close()
