@@ -327,3 +327,26 @@ def test_a_context_of_separate_launches_gives_the_same_bits(c8, monkeypatch):
     a, b = (attend(apw.attn_decode, bt, q[:2], 8, out8=True, c=c) for c in (ctx(), other))
     assert all(torch.equal(x, y) for x, y in zip(a, b))
     other.close()
+
+
+@pytest.mark.parametrize("fn", BOTH)
+def test_lengths_below_zero_are_empty(fn):
+    """Their rows are zeros and see nothing, with a window and without; nothing of them is stored."""
+    rng = rng_of("negative")
+    lens = [-1, -(1 << 31), 40, -5, -(1 << 31) + 3]
+    bt = Batch(rng, lens, None if fn is apw.attn_decode else [2, 1, 3, 70, 1], 2, 64, 32, "f16", False)
+    q = queries(rng, bt.T, 4, 64, "f16")
+    for window, sinks in ((0, 0), (7, 3), (1 << 30, (1 << 31) - 1)):
+        g = np64(check(fn, bt, q, 4, window=window, sinks=sinks))
+        empty = np.ones(bt.T, bool)
+        first = 2 if fn is apw.attn_decode else 3
+        empty[first:first + (1 if fn is apw.attn_decode else 3)] = False
+        assert np.all(g[empty] == 0) and np.any(g[~empty] != 0)
+    kv, batch = bt.upload()
+    before = [x.clone() for x in (bt.k, bt.v)]
+    x = queries(rng, bt.T, 2, 64, "f16").cuda()
+    apw.kv_append(ctx(), kv, batch, None, x, x, 0, None, 0, False, None)
+    torch.cuda.synchronize()
+    for a, b in zip(before, (bt.k, bt.v)):
+        other = [p for p in range(bt.cache.n_pages) if p not in bt.table[2]]
+        assert torch.equal(a[other].view(torch.int16), b[other].view(torch.int16))
