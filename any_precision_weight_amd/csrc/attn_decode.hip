@@ -16,10 +16,14 @@
 // operands of the products are whole lines of the cache); the next tile's keys are asked for
 // when this one's are used, its values likewise, so a wave always has 8 to 16 KB on the way.
 //
+// Every workgroup finds its sequence by a scan of the lengths, 64 a step, so a call's time has a
+// part that grows with the square of the batch: sequences of 200 tokens, 32 heads over 8, take 42 us
+// for 256 (5.0 TB/s), 190 for 1024 (4.5), 1177 for 4096 (2.9) and 11200 for 16384 (1.2).
+//
 // Probabilities are given to the second product as the sum of two 16-bit numbers: the
 // matrix units have room (16 columns are computed for a group of 1 to 16 heads), and the
 // output then has the error of its own rounding only.  In fp16 they are 2^15 times as large, so
-// what is left of one is 2^-40 of the largest.
+// what is lost of one is at most 2^-40 of the largest; in bf16 2^-30 times (kTop, attn.h).
 #include <algorithm>
 
 #include "attn.h"
@@ -43,7 +47,9 @@ constexpr int kCols = 16;  // query heads of one workgroup
 // 2048 with many workgroups (one of 601 8.4 us against 9.0, one of 1000 9.8 against 9.2; 32 of 512
 // to 1024 20 against 26, 128 of 167 to 500 30 against 37), or 4096 of an 8-bit cache with kMany
 // (as many bytes; 200 of 870 to 2600 123 us against 150; 160 of 30 to 3000 70 against 79; with 16
-// bits 200 of 870 to 2600 take 210 against 223, but 128 of 133 to 4000 122 against 110).  Then few
+// bits 200 of 870 to 2600 take 210 against 223, but 128 of 133 to 4000 122 against 110).  These look at
+// the bound of the lengths, which the host knows, and not at the lengths: one long sequence among
+// short ones is then walked by one workgroup a head (not measured).  Then few
 // have eight waves each (16 of 133 to 400 8.0 us against 9.4 with four), many four (128 of 167 to
 // 500 30 against 40).
 constexpr int kFew = 256, kMany = 1024;

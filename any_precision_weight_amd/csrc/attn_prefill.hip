@@ -10,17 +10,25 @@
 //
 // A step is the products of the next scores with this step's exponentials between them, then
 // the second products with the next maximum between them: a wave's vector instructions run in
-// its own matrix instructions' time (3.4 of them and one exponential beside each, where one of
-// two waves a SIMD has room for about 6), and two workgroups a CU cover each other's barriers.
+// its own matrix instructions' time (5 of them beside each with the exponential, by the
+// counters, where one of two waves a SIMD has room for about 6), and two workgroups a CU cover
+// each other's barriers.
 //
-// Bound by the matrix units at the clock that the power allows: 8192 tokens, 32 heads over 8 of
-// 128 in bf16 511 to 528 us, 1.04 to 1.08 PFLOP/s; 6000 tokens of each of three sequences behind
-// up to 14000, with a window, 3.1 to 3.3 ms, 1.04 to 1.09 (a large library product reaches 1.50
-// here).  The matrix units are busy for 59% of the SIMDs' cycles, at 1.6 GHz; before the
-// interleaving it was 47% at 2.0 GHz for 571 us.  Heads of 64 take 327 us for two prompts of 6000
-// (0.90), of 256 (one wave a SIMD) 528 us for two of 5000 of 16 heads (0.78); an 8-bit cache,
-// converted on its way into LDS, 680 us for the first (0.81).  64 rows a wave (half the reads
-// from LDS, one wave a SIMD) took 654 us for it.
+// 8192 tokens, 32 heads over 8 of 128 in bf16 take 511 to 535 us, 1.03 to 1.08 PFLOP/s; 6000 tokens
+// of each of three sequences behind up to 14000, with a window, 3.1 to 3.3 ms, 1.03 to 1.09 (a large
+// library product reaches 1.50 here).  In the counters' runs the matrix units are busy for 60 and
+// 62% of the CUs' cycles, at 1.55 and 1.7 GHz, and waves stand at a wait or a barrier for 30%
+// of theirs: neither the units alone nor the clock alone is the bound.  Before the softmax was
+// interleaved with the products it took 571 us.  Heads of 64 take 327 to 348 us for two prompts of
+// 6000 (0.85 to 0.90; a step's 32 exponentials a lane, at a quarter of the rate, take as long as
+// its 16 products), of 256 (one wave a SIMD) 528 to 549 us for two of 5000 of 16 heads (0.75 to
+// 0.78); an 8-bit cache, converted on its way into LDS for each row tile, 675 to 695 us for the
+// first (0.79 to 0.81), 68 bytes of scratch a lane, and with fp16 queries 950 (0.58), 116 bytes.  64
+// rows a wave (half the reads from LDS, one wave a SIMD) took 654 us for it.
+//
+// Probabilities go into the second product as one 16-bit number (2^-8 of each in bf16), where
+// decode gives two: a second number would be half as many matrix instructions again.  The
+// output's error against 64 bits in norm is 0.0018 for 8192 tokens; its own rounding alone is 0.0017.
 //
 // Rows of a key operand: row 16 t + 8 a + 4 h + b of a 32-token product is token 16 a + 8 t +
 // 4 h + b.  Lane half h then has, of scores 8t .. 8t+7, the tokens of granule g = 2 t + h of
@@ -42,8 +50,10 @@ constexpr float kFar = 0x1p10f;
 // Calls of few row tiles are split over the steps: up to kSplitBlocks workgroups (of 256 CUs
 // that hold two) into parts of kPartSteps steps or more.  512 new tokens behind 32256, 32 heads
 // over 8: 796 -> 301 us, 4 of each of 16 sequences of 2700 to 8000 252 -> 93, 64 behind 4000
-// 93 -> 29; of 4 steps 316, 96 and 33, of 16 287, 93 and 37.  Not with more workgroups: 1000
-// behind 1000, 256 of them, 44.5 us and split in two 51.
+// 93 -> 29; of 4 steps 316, 96 and 33, of 16 287, 93 and 37.  Not with more workgroups, by
+// one case of about 31 steps: 1000 behind 1000, 256 of them, 44.5 us and split in two 51.  Larger
+// calls of many steps have not been measured split; unsplit, 4 new tokens of each of 32 and 64
+// sequences of 2000 to 8000 take 210 and 269 us.
 constexpr int kPartSteps = 8;
 constexpr int kSplitBlocks = 192;
 constexpr int kMaxParts = 64;
@@ -403,8 +413,8 @@ __global__ void __launch_bounds__(kWaves *kWave, D == 64 && !C8 ? 3 : D <= 128 ?
     // probability would be 2^8: up to there they are as exact, and the sums have room.  An
     // exponent is then one operation, s c + zero with zero = kFirst - m c.  The rounding of m c is
     // part of it, and another one after each new maximum: 2^-15 at most below |m c| = 2^10, a
-    // 16th of what the probabilities are rounded by.  From there on (far; weights of e^710 and
-    // more) m is taken from the scores before, and without slack.
+    // 16th of what fp16 rounds the probabilities by.  From there on (far; weights of e^710 and
+    // more) m is taken from the scores before, and without slack: 3% of 8192 tokens' time.
     float limit, zero;
     bool far;
     auto rescale = [&](float16v(&s)[2]) __attribute__((always_inline)) {

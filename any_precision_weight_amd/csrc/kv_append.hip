@@ -223,7 +223,8 @@ __device__ inline void store_q(const AppendParams &P, uint32_t t, int h, const P
 }
 
 // Bound by the chain of its loads: 1 token of 32 + 16 heads of 128 2.6 us (one kernel launch
-// in a graph), 256 tokens of 16 + 8 heads of 256 5.3 us.
+// in a graph), 256 tokens of 16 + 8 heads of 256 5.3 us, of 32 + 16 heads of 128 5.6 and to e4m3 5.5
+// (one token 3.6).
 //
 // One row a sequence: a workgroup has some heads of a token, a thread a pair of chunks of a
 // query, a key or a value.  Values go to their granules, of 8 tokens each, element by element.
@@ -298,7 +299,8 @@ __global__ void __launch_bounds__(kThreads) append_token(const AppendParams P)
 // 18657 rows of 48 + 16 heads of 128 in fp16: 135 us, 4.6 TB/s of the 4.9 that a copy reaches
 // here; written token by token, 16 bytes and 2 bytes at a time, it was 324 us, for a cache line
 // of 8 tokens was put together from 8 workgroups on 8 XCDs.  4556 rows of 32 + 16 heads to
-// e4m3: 32 us, 3.3 TB/s.  Three waves a SIMD is what the fp64 pairs' registers leave room for.
+// e4m3: 32 us, 3.3 TB/s.  Three waves a SIMD is what the fp64 pairs' registers leave room for, and
+// not quite: fp16 rows take 12 to 20 bytes of scratch a lane, e4m3 ones 20 to 48.
 template <int DT, bool C8, int D>
 __global__ void __launch_bounds__(kThreads, 3) append_tile(const AppendParams P)
 {

@@ -652,7 +652,9 @@ apmoe_status apmoe_kv_append(apmoe_ctx *ctx, const apmoe_kv_cache *cache, const 
                              int32_t n_pos, int32_t rot, int32_t interleaved, uint16_t *q_out, void *stream);
 
 /* Device workspace bytes of either attention for this batch or a smaller one (fewer
- * sequences, rows or tokens) on this cache.  Host only; pointers are not looked at. */
+ * sequences, rows or tokens) on this cache: room for the parts of what may be split, at
+ * least 65536 rows of head_dim + 2 fp32 numbers (34 MB with head_dim 128), whether a call
+ * splits anything or not.  Host only; pointers are not looked at. */
 apmoe_status apmoe_attn_workspace(apmoe_ctx *ctx, const apmoe_kv_cache *cache, const apmoe_kv_batch *batch,
                                   int32_t q_heads, size_t *bytes);
 
@@ -680,7 +682,9 @@ apmoe_status apmoe_attn_workspace(apmoe_ctx *ctx, const apmoe_kv_cache *cache, c
  * split over workgroups and joined in a second launch, in an order that depends on the
  * batch's sizes and lengths only: repeated calls give identical bits.
  * Limits: 1 <= q_heads <= 1024, a multiple of kv_heads; |scale| <= 2^100; 0 <= window <= 2^30,
- * 0 <= sinks; q_stride a multiple of 8, at least q_heads * D.  The call enqueues only kernel
+ * 0 <= sinks; q_stride a multiple of 8, at least q_heads * D.  Every workgroup scans the
+ * sequences' lengths: up to about 1000 sequences that costs little, above it the time grows
+ * with their square (several calls of fewer sequences do the same).  The call enqueues only kernel
  * launches on `stream` and can be captured.  Errors as apmoe_kv_append (out_scale 4 bytes),
  * UNSUPPORTED also for out8 with head_dim 64.
  */
